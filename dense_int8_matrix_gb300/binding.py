@@ -33,6 +33,18 @@ GEMM_KERNEL_REQUANT = 3
 GEMM_KERNEL_KINDS = 4
 GEMM_OUT_BF16 = 1
 GEMM_OUT_I8 = 2
+GEMM_OUT_F32 = 3
+GEMM_DTYPE_F32 = 2
+GEMM_F8_E4M3 = 0
+GEMM_F8_E5M2 = 1
+GEMM_SCALE_ROWS = 0
+GEMM_SCALE_BLOCKS = 1
+GEMM_GROUP_NONE = 0
+GEMM_GROUP_ROWS = 1
+GEMM_GROUP_K = 2
+GEMM_PLAN_F8_VERSION = 1
+GEMM_F8_MAX_GROUPS = 1024
+GEMM_NORM_MAX_D = 32768
 GEMM_PLAN_VERSION = 2
 GEMM_I8_MAX_K = 131071
 GEMM_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -43,6 +55,9 @@ EXPORTED = (
     "gemm_i8_run_host", "gemm_bf16_run_host", "gemm_device_error", "gemm_trace_begin",
     "gemm_trace_collect", "gemm_tc_kernel_info", "gemm_selftest_wait_timeout", "gemm_status_string",
     "gemm_i8_run_noalloc", "gemm_pool_usage", "gemm_i8_run_requant",
+    "gemm_f8_plan", "gemm_f8_grouped_plan", "gemm_f8_plan_for_sms", "gemm_f8_run", "gemm_f8_grouped_run",
+    "gemm_f8_quantize", "gemm_f8_quantize_cols", "gemm_f8_padded_k", "gemm_norm_f8", "gemm_norm_i8",
+    "gemm_norm_backward",
 )
 
 
@@ -58,6 +73,22 @@ class gemm_plan(ctypes.Structure):
         ("ratio", ctypes.c_double), ("workspace_bytes", ctypes.c_int64),
         ("split_from", ctypes.c_int32), ("a_on_chip", ctypes.c_int32),
         ("reserved", ctypes.c_int64 * 3),
+    ]
+
+    def as_dict(self):
+        return {name: getattr(self, name) for name, _ in self._fields_
+                if not name.startswith("reserved")}
+
+
+class gemm_plan_f8(ctypes.Structure):
+    _fields_ = [
+        ("version", ctypes.c_int32), ("path", ctypes.c_int32), ("num_sms", ctypes.c_int32),
+        ("group_mode", ctypes.c_int32),
+        ("m", ctypes.c_int64), ("k", ctypes.c_int64), ("n", ctypes.c_int64),
+        ("groups", ctypes.c_int32), ("a_type", ctypes.c_int32), ("b_type", ctypes.c_int32),
+        ("b_scale", ctypes.c_int32), ("bm", ctypes.c_int32), ("bn", ctypes.c_int32),
+        ("split_k", ctypes.c_int32), ("reserved32", ctypes.c_int32),
+        ("reserved", ctypes.c_int64 * 4),
     ]
 
     def as_dict(self):
@@ -96,7 +127,8 @@ def load():
                            "the GEMM has no CPU fallback" % path)
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER(gemm_plan)
-    i64, i32, vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
+    P8 = ctypes.POINTER(gemm_plan_f8)
+    i64, i32, vp, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
     sig = {
         "gemm_i8_plan": [i64, i64, i64, P],
         "gemm_bf16_plan": [i64, i64, i64, P],
@@ -113,11 +145,23 @@ def load():
         "gemm_i8_run_noalloc": [P, vp, vp, vp, vp],
         "gemm_pool_usage": [ctypes.POINTER(i64), ctypes.POINTER(i64), i32],
         "gemm_i8_run_requant": [P, vp, vp, vp, vp, i32, vp, vp],
+        "gemm_f8_plan": [i64, i64, i64, i32, i32, i32, P8],
+        "gemm_f8_grouped_plan": [i32, i32, i64, i64, i64, i32, i32, i32, P8],
+        "gemm_f8_plan_for_sms": [i32, i32, i64, i64, i64, i32, i32, i32, i32, P8],
+        "gemm_f8_run": [P8, vp, i64, vp, vp, i64, vp, i32, vp, i64, vp],
+        "gemm_f8_grouped_run": [P8, vp, i64, vp, vp, i64, vp, vp, i32, vp, i64, vp],
+        "gemm_f8_quantize": [vp, i32, i64, i64, i64, i32, i32, vp, i64, vp, vp],
+        "gemm_f8_quantize_cols": [vp, i32, i64, i64, i64, i32, vp, i32, vp, i64, vp, vp],
+        "gemm_norm_f8": [vp, i64, vp, i64, vp, f32, i32, i64, i64, vp, i64, vp, vp, i64, vp, vp],
+        "gemm_norm_i8": [vp, i64, vp, i64, vp, f32, i32, i64, i64, vp, i64, vp, vp, i64, vp, vp],
+        "gemm_norm_backward": [vp, i64, vp, i64, vp, vp, vp, i64, i32, i64, i64, vp, i64, vp, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = ctypes.c_int
+    lib.gemm_f8_padded_k.argtypes = [i64, i32]
+    lib.gemm_f8_padded_k.restype = i64
     lib.gemm_status_string.argtypes = [ctypes.c_int]
     lib.gemm_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -285,6 +329,198 @@ def gemm_tc_kernel_info(bm: int, bn: int, dtype: int):
 
 def gemm_selftest_wait_timeout(timeout_us: int, stream=None) -> None:
     _check(load().gemm_selftest_wait_timeout(timeout_us, _stream(stream)), "gemm_selftest_wait_timeout")
+
+
+# ------------------------------------------------------- 8-bit operators --
+
+def gemm_f8_plan(m: int, k: int, n: int, a_type: int = GEMM_F8_E4M3, b_type: int = GEMM_F8_E4M3,
+                 b_scale: int = GEMM_SCALE_BLOCKS) -> gemm_plan_f8:
+    p = gemm_plan_f8()
+    _check(load().gemm_f8_plan(m, k, n, a_type, b_type, b_scale, ctypes.byref(p)), "gemm_f8_plan")
+    return p
+
+
+def gemm_f8_grouped_plan(group_mode: int, groups: int, m: int, k: int, n: int, a_type: int = GEMM_F8_E4M3,
+                         b_type: int = GEMM_F8_E4M3, b_scale: int = GEMM_SCALE_BLOCKS) -> gemm_plan_f8:
+    p = gemm_plan_f8()
+    _check(load().gemm_f8_grouped_plan(group_mode, groups, m, k, n, a_type, b_type, b_scale, ctypes.byref(p)),
+           "gemm_f8_grouped_plan")
+    return p
+
+
+def gemm_f8_plan_for_sms(group_mode: int, groups: int, m: int, k: int, n: int, num_sms: int,
+                         a_type: int = GEMM_F8_E4M3, b_type: int = GEMM_F8_E4M3,
+                         b_scale: int = GEMM_SCALE_BLOCKS) -> gemm_plan_f8:
+    p = gemm_plan_f8()
+    _check(load().gemm_f8_plan_for_sms(group_mode, groups, m, k, n, a_type, b_type, b_scale, num_sms,
+                                       ctypes.byref(p)), "gemm_f8_plan_for_sms")
+    return p
+
+
+def gemm_f8_padded_k(rows: int, groups: int = 1) -> int:
+    return load().gemm_f8_padded_k(rows, groups)
+
+
+def _f8_dtype(f8_type):
+    import torch
+    return torch.float8_e4m3fn if f8_type == GEMM_F8_E4M3 else torch.float8_e5m2
+
+
+def _f8_type(q):
+    import torch
+    if q.dtype == torch.float8_e4m3fn:
+        return GEMM_F8_E4M3
+    if q.dtype == torch.float8_e5m2:
+        return GEMM_F8_E5M2
+    raise TypeError("expected torch.float8_e4m3fn or torch.float8_e5m2, got %s" % q.dtype)
+
+
+def _real_type(x):
+    import torch
+    if x.dtype == torch.bfloat16:
+        return GEMM_DTYPE_BF16
+    if x.dtype == torch.float32:
+        return GEMM_DTYPE_F32
+    raise TypeError("expected torch.bfloat16 or torch.float32, got %s" % x.dtype)
+
+
+def _matrix(x, dtype, shape):
+    """(address, row pitch) of a CUDA tensor whose rows are contiguous; the
+    leading dimensions before the last two lie one after the other."""
+    if x.dtype != dtype:
+        raise TypeError("expected %s, got %s" % (dtype, x.dtype))
+    if x.shape != shape:
+        raise ValueError("expected shape %s, got %s" % (tuple(shape), tuple(x.shape)))
+    if not x.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    stride = x.stride()
+    groups = shape[0] if len(shape) == 3 else 1
+    if shape[-2] > 1:
+        pitch = stride[-2]
+    elif groups > 1:
+        pitch = stride[0]
+    else:   # one row: any pitch will do
+        pitch = (shape[-1] + 15) // 16 * 16
+    if (shape[-1] > 1 and stride[-1] != 1) or pitch < shape[-1]:
+        raise ValueError("rows must be contiguous and must not overlap")
+    if groups > 1 and stride[0] != pitch * shape[1]:
+        raise ValueError("groups must lie one after the other")
+    return x.data_ptr(), pitch
+
+
+def _f8_run(plan, A, a_scale, Bt, b_scale, offsets, D, stream):
+    import torch
+    m, k, n, g = plan.m, plan.k, plan.n, plan.groups
+    kb = (k + 127) // 128
+    f32 = torch.float32
+    a, lda = _matrix(A, _f8_dtype(plan.a_type), (m, k))
+    rows = plan.group_mode == GEMM_GROUP_ROWS
+    b, ldb = _matrix(Bt, _f8_dtype(plan.b_type), (g, n, k) if rows else (n, k))
+    if plan.b_scale == GEMM_SCALE_BLOCKS:
+        sb = _addr(b_scale, f32, (g, (n + 127) // 128, kb) if rows else ((n + 127) // 128, kb))
+    else:
+        sb = _addr(b_scale, f32, (kb, g * n) if rows else (kb, n))
+    sa = _addr(a_scale, f32, (kb, m))
+    if D.dtype != f32 and D.dtype != torch.bfloat16:
+        raise TypeError("expected a torch.bfloat16 or torch.float32 output, got %s" % D.dtype)
+    d, ldd = _matrix(D, D.dtype, (g, m, n) if plan.group_mode == GEMM_GROUP_K else (m, n))
+    out = GEMM_OUT_F32 if D.dtype == f32 else GEMM_OUT_BF16
+    if offsets is None:
+        return load().gemm_f8_run(ctypes.byref(plan), a, lda, sa, b, ldb, sb, out, d, ldd, _stream(stream))
+    off = _addr(offsets, torch.int32, (g + 1,))
+    return load().gemm_f8_grouped_run(ctypes.byref(plan), a, lda, sa, b, ldb, sb, off, out, d, ldd, _stream(stream))
+
+
+def gemm_f8_run(plan: gemm_plan_f8, A, a_scale, Bt, b_scale, D, stream=None) -> None:
+    """D (m x n, bfloat16 or fp32) = A x B for FP8 tensors A (m x k) and Bt
+    (n x k) with fp32 scales: a_scale (ceil(k/128), m); b_scale
+    (ceil(n/128), ceil(k/128)), or (ceil(k/128), n) for a plan with
+    GEMM_SCALE_ROWS.  Rows may have a pitch (a multiple of 16 for A and Bt)."""
+    _check(_f8_run(plan, A, a_scale, Bt, b_scale, None, D, stream), "gemm_f8_run")
+
+
+def gemm_f8_grouped_run(plan: gemm_plan_f8, A, a_scale, Bt, b_scale, offsets, D, stream=None) -> None:
+    """The grouped product.  GEMM_GROUP_ROWS: Bt (groups, n, k), b_scale
+    (groups, ceil(n/128), ceil(k/128)); rows offsets[g]:offsets[g+1] of A and
+    D belong to group g.  GEMM_GROUP_K: A (m, k), Bt (n, k) from
+    gemm_f8_quantize_cols with the same offsets, D (groups, m, n).  offsets:
+    groups + 1 int32 on the GPU."""
+    if offsets is None:
+        raise TypeError("offsets are needed")
+    _check(_f8_run(plan, A, a_scale, Bt, b_scale, offsets, D, stream), "gemm_f8_grouped_run")
+
+
+def gemm_f8_quantize(X, Q, scale, scale_mode: int = GEMM_SCALE_ROWS, stream=None) -> None:
+    """Q (float8, like X) and its scales from X (rows x cols, bfloat16 or
+    fp32): scale (ceil(cols/128), rows), or (ceil(rows/128), ceil(cols/128))
+    for GEMM_SCALE_BLOCKS."""
+    import torch
+    rows, cols = X.shape
+    x, ldx = _matrix(X, X.dtype, (rows, cols))
+    q, ldq = _matrix(Q, Q.dtype, (rows, cols))
+    kb = (cols + 127) // 128
+    shape = (kb, rows) if scale_mode == GEMM_SCALE_ROWS else ((rows + 127) // 128, kb)
+    st = load().gemm_f8_quantize(x, _real_type(X), rows, cols, ldx, _f8_type(Q), scale_mode, q, ldq,
+                                 _addr(scale, torch.float32, shape), _stream(stream))
+    _check(st, "gemm_f8_quantize")
+
+
+def gemm_f8_quantize_cols(X, Q, scale, offsets=None, stream=None) -> None:
+    """Q (cols x gemm_f8_padded_k(rows, groups), float8) = X^T quantised in
+    blocks of 128 rows of each group, scale (padded_k / 128, cols).  offsets:
+    groups + 1 int32 on the GPU, None for one group of all rows."""
+    import torch
+    rows, cols = X.shape
+    groups = 1 if offsets is None else offsets.shape[0] - 1
+    kp = gemm_f8_padded_k(rows, groups)
+    x, ldx = _matrix(X, X.dtype, (rows, cols))
+    q, ldq = _matrix(Q, Q.dtype, (cols, kp))
+    off = None if offsets is None else _addr(offsets, torch.int32, (groups + 1,))
+    st = load().gemm_f8_quantize_cols(x, _real_type(X), rows, cols, ldx, _f8_type(Q), off, groups, q, ldq,
+                                      _addr(scale, torch.float32, (kp // 128, cols)), _stream(stream))
+    _check(st, "gemm_f8_quantize_cols")
+
+
+def _norm(name, X, R, W, eps, H, rstd, Q, q_dtype, scale, scale_shape, stream):
+    import torch
+    rows, d = X.shape
+    x, ldx = _matrix(X, X.dtype, (rows, d))
+    r, ldr = (None, 0) if R is None else _matrix(R, X.dtype, (rows, d))
+    h, ldh = (None, 0) if H is None else _matrix(H, X.dtype, (rows, d))
+    q, ldq = _matrix(Q, q_dtype, (rows, d))
+    f32 = torch.float32
+    st = getattr(load(), name)(x, ldx, r, ldr, _addr(W, f32, (d,)), eps, _real_type(X), rows, d, h, ldh,
+                               _addr(rstd, f32, (rows,)), q, ldq, _addr(scale, f32, scale_shape), _stream(stream))
+    _check(st, name)
+
+
+def gemm_norm_f8(X, R, W, eps, H, rstd, Q, scale, stream=None) -> None:
+    """h = X + R (kept in H), rstd, and y = h * rstd * W as e4m3 Q with scale
+    (ceil(d/128), rows).  R, H and rstd may be None (H only without R)."""
+    import torch
+    rows, d = X.shape
+    _norm("gemm_norm_f8", X, R, W, eps, H, rstd, Q, torch.float8_e4m3fn, scale, ((d + 127) // 128, rows), stream)
+
+
+def gemm_norm_i8(X, R, W, eps, H, rstd, Q, row_scale, stream=None) -> None:
+    """As gemm_norm_f8 with int8 Q and one scale per row."""
+    import torch
+    _norm("gemm_norm_i8", X, R, W, eps, H, rstd, Q, torch.int8, row_scale, (X.shape[0],), stream)
+
+
+def gemm_norm_backward(dY, H, W, rstd, dR, dX, dW, stream=None) -> None:
+    """dX (the gradient of h) and dW from dY, the gradient of y; dR (may be
+    None) is the gradient that reaches h as the residual, dW may be None."""
+    import torch
+    rows, d = dY.shape
+    dt, f32 = dY.dtype, torch.float32
+    dy, lddy = _matrix(dY, dt, (rows, d))
+    h, ldh = _matrix(H, dt, (rows, d))
+    r, lddr = (None, 0) if dR is None else _matrix(dR, dt, (rows, d))
+    dx, lddx = _matrix(dX, dt, (rows, d))
+    st = load().gemm_norm_backward(dy, lddy, h, ldh, _addr(W, f32, (d,)), _addr(rstd, f32, (rows,)), r, lddr,
+                                   _real_type(dY), rows, d, dx, lddx, _addr(dW, f32, (d,)), _stream(stream))
+    _check(st, "gemm_norm_backward")
 
 
 # ------------------------------------------------------------ convenience --

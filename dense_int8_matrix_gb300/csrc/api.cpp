@@ -8,6 +8,7 @@
 #include <vector>
 
 #include "../../include/dense_int8_matrix.h"
+#include "context.h"
 #include "internal.h"
 
 namespace gemm {
@@ -666,6 +667,43 @@ cudaError_t gemm::kernel_attrs_once(const void* kern, int smem_bytes, bool max_c
                                  static_cast<int>(cudaSharedmemCarveoutMaxShared));
     if (e == cudaSuccess) g_attr_done.push_back(AttrDone{kern, dev});
     return e;
+}
+
+gemm_status gemm::device_context(DeviceContext* out) {
+    DeviceState* ds = nullptr;
+    const gemm_status st = device_state(&ds);
+    if (st != GEMM_OK) return st;
+    if (!ds->supported) return GEMM_ERR_UNSUPPORTED_DEVICE;
+    out->num_sms = ds->num_sms;
+    out->err_word = ds->err_word;
+    out->pool = ds->pool;
+    out->pairs = ds->tc2_pairs;
+    return GEMM_OK;
+}
+
+gemm_status gemm::device_sms(int* num_sms) {
+    DeviceState* ds = nullptr;
+    const gemm_status st = device_state(&ds);
+    if (st == GEMM_OK) *num_sms = ds->num_sms;
+    return st;
+}
+
+bool gemm::trace_begin_call() { return trace_sample_call(); }
+
+void gemm::trace_launch(int kind) { trace_count(kind); }
+
+void* gemm::trace_unit_begin(int kind, cudaStream_t stream, bool sampled) {
+    if (!sampled) return nullptr;
+    std::lock_guard<std::mutex> lock(g_trace_mu);
+    if (!g_trace_on || g_trace_used >= g_trace_cap) return nullptr;
+    TraceRec* rec = &g_trace[g_trace_used++];
+    rec->kind = kind;
+    cudaEventRecord(rec->start, stream);
+    return rec->stop;
+}
+
+void gemm::trace_unit_end(void* unit, cudaStream_t stream) {
+    if (unit) cudaEventRecord(static_cast<cudaEvent_t>(unit), stream);
 }
 
 extern "C" {

@@ -1,0 +1,162 @@
+// Device helpers of the 8-bit operators: vectors of eight input values,
+// rounding to e4m3 / e5m2, group lookup, warp and CTA reductions.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "f8.h"
+
+namespace gemm {
+
+constexpr float kE4M3Max = 448.f;
+constexpr float kE5M2Max = 57344.f;
+constexpr float kScaleMin = 1.17549435e-38f;   // 2^-126: scale of a block of zeros; its reciprocal is finite
+
+// The scale of a block of largest magnitude amax, M the type's largest value.
+__device__ __forceinline__ float block_scale(float amax, float M) { return fmaxf(__fdiv_rn(amax, M), kScaleMin); }
+
+// Two fp32 values to two FP8 values (a in the low byte), round to nearest
+// even, clamped to the largest finite value, NaN stays NaN.
+template <int F8>
+__device__ __forceinline__ uint32_t f8x2(float a, float b) {
+    uint16_t r;
+    if constexpr (F8 == GEMM_F8_E4M3)
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+template <int F8>
+__device__ __forceinline__ uint32_t f8x4(float a, float b, float c, float d) {
+    return f8x2<F8>(a, b) | (f8x2<F8>(c, d) << 16);
+}
+
+// Eight consecutive elements of a row, as stored (16 or 32 bytes).
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {   // rounds to nearest even
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        u = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+};
+template <>
+struct Vec8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        a = make_float4(f[0], f[1], f[2], f[3]);
+        b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void store(float* p) const {
+        reinterpret_cast<float4*>(p)[0] = a;
+        reinterpret_cast<float4*>(p)[1] = b;
+    }
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f32(float x, float* p) { *p = x; }
+__device__ __forceinline__ void from_f32(float x, __nv_bfloat16* p) { *p = __float2bfloat16_rn(x); }
+
+// Elements [c, c + 8) of a row of d; those at or past d are zero.  vec: the
+// row is aligned for whole-vector access.
+template <typename T>
+__device__ __forceinline__ Vec8<T> load8(const T* row, int64_t c, int64_t d, bool vec) {
+    Vec8<T> v;
+    if (vec && c + 8 <= d) {
+        v.load(row + c);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = c + i < d ? to_f32(row[c + i]) : 0.f;
+        v.set(f);
+    }
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int64_t c, int64_t d, bool vec, const Vec8<T>& v) {
+    if (vec && c + 8 <= d) {
+        v.store(row + c);
+    } else {
+        float f[8];
+        v.get(f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < d) from_f32(f[i], row + c + i);
+    }
+}
+// Eight bytes (two words) to elements [c, c + 8) of a byte row of d.
+__device__ __forceinline__ void store8_bytes(uint8_t* row, int64_t c, int64_t d, bool vec, uint32_t lo, uint32_t hi) {
+    if (vec && c + 8 <= d) {
+        *reinterpret_cast<uint2*>(row + c) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < d) row[c + i] = static_cast<uint8_t>((i < 4 ? lo >> (8 * i) : hi >> (8 * i - 32)) & 0xffu);
+    }
+}
+__device__ __forceinline__ void load8_f32(const float* w, int64_t c, int64_t d, bool vec, float (&f)[8]) {
+    if (vec && c + 8 <= d) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(w + c));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = c + i < d ? __ldg(w + c + i) : 0.f;
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+// Largest of the 16 lanes of this half warp (one block of 128 columns).
+__device__ __forceinline__ float half_warp_max(float v) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// Row range of group g, clamped to [0, rows].
+__device__ __forceinline__ void group_rows(const int32_t* offsets, int g, int rows, int& lo, int& hi) {
+    lo = min(max(__ldg(offsets + g), 0), rows);
+    hi = min(max(__ldg(offsets + g + 1), lo), rows);
+}
+
+}  // namespace gemm

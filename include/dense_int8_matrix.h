@@ -247,6 +247,199 @@ GEMM_API gemm_status gemm_i8_run_host(const gemm_plan *plan, const int8_t *A, co
 GEMM_API gemm_status gemm_bf16_run_host(const gemm_plan *plan, const uint16_t *A, const uint16_t *Bt, float *C,
                                void *stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit operators around the GEMM: FP8 products with a scale for each block
+ * of 128, the same products grouped by expert, the FP8 quantisation that
+ * makes their operands, and the RMS norm that writes an 8-bit activation.
+ *
+ * FP8 values are one byte each (GEMM_F8_E4M3: 4 exponent bits, largest value
+ * 448; GEMM_F8_E5M2: 5 exponent bits, largest value 57344), rows contiguous,
+ * with a row pitch in elements.  An FP8 operand of the product needs a
+ * 16-byte aligned address and a row pitch that is a multiple of 16; k itself
+ * may be any size, and the bytes between k and the pitch are never used.
+ *
+ * A scale is an fp32 factor: the element stands for (8-bit value) * scale.
+ *   GEMM_SCALE_ROWS    one scale per row and block of 128 columns, stored
+ *                      block-major: scale[b * rows + i], b < ceil(k / 128);
+ *   GEMM_SCALE_BLOCKS  one scale per 128 x 128 block, stored
+ *                      scale[(j / 128) * ceil(k / 128) + b].
+ * Quantising takes scale = max(amax / M, 2^-126), amax the block's largest
+ * magnitude and M the type's largest value, and rounds x * (1 / scale) to the
+ * nearest 8-bit value, ties to even; each step is one fp32 operation.  A
+ * block of zeros gets the scale 2^-126.  An infinity in a block makes its
+ * scale infinite, its own 8-bit value NaN and the block's others zero, so
+ * every product that reads the block is NaN; a NaN element is a NaN of the
+ * 8-bit type and leaves its block's scale to the others.
+ *
+ * The entry points below take device pointers, enqueue on `stream` and
+ * return, like gemm_*_run; the trace counts quantisation and norms as
+ * GEMM_KERNEL_STAGE, products as GEMM_KERNEL_TC or GEMM_KERNEL_SKINNY.
+ * ------------------------------------------------------------------------ */
+enum { GEMM_F8_E4M3 = 0, GEMM_F8_E5M2 = 1 };
+enum { GEMM_SCALE_ROWS = 0, GEMM_SCALE_BLOCKS = 1 };
+enum { GEMM_OUT_F32 = 3 };    /* beside GEMM_OUT_BF16: output types of gemm_f8_*run */
+enum { GEMM_DTYPE_F32 = 2 };  /* beside GEMM_DTYPE_BF16: input types of gemm_f8_quantize* and gemm_norm_* */
+
+/* How a product is grouped by expert. */
+enum {
+    GEMM_GROUP_NONE = 0, /* one product */
+    GEMM_GROUP_ROWS = 1, /* the rows of A (and of D) belong to groups, each with its own Bt */
+    GEMM_GROUP_K = 2     /* the K columns of A and Bt belong to groups, each with its own D */
+};
+
+#define GEMM_PLAN_F8_VERSION 1
+#define GEMM_F8_MAX_GROUPS 1024
+#define GEMM_NORM_MAX_D 32768
+
+/* The configuration of an FP8 product.  Plain data, filled by gemm_f8_*plan*. */
+typedef struct gemm_plan_f8 {
+    int32_t version;    /* GEMM_PLAN_F8_VERSION */
+    int32_t path;       /* GEMM_PATH_TENSOR: two-SM tiles; GEMM_PATH_SKINNY: few rows, Bt streamed */
+    int32_t num_sms;    /* SM count the plan was made for */
+    int32_t group_mode; /* GEMM_GROUP_* */
+    int64_t m, k, n;
+    int32_t groups;     /* 1 for GEMM_GROUP_NONE */
+    int32_t a_type, b_type; /* GEMM_F8_* */
+    int32_t b_scale;    /* GEMM_SCALE_*: layout of b_scale (a_scale is always GEMM_SCALE_ROWS) */
+    int32_t bm, bn;     /* rows and columns of D per tile */
+    int32_t split_k;    /* skinny path: CTAs that share a tile along K and join their sums */
+    int32_t reserved32;
+    int64_t reserved[4];
+} gemm_plan_f8;
+
+/*
+ * Plan D (m x n) = A (m x k) x B with FP8 A and Bt (n x k).  Grouped:
+ *   GEMM_GROUP_ROWS  A is m x k, D m x n, and Bt holds `groups` matrices of
+ *                    n x k one after the other (group g starts at row g*n);
+ *                    rows offsets[g] .. offsets[g+1]-1 of A are multiplied
+ *                    with group g's Bt: the forward product of a layer of
+ *                    experts, and its input gradient.
+ *   GEMM_GROUP_K     A is m x k and Bt n x k as gemm_f8_quantize_cols writes
+ *                    them (k = gemm_f8_padded_k(rows, groups)); D holds
+ *                    `groups` matrices of m x n, and group g's is the sum
+ *                    over that group's columns: the weight gradient.  A
+ *                    group without rows gets zeros.
+ * Host-only apart from one cached query of the device's SM count;
+ * gemm_f8_plan_for_sms makes no CUDA call.
+ * Errors: GEMM_ERR_INVALID_ARG (NULL out; m, k or n outside [1, 2^31-1];
+ * groups outside [1, GEMM_F8_MAX_GROUPS], or not 1 without grouping;
+ * groups * n (ROWS) or groups * m (K) above 2^31-1; k no multiple of 128
+ * (K); unknown type, scale layout or mode), GEMM_ERR_CUDA (no device).
+ */
+GEMM_API gemm_status gemm_f8_plan(int64_t m, int64_t k, int64_t n, int32_t a_type, int32_t b_type, int32_t b_scale,
+                                  gemm_plan_f8 *out);
+GEMM_API gemm_status gemm_f8_grouped_plan(int32_t group_mode, int32_t groups, int64_t m, int64_t k, int64_t n,
+                                          int32_t a_type, int32_t b_type, int32_t b_scale, gemm_plan_f8 *out);
+GEMM_API gemm_status gemm_f8_plan_for_sms(int32_t group_mode, int32_t groups, int64_t m, int64_t k, int64_t n,
+                                          int32_t a_type, int32_t b_type, int32_t b_scale, int32_t num_sms,
+                                          gemm_plan_f8 *out);
+
+/*
+ * D[i][j] = sum_b (a_scale[b][i] * b_scale[..]) * sum_{kk in block b} A[i][kk] * Bt[j][kk]
+ * with fp32 accumulation: each block of 128 is summed, scaled and added to an
+ * fp32 running sum, which is rounded once to the output type (GEMM_OUT_BF16
+ * or GEMM_OUT_F32).  lda, ldb, ldd: row pitches in elements (lda, ldb >= k
+ * and multiples of 16, ldd >= n).  D needs its element's alignment only.
+ * A plan may be edited to force the path, bn (skinny: 16, 32, 64 or 128 rows
+ * in bm) or split_k (1, 2, 4 or 8) before the call; the sums then join in
+ * another order, so results agree to fp32 rounding, not bit for bit.  One
+ * plan always gives the same bits.
+ * Errors: GEMM_ERR_INVALID_ARG (null pointer, bad plan, a grouped plan, pitch
+ * too small, out_type), GEMM_ERR_MISALIGNED (A or Bt not 16-byte aligned, lda
+ * or ldb not a multiple of 16, a scale not 4-byte or D not element aligned),
+ * GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
+ */
+GEMM_API gemm_status gemm_f8_run(const gemm_plan_f8 *plan, const uint8_t *A, int64_t lda, const float *a_scale,
+                                 const uint8_t *Bt, int64_t ldb, const float *b_scale, int32_t out_type, void *D,
+                                 int64_t ldd, void *stream);
+
+/*
+ * The grouped product; plan from gemm_f8_grouped_plan.  offsets: groups + 1
+ * int32 on the device, non-decreasing, read by the kernels only (the host
+ * never waits for them): rows for GEMM_GROUP_ROWS; for GEMM_GROUP_K the same
+ * row offsets that gemm_f8_quantize_cols was given.  Values are clamped to
+ * the matrix, so a wrong list gives wrong sums but no access outside the
+ * operands.  Rows of D outside every group are not written.  Scales of the
+ * groups' Bt lie one after the other (GEMM_SCALE_BLOCKS: groups x ceil(n/128)
+ * x ceil(k/128); GEMM_SCALE_ROWS: ceil(k/128) x (groups * n)).
+ * Same rules and errors as gemm_f8_run.
+ */
+GEMM_API gemm_status gemm_f8_grouped_run(const gemm_plan_f8 *plan, const uint8_t *A, int64_t lda,
+                                         const float *a_scale, const uint8_t *Bt, int64_t ldb, const float *b_scale,
+                                         const int32_t *offsets, int32_t out_type, void *D, int64_t ldd,
+                                         void *stream);
+
+/*
+ * Quantise X (rows x cols, x_type GEMM_DTYPE_BF16 or GEMM_DTYPE_F32, row
+ * pitch ldx) to FP8: Q (rows x cols, row pitch ldq) and its scales, in the
+ * layout `scale_mode` (GEMM_SCALE_ROWS or GEMM_SCALE_BLOCKS).
+ * Errors: GEMM_ERR_INVALID_ARG (null pointer, size outside [1, 2^31-1],
+ * pitch below cols, unknown type or mode), GEMM_ERR_MISALIGNED (X or scale
+ * not element aligned), GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
+ */
+GEMM_API gemm_status gemm_f8_quantize(const void *X, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx,
+                                      int32_t f8_type, int32_t scale_mode, uint8_t *Q, int64_t ldq, float *scale,
+                                      void *stream);
+
+/*
+ * The transposed form, for products that sum over rows (weight gradients):
+ * Q (cols x kp, row pitch ldq >= kp, kp = gemm_f8_padded_k(rows, groups))
+ * holds X^T, one GEMM_SCALE_ROWS scale per column and block of 128 rows:
+ * scale[b * cols + j].  offsets == NULL: one group of all rows (groups must
+ * be 1).  Otherwise offsets (groups + 1 int32 on the device) gives each
+ * group's rows; a group's columns of Q start at a multiple of 128 behind the
+ * group before it and are filled up to a multiple of 128 with zeros.
+ * Columns behind the last group are not written.  Q must be 16-byte aligned
+ * with ldq a multiple of 16.  Same errors as gemm_f8_quantize, and
+ * GEMM_ERR_MISALIGNED for Q and ldq.
+ */
+GEMM_API gemm_status gemm_f8_quantize_cols(const void *X, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx,
+                                           int32_t f8_type, const int32_t *offsets, int32_t groups, uint8_t *Q,
+                                           int64_t ldq, float *scale, void *stream);
+
+/* Columns that `rows` rows in `groups` groups can take when each group is
+ * filled up to a multiple of 128: floor((rows + 127 * groups) / 128) * 128.
+ * 0 if rows or groups is below 1. */
+GEMM_API int64_t gemm_f8_padded_k(int64_t rows, int32_t groups);
+
+/*
+ * Residual addition, RMS norm and 8-bit quantisation in one pass over rows x
+ * d elements (x_type GEMM_DTYPE_BF16 or GEMM_DTYPE_F32):
+ *   h    = X + R, rounded to x_type        (R == NULL: h = X)
+ *   rstd = 1 / sqrt(mean_j(h_j^2) + eps)   (fp32)
+ *   y_j  = h_j * rstd * W[j]
+ * gemm_norm_f8 writes y as e4m3 with GEMM_SCALE_ROWS scales, ready as A of
+ * gemm_f8_run.  gemm_norm_i8 writes int8 with one scale per row, scale =
+ * max(amax / 127, 2^-126), nearest integer, ties to even: ready as A and
+ * row_scale of gemm_i8_run_requant; a row whose mean square is infinite or
+ * NaN has a NaN scale.  H (may be NULL if R is NULL) gets h and may be X or R itself (with
+ * that one's pitch); rstd (rows floats, may be NULL) is kept for the
+ * backward pass.  W: d floats.  Pitches ldx, ldr, ldh, ldq in elements.
+ * d <= GEMM_NORM_MAX_D; eps >= 0.
+ * Errors: as gemm_f8_quantize.
+ */
+GEMM_API gemm_status gemm_norm_f8(const void *X, int64_t ldx, const void *R, int64_t ldr, const float *W, float eps,
+                                  int32_t x_type, int64_t rows, int64_t d, void *H, int64_t ldh, float *rstd,
+                                  uint8_t *Q, int64_t ldq, float *scale, void *stream);
+GEMM_API gemm_status gemm_norm_i8(const void *X, int64_t ldx, const void *R, int64_t ldr, const float *W, float eps,
+                                  int32_t x_type, int64_t rows, int64_t d, void *H, int64_t ldh, float *rstd,
+                                  int8_t *Q, int64_t ldq, float *row_scale, void *stream);
+
+/*
+ * The gradient of y = h * rstd * W (the quantisation passes gradients
+ * through unchanged), from dY, h and rstd as the forward call wrote them:
+ *   xhat = h * rstd,  g = dY * W
+ *   dX = dR + rstd * (g - xhat * mean_j(g * xhat))   (dR may be NULL: 0)
+ *   dW_j = sum_i dY_ij * xhat_ij                      (fp32, overwritten)
+ * dR is the gradient that reaches h as the residual; dX (x_type, pitch lddx)
+ * is the gradient of X and of R, and may be dR itself (with its pitch).  dW
+ * may be NULL.  Sums are taken in a fixed order: the same call gives the same
+ * bits.  Errors: as gemm_norm_f8.
+ */
+GEMM_API gemm_status gemm_norm_backward(const void *dY, int64_t lddy, const void *H, int64_t ldh, const float *W,
+                                        const float *rstd, const void *dR, int64_t lddr, int32_t x_type, int64_t rows,
+                                        int64_t d, void *dX, int64_t lddx, float *dW, void *stream);
+
 /*
  * Waits for `stream`, then reads and clears the current device's error word,
  * which the kernels of every run entry point (gemm_i8_run_noalloc included)
