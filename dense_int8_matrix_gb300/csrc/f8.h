@@ -31,6 +31,8 @@ struct F8Launch {
 };
 
 cudaError_t launch_f8_simple(const F8Launch& a, cudaStream_t stream);
+// Two-SM tiles of 256 x bn (gemm_f8_tc2.cu).
+cudaError_t launch_f8_tc2(const F8Launch& a, cudaStream_t stream);
 
 // ---- quantisation (quantize.cu) ----------------------------------------------
 struct F8Quant {

@@ -9,7 +9,7 @@ using namespace gemm;
 
 namespace {
 
-constexpr int64_t kMaxDim = INT32_MAX;
+constexpr int64_t kMaxDim = int64_t(1) << 30;   // coordinates of tiles past the edge stay in 32 bits
 
 bool al(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool dim_ok(int64_t v) { return v >= 1 && v <= kMaxDim; }
@@ -119,7 +119,7 @@ gemm_status run_f8(const gemm_plan_f8* p, const uint8_t* A, int64_t lda, const f
     const int kind = p->path == GEMM_PATH_SKINNY ? GEMM_KERNEL_SKINNY : GEMM_KERNEL_TC;
     const bool sampled = trace_begin_call();
     void* unit = trace_unit_begin(kind, stream, sampled);
-    const cudaError_t e = launch_f8_simple(L, stream);
+    const cudaError_t e = p->path == GEMM_PATH_SKINNY ? launch_f8_simple(L, stream) : launch_f8_tc2(L, stream);
     trace_unit_end(unit, stream);
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     trace_launch(kind);

@@ -1,0 +1,375 @@
+// FP8 product with block scales on two-SM tiles (tcgen05 cta_group::2).
+//
+//   D[i][j] = sum_b (sa[b][i] * sb[..]) * (sum of block b of A[i] * Bt[j])
+//
+// A cluster of two CTAs computes a 256 x BN tile; each CTA loads 128 rows of
+// A and BN / 2 rows of Bt per K block with TMA, and one tcgen05.mma (M = 256,
+// N = BN, K = 32, four per block) leaves its 128 rows in its own TMEM.  The
+// scales change with every block of 128, so a block's sums are not added up
+// in TMEM: the MMA of block b + 1 writes another TMEM buffer while the eight
+// epilogue warps read block b's, multiply by the scales and add to fp32
+// running sums in registers (BN / 2 per thread).  The tensor pipe needs
+// 2 * BN cycles per block; reading BN columns of TMEM and the BN multiply-adds
+// per lane quarter fit beside it.
+//
+// Roles as in the library's other two-SM kernel: warp 0 loads, warp 1 of the
+// even CTA issues MMAs, warps 4-11 scale, add and store.  Grouped products
+// read the group offsets on the device: warp 2 sums them into shared memory
+// first, and every role walks the same list of tiles.
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "f8_tc.cuh"
+#include "internal.h"
+
+namespace gemm {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kHalfRows = 128;                       // rows of A per CTA
+constexpr int kABytes = kHalfRows * kF8RowBytes;
+constexpr int kEpiBytes = kEpiWarps * 4096;
+constexpr int kScaleBytes = kEpiWarps * 128 * 4;     // column scales of one block, per warp
+constexpr int kPreBytes = (GEMM_F8_MAX_GROUPS + 1) * 4 + 12;
+constexpr int kCtrlBytes = 512;
+
+template <int BN>
+struct Ring {
+    static constexpr int B_BYTES = BN / 2 * kF8RowBytes;
+    static constexpr int STAGE = kABytes + B_BYTES;
+    static constexpr int STAGES = BN == 256 ? 5 : 7;
+    static constexpr int BUFS = 512 / BN;            // TMEM accumulators
+    static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + kEpiBytes + kScaleBytes + kPreBytes + kCtrlBytes + 1024;
+};
+static_assert(Ring<256>::SMEM <= 232448 && Ring<128>::SMEM <= 232448, "shared memory");
+
+struct Unit {
+    int arow;      // first row of A of the pair's tile
+    int drow;      // its row of D
+    int dend;      // rows of D at or past this are not the tile's
+    int brow;      // first row of Bt
+    int col;       // first column of D
+    int sblock;    // block-scale row: group * nb + col / 128
+    int kb_lo, kb_hi;
+};
+
+__device__ __forceinline__ int unit_count(const F8Params& p, const int32_t* pre) {
+    if (p.mode == GEMM_GROUP_ROWS) return pre[p.groups] * p.tiles_n;
+    return p.groups * p.tiles_m * p.tiles_n;
+}
+
+template <int BN>
+__device__ __forceinline__ Unit unit_at(int u, const F8Params& p, const int32_t* pre) {
+    Unit x;
+    int g = 0, tm, tn, lo = 0, hi = p.m;
+    if (p.mode == GEMM_GROUP_ROWS) {
+        g = group_of(pre, p.groups, u / p.tiles_n);
+        group_rows(p.offsets, g, p.m, lo, hi);
+        tc_tile_coords(u - pre[g] * p.tiles_n, pre[g + 1] - pre[g], p.tiles_n, tm, tn);
+    } else {
+        const int per = p.tiles_m * p.tiles_n;
+        g = u / per;
+        tc_tile_coords(u - g * per, p.tiles_m, p.tiles_n, tm, tn);
+    }
+    x.arow = lo + tm * 256;
+    x.drow = x.arow;
+    x.dend = hi;
+    x.col = tn * BN;
+    x.brow = x.col;
+    x.sblock = x.col / kF8Block;
+    x.kb_lo = 0;
+    x.kb_hi = p.kb;
+    if (p.mode == GEMM_GROUP_ROWS) {
+        x.brow += g * p.n;
+        x.sblock += g * p.nb;
+    } else if (p.mode == GEMM_GROUP_K) {
+        x.drow += g * p.m;
+        x.dend += g * p.m;
+        x.kb_lo = min(pre[g], p.kb);
+        x.kb_hi = min(pre[g + 1], p.kb);
+    }
+    return x;
+}
+
+template <int BN, bool BROWS>
+__global__ void __launch_bounds__(kThreads, 1)
+    f8_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Params p,
+                  const uint32_t idesc) {
+    using R = Ring<BN>;
+    constexpr int kStages = R::STAGES, kBufs = R::BUFS;
+    constexpr int kCols = BN / 2;   // columns per epilogue thread
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t sA = base;
+    const uint32_t sB = base + kStages * kABytes;
+    const uint32_t sEpi = base + kStages * R::STAGE;
+    const uint32_t sScale = sEpi + kEpiBytes;
+    uint8_t* ctrl = smem_raw + (sScale - raw) + kScaleBytes;
+    int32_t* pre = reinterpret_cast<int32_t*>(ctrl + kCtrlBytes);
+    const uint32_t bar0 = smem_u32(ctrl);
+    const uint32_t full0 = bar0;                      // used in the even CTA
+    const uint32_t empty0 = full0 + 8u * kStages;
+    const uint32_t accf0 = empty0 + 8u * kStages;
+    const uint32_t acce0 = accf0 + 8u * kBufs;        // used in the even CTA
+    const uint32_t done = acce0 + 8u * kBufs;
+    static_assert(8 * (2 * kStages + 2 * kBufs + 1) + 8 <= kCtrlBytes, "barriers fit");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kStages + 2 * kBufs + 1));
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank_in_cluster();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full0 + 8u * s, 1);
+            mbar_init(empty0 + 8u * s, 1);
+        }
+        for (int b = 0; b < kBufs; ++b) {
+            mbar_init(accf0 + 8u * b, 1);
+            mbar_init(acce0 + 8u * b, 2 * kEpiWarps);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0u;
+        fence_barrier_init();
+    }
+    if (warp == 1) alloc_pair(smem_u32(tmem_slot), 512);
+    if (warp == 2 && p.mode != GEMM_GROUP_NONE) {
+        pdl_wait();   // the offsets may come from the kernel before
+        if (p.mode == GEMM_GROUP_ROWS)
+            group_prefix(p.offsets, p.groups, p.m, 256, p.pieces, lane, pre);
+        else
+            group_prefix(p.offsets, p.groups, p.kb * kF8Block, kF8Block, p.kb, lane, pre);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();   // barriers and TMEM of both CTAs are ready
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int units = unit_count(p, pre);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            pdl_wait();
+            const uint64_t pol = policy_evict_normal();
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int u = pair; ok && u < units; u += npairs) {
+                const Unit w = unit_at<BN>(u, p, pre);
+                const int ya = w.arow + static_cast<int>(rank) * kHalfRows;
+                const int yb = w.brow + static_cast<int>(rank) * (BN / 2);
+                for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
+                    const uint32_t s = issued % kStages, ph = (issued / kStages) & 1u;
+                    if (!wait_bounded(empty0 + 8u * s, ph ^ 1u, abort_flag, p.err, kDevErrTimeoutProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = peer_address(full0 + 8u * s, 0);
+                    if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * R::STAGE);
+                    load_2d_pair(sA + s * kABytes, &tmA, kb * kF8Block, ya, fb, pol);
+                    load_2d_pair(sB + s * R::B_BYTES, &tmB, kb * kF8Block, yb, fb, pol);
+                    ++issued;
+                }
+            }
+            // after a time-out the copies still in flight land before the pair ends
+            if (!ok && leader)
+                for (uint32_t j = issued > kStages ? issued - kStages : 0u; j < issued; ++j)
+                    wait_bounded(full0 + 8u * (j % kStages), (j / kStages) & 1u, nullptr, p.err, kDevErrTimeoutTeardown);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            uint32_t n = 0;   // K blocks so far: operand stage and accumulator in turn
+            bool ok = true;
+            for (int u = pair; ok && u < units; u += npairs) {
+                const Unit w = unit_at<BN>(u, p, pre);
+                for (int kb = w.kb_lo; kb < w.kb_hi; ++kb, ++n) {
+                    const uint32_t s = n % kStages, b = n % kBufs;
+                    if (!wait_bounded(acce0 + 8u * b, ((n / kBufs) & 1u) ^ 1u, abort_flag, p.err, kDevErrTimeoutMma) ||
+                        !wait_bounded(full0 + 8u * s, (n / kStages) & 1u, abort_flag, p.err, kDevErrTimeoutMma)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = smem_desc_sw128_kmajor(sA + s * kABytes);
+                    const uint64_t bd = smem_desc_sw128_kmajor(sB + s * R::B_BYTES);
+#pragma unroll
+                    for (int kk = 0; kk < kF8Block / kF8MmaK; ++kk)
+                        mma_f8<2>(tmem + b * BN, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0 ? 1u : 0u);
+                    commit_pair(empty0 + 8u * s);
+                    commit_pair(accf0 + 8u * b);
+                }
+            }
+            commit_pair(done);
+            wait_bounded(done, 0u, nullptr, p.err, kDevErrTimeoutTeardown);
+        }
+    } else if (warp >= 4) {
+        pdl_wait();
+        const int e = warp - 4, q = warp & 3, h = e >> 2;
+        const uint32_t stg = sEpi + e * 4096, scl = sScale + e * 512;
+        const uint32_t acce = peer_address(acce0, 0);
+        uint32_t n = 0;
+        bool ok = true;
+        for (int u = pair; ok && u < units; u += npairs) {
+            const Unit w = unit_at<BN>(u, p, pre);
+            const int in_tile = static_cast<int>(rank) * kHalfRows + q * 32;   // the warp's first row
+            const int arow = min(w.arow + in_tile + lane, static_cast<int>(p.rows_a) - 1);
+            const int col = w.col + h * kCols;
+            const float* sa = p.a_scale + arow;
+            // column scales: one per block of 128 columns, or one per column
+            const float* sb = BROWS ? p.b_scale + (w.brow - w.col) + col
+                                    : p.b_scale + static_cast<int64_t>(w.sblock + (BN == 256 ? h : 0)) * p.kb;
+            const bool col_in = BROWS || col / kF8Block < p.nb;
+            float acc[kCols];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) acc[j] = 0.f;
+            for (int kb = w.kb_lo; kb < w.kb_hi; ++kb, ++n) {
+                const uint32_t b = n % kBufs;
+                float s = __ldg(sa + static_cast<int64_t>(kb) * p.rows_a);
+                if constexpr (BROWS) {
+                    __syncwarp();   // the block before has been read
+#pragma unroll
+                    for (int i = 0; i < kCols / 32; ++i) {
+                        const int c = lane + 32 * i;
+                        const float v = col + c < p.n ? __ldg(sb + static_cast<int64_t>(kb) * p.rows_b + c) : 0.f;
+                        st_shared_u32(scl + 4 * c, __float_as_uint(v));
+                    }
+                    __syncwarp();
+                } else {
+                    s *= col_in ? __ldg(sb + kb) : 0.f;
+                }
+                if (!wait_bounded(accf0 + 8u * b, (n / kBufs) & 1u, abort_flag, p.err, kDevErrTimeoutEpilogue)) ok = false;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * BN + h * kCols;
+#pragma unroll
+                for (int c = 0; c < kCols / 16; ++c) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(t0 + c * 16, v);
+                    tmem_wait_ld();
+                    if constexpr (BROWS) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const uint4 x = ld_shared_v4(scl + (c * 16 + j) * 4);
+                            acc[c * 16 + j] = fmaf(__uint_as_float(v[j]) * s, __uint_as_float(x.x), acc[c * 16 + j]);
+                            acc[c * 16 + j + 1] = fmaf(__uint_as_float(v[j + 1]) * s, __uint_as_float(x.y), acc[c * 16 + j + 1]);
+                            acc[c * 16 + j + 2] = fmaf(__uint_as_float(v[j + 2]) * s, __uint_as_float(x.z), acc[c * 16 + j + 2]);
+                            acc[c * 16 + j + 3] = fmaf(__uint_as_float(v[j + 3]) * s, __uint_as_float(x.w), acc[c * 16 + j + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fmaf(__uint_as_float(v[j]), s, acc[c * 16 + j]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_in_cluster(acce + 8u * b);
+            }
+            if (!ok) break;
+            if (p.out_f32)
+                store_rows<true>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
+                                 p.d_vec != 0);
+            else
+                store_rows<false>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
+                                  p.d_vec != 0);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_barrier();   // the peer may still use this CTA's shared memory or barriers until here
+    tc_fence_after();
+    if (warp == 1) free_pair(tmem, 512);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+template <int BN, bool BROWS>
+cudaError_t launch(const F8Launch& a, cudaStream_t stream) {
+    using R = Ring<BN>;
+    CUtensorMap mA, mB;
+    if (!encode_f8(&mA, a.A, a.k, a.rows_a, a.lda, kHalfRows) || !encode_f8(&mB, a.Bt, a.k, a.rows_b, a.ldb, BN / 2))
+        return cudaErrorInvalidValue;
+    F8Params p = f8_params(a, 256, BN);
+    const int64_t units = a.group_mode == GEMM_GROUP_ROWS ? static_cast<int64_t>(p.pieces) * p.tiles_n
+                                                          : static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.groups;
+    if (units > INT32_MAX) return cudaErrorInvalidValue;
+    int64_t pairs = a.pairs > 0 ? a.pairs : a.num_sms / 2;
+    if (pairs > units) pairs = units;
+    if (pairs < 1) pairs = 1;
+    const void* kern = reinterpret_cast<const void*>(f8_tc2_kernel<BN, BROWS>);
+    const cudaError_t e = kernel_attrs_once(kern, static_cast<int>(R::SMEM), true);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = R::SMEM;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    uint32_t idesc = idesc_f8(a.a_type, a.b_type, 256, BN);
+    void* args[] = {&mA, &mB, &p, &idesc};
+    const cudaError_t r = cudaLaunchKernelExC(&cfg, kern, args);
+    return r != cudaSuccess ? r : cudaGetLastError();
+}
+
+}  // namespace
+
+bool encode_f8(CUtensorMap* map, const void* ptr, int64_t k, int64_t rows, int64_t ld, int box_rows) {
+    auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (!enc) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(kF8RowBytes), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+F8Params f8_params(const F8Launch& a, int bm, int bn) {
+    F8Params p;
+    p.a_scale = a.a_scale;
+    p.b_scale = a.b_scale;
+    p.offsets = a.offsets;
+    p.D = a.D;
+    p.err = a.err;
+    p.ldd = a.ldd;
+    p.rows_a = a.rows_a;
+    p.rows_b = a.rows_b;
+    p.m = static_cast<int>(a.m);
+    p.n = static_cast<int>(a.n);
+    p.groups = a.groups;
+    p.mode = a.group_mode;
+    p.kb = static_cast<int>((a.k + kF8Block - 1) / kF8Block);
+    p.nb = static_cast<int>((a.n + kF8Block - 1) / kF8Block);
+    p.tiles_m = static_cast<int>((a.m + bm - 1) / bm);
+    p.tiles_n = static_cast<int>((a.n + bn - 1) / bn);
+    p.pieces = static_cast<int>(a.m / bm + (a.groups < a.m ? a.groups : a.m));   // each group may end in a part of a tile
+    p.out_f32 = a.out_f32 ? 1 : 0;
+    p.d_vec = reinterpret_cast<uintptr_t>(a.D) % 16 == 0 && (a.ldd * (a.out_f32 ? 4 : 2)) % 16 == 0;
+    return p;
+}
+
+cudaError_t launch_f8_tc2(const F8Launch& a, cudaStream_t stream) {
+    const bool rows = a.b_scale_mode == GEMM_SCALE_ROWS;
+    if (a.bn == 128) return rows ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+    return rows ? launch<256, true>(a, stream) : launch<256, false>(a, stream);
+}
+
+}  // namespace gemm

@@ -321,9 +321,9 @@ typedef struct gemm_plan_f8 {
  *                    group without rows gets zeros.
  * Host-only apart from one cached query of the device's SM count;
  * gemm_f8_plan_for_sms makes no CUDA call.
- * Errors: GEMM_ERR_INVALID_ARG (NULL out; m, k or n outside [1, 2^31-1];
+ * Errors: GEMM_ERR_INVALID_ARG (NULL out; m, k or n outside [1, 2^30];
  * groups outside [1, GEMM_F8_MAX_GROUPS], or not 1 without grouping;
- * groups * n (ROWS) or groups * m (K) above 2^31-1; k no multiple of 128
+ * groups * n (ROWS) or groups * m (K) above 2^30; k no multiple of 128
  * (K); unknown type, scale layout or mode), GEMM_ERR_CUDA (no device).
  */
 GEMM_API gemm_status gemm_f8_plan(int64_t m, int64_t k, int64_t n, int32_t a_type, int32_t b_type, int32_t b_scale,
@@ -373,7 +373,7 @@ GEMM_API gemm_status gemm_f8_grouped_run(const gemm_plan_f8 *plan, const uint8_t
  * Quantise X (rows x cols, x_type GEMM_DTYPE_BF16 or GEMM_DTYPE_F32, row
  * pitch ldx) to FP8: Q (rows x cols, row pitch ldq) and its scales, in the
  * layout `scale_mode` (GEMM_SCALE_ROWS or GEMM_SCALE_BLOCKS).
- * Errors: GEMM_ERR_INVALID_ARG (null pointer, size outside [1, 2^31-1],
+ * Errors: GEMM_ERR_INVALID_ARG (null pointer, size outside [1, 2^30],
  * pitch below cols, unknown type or mode), GEMM_ERR_MISALIGNED (X or scale
  * not element aligned), GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
  */
@@ -399,7 +399,7 @@ GEMM_API gemm_status gemm_f8_quantize_cols(const void *X, int32_t x_type, int64_
 
 /* Columns that `rows` rows in `groups` groups can take when each group is
  * filled up to a multiple of 128: floor((rows + 127 * groups) / 128) * 128.
- * 0 if rows or groups is below 1. */
+ * 0 if rows is outside [1, 2^30] or groups below 1. */
 GEMM_API int64_t gemm_f8_padded_k(int64_t rows, int32_t groups);
 
 /*
