@@ -26,6 +26,29 @@ struct F8Params {
     int pieces;           // row tiles that all groups together can have (GEMM_GROUP_ROWS)
 };
 
+// wait_bounded() for waits of every K block: the clock it bounds itself with
+// is slow to read, so it is asked only after some probes.
+constexpr int kWaitProbes = 256;
+__device__ __forceinline__ bool wait_step(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int* err_word,
+                                          int code) {
+    for (int i = 0; i < kWaitProbes; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return wait_bounded(bar, parity, abort_flag, err_word, code);
+}
+
+// A place in a ring of N and the parity of the round, stepped without division.
+template <uint32_t N>
+struct Turn {
+    uint32_t i = 0, ph = 0;
+    __device__ __forceinline__ void next(uint32_t by = 1) {
+        i += by;
+        if (i >= N) {
+            i -= N;
+            ph ^= 1u;
+        }
+    }
+};
+
 // Instruction descriptor of tcgen05.mma kind::f8f6f4: D fp32 (bits 4-5 = 1),
 // A and B format (bits 7-9, 10-12: 0 = e4m3, 1 = e5m2), both K-major, N >> 3
 // in bits 17-22, M >> 4 in bits 24-28.
@@ -100,13 +123,87 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// Waits for this thread's TMEM loads; r is not read before.
+__device__ __forceinline__ void wait_tmem(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// Two fp32 values in one 64-bit register pair, and a * b + c on both.
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float& lo, float& hi) {
+    uint32_t a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(d));
+    lo = __uint_as_float(a);
+    hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Adds 32 columns of a block's sums, scaled, to the running sums: by s, or by
+// s and the column scales at shared address `cols`.
+template <bool COLS>
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[32], uint64_t s, uint32_t cols) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        uint64_t x0 = s, x1 = s;
+        if constexpr (COLS) {
+            const uint4 c = ld_shared_v4(cols + 8 * j);
+            x0 = mul2(s, pair_of(c.x, c.y));
+            x1 = mul2(s, pair_of(c.z, c.w));
+        }
+        acc[j] = fma2(pair_of(v[2 * j], v[2 * j + 1]), x0, acc[j]);
+        acc[j + 1] = fma2(pair_of(v[2 * j + 2], v[2 * j + 3]), x1, acc[j + 1]);
+    }
+}
+
+// Four bytes from global to shared memory without waiting (zero if !in).
+__device__ __forceinline__ void copy4_async(uint32_t dst, const float* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)),
+                 "r"(in ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's groups of copies are on their way.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
+
+// Registers of the calling warpgroup (all four warps call it).
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // A warp's 32 rows (lane = row) x C columns of sums leave for D in slices of
 // 128 bytes per row: through the warp's 4 KiB staging buffer (16-byte chunks
 // swizzled by row & 7), so that eight lanes write one row's 128 bytes.  row0:
 // D's row of lane 0; rows at or past row_end and columns at or past n are
 // not written.
 template <bool F32, int C>
-__device__ __forceinline__ void store_rows(const float (&acc)[C], uint32_t stg, int lane, uint8_t* D, int64_t ldd,
+__device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_t stg, int lane, uint8_t* D, int64_t ldd,
                                            int64_t row0, int64_t row_end, int col0, int n, bool vec) {
     constexpr int W = F32 ? 32 : 64;   // columns per slice
     constexpr int ES = F32 ? 4 : 2;
@@ -115,8 +212,16 @@ __device__ __forceinline__ void store_rows(const float (&acc)[C], uint32_t stg, 
     for (int s = 0; s < C / W; ++s) {
         uint32_t r[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            r[i] = F32 ? __float_as_uint(acc[s * W + i]) : bf16x2(acc[s * W + 2 * i], acc[s * W + 2 * i + 1]);
+        for (int i = 0; i < W / 2; ++i) {
+            float a, b;
+            unpair(acc[s * W / 2 + i], a, b);
+            if constexpr (F32) {
+                r[2 * i] = __float_as_uint(a);
+                r[2 * i + 1] = __float_as_uint(b);
+            } else {
+                r[i] = bf16x2(a, b);
+            }
+        }
         __syncwarp();   // the slice before has been read out
         stage_rows32(stg, lane, r);
         __syncwarp();
@@ -145,8 +250,11 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Arrives on a barrier of a CTA of the cluster, releasing no memory beyond the
+// CTA: for hand-offs whose data is in TMEM (tcgen05.fence orders it).  A
+// release for the cluster waits for the thread's global accesses.
 __device__ __forceinline__ void arrive_in_cluster(uint32_t bar_cluster) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 // TMA load into this CTA's shared memory, completing on a barrier of the pair.
 __device__ __forceinline__ void load_2d_pair(uint32_t dst, const void* desc, int32_t x, int32_t y, uint32_t bar,

@@ -32,7 +32,6 @@ constexpr int kEpiWarps = 8;
 constexpr int kHalfRows = 128;                       // rows of A per CTA
 constexpr int kABytes = kHalfRows * kF8RowBytes;
 constexpr int kEpiBytes = kEpiWarps * 4096;
-constexpr int kScaleBytes = kEpiWarps * 128 * 4;     // column scales of one block, per warp
 constexpr int kPreBytes = (GEMM_F8_MAX_GROUPS + 1) * 4 + 12;
 constexpr int kCtrlBytes = 512;
 
@@ -42,7 +41,8 @@ struct Ring {
     static constexpr int STAGE = kABytes + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 5 : 7;
     static constexpr int BUFS = 512 / BN;            // TMEM accumulators
-    static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + kEpiBytes + kScaleBytes + kPreBytes + kCtrlBytes + 1024;
+    static constexpr int SCALES = 2 * (BN / 2) * 4;  // column scales of two blocks, per epilogue warp
+    static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + kEpiBytes + kEpiWarps * SCALES + kPreBytes + kCtrlBytes + 1024;
 };
 static_assert(Ring<256>::SMEM <= 232448 && Ring<128>::SMEM <= 232448, "shared memory");
 
@@ -108,16 +108,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sB = base + kStages * kABytes;
     const uint32_t sEpi = base + kStages * R::STAGE;
     const uint32_t sScale = sEpi + kEpiBytes;
-    uint8_t* ctrl = smem_raw + (sScale - raw) + kScaleBytes;
+    uint8_t* ctrl = smem_raw + (sScale - raw) + kEpiWarps * R::SCALES;
     int32_t* pre = reinterpret_cast<int32_t*>(ctrl + kCtrlBytes);
     const uint32_t bar0 = smem_u32(ctrl);
     const uint32_t full0 = bar0;                      // used in the even CTA
-    const uint32_t empty0 = full0 + 8u * kStages;
-    const uint32_t accf0 = empty0 + 8u * kStages;
-    const uint32_t acce0 = accf0 + 8u * kBufs;        // used in the even CTA
-    const uint32_t done = acce0 + 8u * kBufs;
-    static_assert(8 * (2 * kStages + 2 * kBufs + 1) + 8 <= kCtrlBytes, "barriers fit");
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kStages + 2 * kBufs + 1));
+    const uint32_t done0 = full0 + 8u * kStages;      // a stage's block is multiplied
+    const uint32_t acce0 = done0 + 8u * kStages;      // used in the even CTA: an accumulator has been read
+    const uint32_t last0 = acce0 + 8u * kBufs;
+    static_assert(8 * (2 * kStages + kBufs + 2) + 8 <= kCtrlBytes, "barriers fit");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kStages + kBufs + 2));
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     pdl_launch_dependents();
@@ -128,14 +127,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full0 + 8u * s, 1);
-            mbar_init(empty0 + 8u * s, 1);
+            mbar_init(full0 + 8u * s, 2);   // the arrivals that announce A's and Bt's bytes
+            mbar_init(done0 + 8u * s, 1);
         }
-        for (int b = 0; b < kBufs; ++b) {
-            mbar_init(accf0 + 8u * b, 1);
-            mbar_init(acce0 + 8u * b, 2 * kEpiWarps);
-        }
-        mbar_init(done, 1);
+        for (int b = 0; b < kBufs; ++b) mbar_init(acce0 + 8u * b, 2 * kEpiWarps);
+        mbar_init(last0, 1);
+        mbar_init(last0 + 8u, 1);
         *abort_flag = 0u;
         fence_barrier_init();
     }
@@ -154,27 +151,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const int units = unit_count(p, pre);
 
-    if (warp == 0) {
-        if (lane == 0) {
+    // the epilogue's running sums need more registers than an even share: 128
+    // threads keep 40 each, 256 take 232, as many as were launched (384 * 168)
+    if (warp < 4) {
+        fewer_registers<40>();
+        if ((warp == 0 || warp == 2) && lane == 0) {
+            // ------------------------------- loads: warp 0 A, warp 2 Bt --
             pdl_wait();
+            const bool isA = warp == 0;
             const uint64_t pol = policy_evict_normal();
+            const uint32_t dst = isA ? sA : sB, step = isA ? kABytes : R::B_BYTES;
+            const void* map = isA ? &tmA : &tmB;
+            const int off = static_cast<int>(rank) * (isA ? kHalfRows : BN / 2);
+            const uint32_t full_leader = peer_address(full0, 0);
+            Turn<kStages> at;
             uint32_t issued = 0;
             bool ok = true;
             for (int u = pair; ok && u < units; u += npairs) {
                 const Unit w = unit_at<BN>(u, p, pre);
-                const int ya = w.arow + static_cast<int>(rank) * kHalfRows;
-                const int yb = w.brow + static_cast<int>(rank) * (BN / 2);
-                for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
-                    const uint32_t s = issued % kStages, ph = (issued / kStages) & 1u;
-                    if (!wait_bounded(empty0 + 8u * s, ph ^ 1u, abort_flag, p.err, kDevErrTimeoutProducer)) {
+                const int y = (isA ? w.arow : w.brow) + off;
+                for (int kb = w.kb_lo; kb < w.kb_hi; ++kb, ++issued) {
+                    // the stage is free once the block that was in it has been multiplied
+                    if (!wait_step(done0 + 8u * at.i, at.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutProducer)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t fb = peer_address(full0 + 8u * s, 0);
-                    if (leader) mbar_arrive_expect_tx(full0 + 8u * s, 2 * R::STAGE);
-                    load_2d_pair(sA + s * kABytes, &tmA, kb * kF8Block, ya, fb, pol);
-                    load_2d_pair(sB + s * R::B_BYTES, &tmB, kb * kF8Block, yb, fb, pol);
-                    ++issued;
+                    if (leader) mbar_arrive_expect_tx(full0 + 8u * at.i, 2 * step);
+                    load_2d_pair(dst + at.i * step, map, kb * kF8Block, y, full_leader + 8u * at.i, pol);
+                    at.next();
                 }
             }
             // after a time-out the copies still in flight land before the pair ends
@@ -182,38 +186,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t j = issued > kStages ? issued - kStages : 0u; j < issued; ++j)
                     wait_bounded(full0 + 8u * (j % kStages), (j / kStages) & 1u, nullptr, p.err, kDevErrTimeoutTeardown);
         }
-    } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            uint32_t n = 0;   // K blocks so far: operand stage and accumulator in turn
+        if ((warp == 1 || warp == 3) && lane == 0 && leader) {
+            // ------------ MMAs: warps 1 and 3 take the K blocks in turn --
+            const uint32_t turn = warp >> 1;
+            Turn<kStages> st;
+            Turn<kBufs> buf;
+            st.i = buf.i = turn;
+            uint32_t skip = turn;   // blocks until this warp's next one
             bool ok = true;
             for (int u = pair; ok && u < units; u += npairs) {
                 const Unit w = unit_at<BN>(u, p, pre);
-                for (int kb = w.kb_lo; kb < w.kb_hi; ++kb, ++n) {
-                    const uint32_t s = n % kStages, b = n % kBufs;
-                    if (!wait_bounded(acce0 + 8u * b, ((n / kBufs) & 1u) ^ 1u, abort_flag, p.err, kDevErrTimeoutMma) ||
-                        !wait_bounded(full0 + 8u * s, (n / kStages) & 1u, abort_flag, p.err, kDevErrTimeoutMma)) {
+                const uint32_t blocks = static_cast<uint32_t>(w.kb_hi - w.kb_lo);
+                uint32_t j = skip;
+                for (; j < blocks; j += 2) {
+                    if (!wait_step(acce0 + 8u * buf.i, buf.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutMma) ||
+                        !wait_step(full0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutMma)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t ad = smem_desc_sw128_kmajor(sA + s * kABytes);
-                    const uint64_t bd = smem_desc_sw128_kmajor(sB + s * R::B_BYTES);
+                    const uint64_t ad = smem_desc_sw128_kmajor(sA + st.i * kABytes);
+                    const uint64_t bd = smem_desc_sw128_kmajor(sB + st.i * R::B_BYTES);
 #pragma unroll
                     for (int kk = 0; kk < kF8Block / kF8MmaK; ++kk)
-                        mma_f8<2>(tmem + b * BN, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0 ? 1u : 0u);
-                    commit_pair(empty0 + 8u * s);
-                    commit_pair(accf0 + 8u * b);
+                        mma_f8<2>(tmem + buf.i * BN, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0 ? 1u : 0u);
+                    commit_pair(done0 + 8u * st.i);
+                    st.next(2);
+                    buf.next(2);
                 }
+                skip = j - blocks;
             }
-            commit_pair(done);
-            wait_bounded(done, 0u, nullptr, p.err, kDevErrTimeoutTeardown);
+            commit_pair(last0 + 8u * turn);
+            wait_bounded(last0 + 8u * turn, 0u, nullptr, p.err, kDevErrTimeoutTeardown);
         }
-    } else if (warp >= 4) {
+    } else {
+        more_registers<232>();
         pdl_wait();
         const int e = warp - 4, q = warp & 3, h = e >> 2;
-        const uint32_t stg = sEpi + e * 4096, scl = sScale + e * 512;
+        const uint32_t stg = sEpi + e * 4096, scl = sScale + e * R::SCALES;
         const uint32_t acce = peer_address(acce0, 0);
-        uint32_t n = 0;
+        Turn<kStages> st;
+        Turn<kBufs> buf;
         bool ok = true;
         for (int u = pair; ok && u < units; u += npairs) {
             const Unit w = unit_at<BN>(u, p, pre);
@@ -225,58 +238,101 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* sb = BROWS ? p.b_scale + (w.brow - w.col) + col
                                     : p.b_scale + static_cast<int64_t>(w.sblock + (BN == 256 ? h : 0)) * p.kb;
             const bool col_in = BROWS || col / kF8Block < p.nb;
-            float acc[kCols];
+            uint64_t acc[kCols / 2];   // pairs of columns
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) acc[j] = 0.f;
-            for (int kb = w.kb_lo; kb < w.kb_hi; ++kb, ++n) {
-                const uint32_t b = n % kBufs;
-                float s = __ldg(sa + static_cast<int64_t>(kb) * p.rows_a);
-                if constexpr (BROWS) {
-                    __syncwarp();   // the block before has been read
+            for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
+            // The scales of four blocks are loaded while the four before are
+            // added: a load takes longer than a block.  Loads past the last
+            // block repeat it.
+            float cur[4], sa_next[4], sb_next[4];
+            const int last = max(w.kb_hi - 1, w.kb_lo);
+            auto load_scales = [&](int kb) {
 #pragma unroll
-                    for (int i = 0; i < kCols / 32; ++i) {
-                        const int c = lane + 32 * i;
-                        const float v = col + c < p.n ? __ldg(sb + static_cast<int64_t>(kb) * p.rows_b + c) : 0.f;
-                        st_shared_u32(scl + 4 * c, __float_as_uint(v));
-                    }
-                    __syncwarp();
-                } else {
-                    s *= col_in ? __ldg(sb + kb) : 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t x = min(kb + i, last);
+                    sa_next[i] = __ldg(sa + x * p.rows_a);
+                    if constexpr (!BROWS) sb_next[i] = col_in ? __ldg(sb + x) : 0.f;
                 }
-                if (!wait_bounded(accf0 + 8u * b, (n / kBufs) & 1u, abort_flag, p.err, kDevErrTimeoutEpilogue)) ok = false;
+            };
+            auto take_scales = [&] {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cur[i] = BROWS ? sa_next[i] : sa_next[i] * sb_next[i];
+            };
+            // column scales: through the warp's shared memory, two blocks deep
+            float sc_next[BROWS ? kCols / 32 : 1];
+            auto load_cols = [&](int kb) {
+                const float* x = sb + static_cast<int64_t>(min(kb, last)) * p.rows_b + lane;
+#pragma unroll
+                for (int i = 0; i < (BROWS ? kCols / 32 : 0); ++i) sc_next[i] = col + lane + 32 * i < p.n ? __ldg(x + 32 * i) : 0.f;
+            };
+            constexpr int kChunks = kCols / 32;
+            const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kCols;
+            // 32 columns are added while the next 32 are on their way, the
+            // first of the next block included
+            uint32_t v[2][32];
+            if (w.kb_lo < w.kb_hi) {
+                load_scales(w.kb_lo);
+                if constexpr (BROWS) load_cols(w.kb_lo);
+                take_scales();
+                load_scales(w.kb_lo + 4);
+                ok = wait_step(done0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutEpilogue);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * BN + h * kCols;
+                tmem_ld_32x32b_x32(t0 + buf.i * BN, v[0]);
+            }
+            int left = w.kb_hi - w.kb_lo;   // blocks
+            for (int i = 0; left > 0; ++i, --left) {
+                const bool more = left > 1;
+                float s = i & 2 ? (i & 1 ? cur[3] : cur[2]) : (i & 1 ? cur[1] : cur[0]);
+                const uint32_t cols = scl + (i & 1) * (kCols * 4);
+                if constexpr (BROWS) {
 #pragma unroll
-                for (int c = 0; c < kCols / 16; ++c) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(t0 + c * 16, v);
-                    tmem_wait_ld();
-                    if constexpr (BROWS) {
+                    for (int x = 0; x < kCols / 32; ++x) st_shared_u32(cols + 4 * (lane + 32 * x), __float_as_uint(sc_next[x]));
+                    __syncwarp();
+                    load_cols(w.kb_lo + i + 1);
+                }
+                if ((i & 3) == 3) {
+                    take_scales();
+                    load_scales(w.kb_lo + i + 5);
+                }
+                const uint64_t s2 = pair_of(__float_as_uint(s), __float_as_uint(s));
+                const uint32_t tb = t0 + buf.i * BN, free_bar = acce + 8u * buf.i;
+                st.next();
+                buf.next();
+                bool ready = true;
+                wait_tmem(v[0]);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const uint4 x = ld_shared_v4(scl + (c * 16 + j) * 4);
-                            acc[c * 16 + j] = fmaf(__uint_as_float(v[j]) * s, __uint_as_float(x.x), acc[c * 16 + j]);
-                            acc[c * 16 + j + 1] = fmaf(__uint_as_float(v[j + 1]) * s, __uint_as_float(x.y), acc[c * 16 + j + 1]);
-                            acc[c * 16 + j + 2] = fmaf(__uint_as_float(v[j + 2]) * s, __uint_as_float(x.z), acc[c * 16 + j + 2]);
-                            acc[c * 16 + j + 3] = fmaf(__uint_as_float(v[j + 3]) * s, __uint_as_float(x.w), acc[c * 16 + j + 3]);
-                        }
+                for (int c = 0; c < kChunks; ++c) {
+                    if (c + 1 < kChunks) {
+                        tmem_ld_32x32b_x32(tb + (c + 1) * 32, v[(c + 1) & 1]);
+                        if (c + 2 == kChunks && more) ready = mbar_try_wait(done0 + 8u * st.i, st.ph);   // asked early
+                        add_scaled<BROWS>(acc + c * 16, v[c & 1], s2, cols + c * 128);
+                        wait_tmem(v[(c + 1) & 1]);
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fmaf(__uint_as_float(v[j]), s, acc[c * 16 + j]);
+                        // all columns are in registers: the accumulator is free
+                        tc_fence_before();
+                        if (lane == 0) arrive_in_cluster(free_bar);
+                        if (more) {
+                            if (!__all_sync(0xffffffffu, ready)) {
+                                ok = wait_step(done0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutEpilogue);
+                                ok = __all_sync(0xffffffffu, ok);
+                                if (!ok) break;
+                            }
+                            tc_fence_after();
+                            tmem_ld_32x32b_x32(t0 + buf.i * BN, v[0]);
+                        }
+                        add_scaled<BROWS>(acc + c * 16, v[c & 1], s2, cols + c * 128);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_in_cluster(acce + 8u * b);
+                if (!ok) break;
             }
             if (!ok) break;
             if (p.out_f32)
-                store_rows<true>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
+                store_rows<true, kCols>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
                                  p.d_vec != 0);
             else
-                store_rows<false>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
+                store_rows<false, kCols>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
                                   p.d_vec != 0);
         }
     }
