@@ -26,14 +26,44 @@ struct F8Params {
     int pieces;           // row tiles that all groups together can have (GEMM_GROUP_ROWS)
 };
 
-// wait_bounded() for waits of every K block: the clock it bounds itself with
-// is slow to read, so it is asked only after some probes.
+// wait_bounded() for a whole converged warp: all lanes probe, and the branches
+// are uniform (a ready barrier costs about 30 cycles; with a loop that each
+// lane leaves by itself it measured 170).  The clock that bounds the wait is
+// slow to read, so it is asked only after some probes.
 constexpr int kWaitProbes = 256;
-__device__ __forceinline__ bool wait_step(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int* err_word,
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag, int* err_word,
                                           int code) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+#pragma unroll 1
     for (int i = 0; i < kWaitProbes; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    return wait_bounded(bar, parity, abort_flag, err_word, code);
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, err_word, code));
+}
+
+// Both barriers at once: one round trip instead of two.
+__device__ __forceinline__ bool wait_warp_both(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1,
+                                               volatile uint32_t* abort_flag, int* err_word, int code) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "and.pred p, p, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar0), "r"(parity0), "r"(bar1), "r"(parity1)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok != 0)) return true;
+    return wait_warp(bar0, parity0, abort_flag, err_word, code) && wait_warp(bar1, parity1, abort_flag, err_word, code);
+}
+
+// One lane of a converged warp.  The loading and MMA warps run their loops
+// whole, so that addresses and descriptors stay in uniform registers, and
+// this lane issues (measured for one MMA issuer, see gemm_f8_tc2.cu).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // A place in a ring of N and the parity of the round, stepped without division.
@@ -179,12 +209,12 @@ __device__ __forceinline__ void copy4_async(uint32_t dst, const float* src, bool
                  "r"(in ? 4 : 0)
                  : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits until at most N of this thread's groups of copies are on their way.
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// One arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+// Waits for them (before the CTA ends).
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
 
 // Registers of the calling warpgroup (all four warps call it).
@@ -198,19 +228,20 @@ __device__ __forceinline__ void more_registers() {
 }
 
 // A warp's 32 rows (lane = row) x C columns of sums leave for D in slices of
-// 128 bytes per row: through the warp's 4 KiB staging buffer (16-byte chunks
-// swizzled by row & 7), so that eight lanes write one row's 128 bytes.  row0:
-// D's row of lane 0; rows at or past row_end and columns at or past n are
-// not written.
+// 64 bytes per row: through the warp's 2 KiB staging buffer (16-byte chunks
+// swizzled by row >> 1, free of bank conflicts both ways), so that four lanes
+// write one row's 64 bytes.  row0: D's row of lane 0; rows at or past row_end
+// and columns at or past n are not written.
+constexpr int kStageRowsBytes = 32 * 64;
 template <bool F32, int C>
 __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_t stg, int lane, uint8_t* D, int64_t ldd,
                                            int64_t row0, int64_t row_end, int col0, int n, bool vec) {
-    constexpr int W = F32 ? 32 : 64;   // columns per slice
+    constexpr int W = F32 ? 16 : 32;   // columns per slice
     constexpr int ES = F32 ? 4 : 2;
     static_assert(C % W == 0, "whole slices");
 #pragma unroll
     for (int s = 0; s < C / W; ++s) {
-        uint32_t r[32];
+        uint32_t r[16];
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
             float a, b;
@@ -223,13 +254,15 @@ __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_
             }
         }
         __syncwarp();   // the slice before has been read out
-        stage_rows32(stg, lane, r);
-        __syncwarp();
-        const int c = col0 + s * W + (lane & 7) * (16 / ES);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int rr = j * 4 + (lane >> 3);
-            const uint4 v = ld_shared_v4(stg + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+        for (int i = 0; i < 4; ++i)
+            st_shared_v4(stg + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        __syncwarp();
+        const int c = col0 + s * W + (lane & 3) * (16 / ES);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int rr = j * 8 + (lane >> 2);
+            const uint4 v = ld_shared_v4(stg + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
             if (row0 + rr < row_end && c < n)
                 store_d16<F32>(D + ((row0 + rr) * ldd + c) * ES, n - c, vec, v);
         }

@@ -27,24 +27,32 @@ namespace gemm {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
 constexpr int kHalfRows = 128;                       // rows of A per CTA
 constexpr int kABytes = kHalfRows * kF8RowBytes;
-constexpr int kEpiBytes = kEpiWarps * 4096;
 constexpr int kPreBytes = (GEMM_F8_MAX_GROUPS + 1) * 4 + 12;
 constexpr int kCtrlBytes = 512;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 
-template <int BN>
-struct Ring {
+template <int BN, bool BROWS>
+struct Config {
+    static constexpr int COLS = BN / 2;                      // columns of D per epilogue thread
     static constexpr int B_BYTES = BN / 2 * kF8RowBytes;
     static constexpr int STAGE = kABytes + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 5 : 7;
-    static constexpr int BUFS = 512 / BN;            // TMEM accumulators
-    static constexpr int SCALES = 2 * (BN / 2) * 4;  // column scales of two blocks, per epilogue warp
-    static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + kEpiBytes + kEpiWarps * SCALES + kPreBytes + kCtrlBytes + 1024;
+    static constexpr int BUFS = 512 / BN;                    // TMEM accumulators
+    // Blocks whose scales are in shared memory.  Block i's are copied once
+    // block i - AHEAD is multiplied: its accumulator was free then, so the
+    // block BUFS before it was read and the one before that added.  AHEAD is
+    // small enough that the barrier it looks at cannot be a round further:
+    // block i - 1 + BUFS is the last that can be multiplied without i's scales.
+    static constexpr int AHEAD = STAGES - BUFS;
+    static constexpr int SLOTS = AHEAD + BUFS + 1;
+    static constexpr int SLOT = kHalfRows * 4 + (BROWS ? BN * 4 : 16);
+    static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + kEpiWarps * kStageRowsBytes + SLOTS * SLOT +
+                                   kPreBytes + kCtrlBytes + 1024;
+    static_assert(SMEM <= 232448, "shared memory");
 };
-static_assert(Ring<256>::SMEM <= 232448 && Ring<128>::SMEM <= 232448, "shared memory");
 
 struct Unit {
     int arow;      // first row of A of the pair's tile
@@ -98,25 +106,26 @@ template <int BN, bool BROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     f8_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Params p,
                   const uint32_t idesc) {
-    using R = Ring<BN>;
+    using R = Config<BN, BROWS>;
     constexpr int kStages = R::STAGES, kBufs = R::BUFS;
-    constexpr int kCols = BN / 2;   // columns per epilogue thread
+    constexpr int kSlots = R::SLOTS, kCols = R::COLS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t sA = base;
     const uint32_t sB = base + kStages * kABytes;
     const uint32_t sEpi = base + kStages * R::STAGE;
-    const uint32_t sScale = sEpi + kEpiBytes;
-    uint8_t* ctrl = smem_raw + (sScale - raw) + kEpiWarps * R::SCALES;
+    const uint32_t sScale = sEpi + kEpiWarps * kStageRowsBytes;
+    uint8_t* ctrl = smem_raw + (sScale - raw) + kSlots * R::SLOT;
     int32_t* pre = reinterpret_cast<int32_t*>(ctrl + kCtrlBytes);
     const uint32_t bar0 = smem_u32(ctrl);
     const uint32_t full0 = bar0;                      // used in the even CTA
     const uint32_t done0 = full0 + 8u * kStages;      // a stage's block is multiplied
     const uint32_t acce0 = done0 + 8u * kStages;      // used in the even CTA: an accumulator has been read
-    const uint32_t last0 = acce0 + 8u * kBufs;
-    static_assert(8 * (2 * kStages + kBufs + 2) + 8 <= kCtrlBytes, "barriers fit");
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kStages + kBufs + 2));
+    const uint32_t scale0 = acce0 + 8u * kBufs;       // a block's scales have landed
+    const uint32_t last0 = scale0 + 8u * kSlots;
+    static_assert(8 * (2 * kStages + kBufs + kSlots + 2) + 8 <= kCtrlBytes, "barriers fit");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kStages + kBufs + kSlots + 2));
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     pdl_launch_dependents();
@@ -127,10 +136,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(full0 + 8u * s, 2);   // the arrivals that announce A's and Bt's bytes
+            mbar_init(full0 + 8u * s, 1);
             mbar_init(done0 + 8u * s, 1);
         }
         for (int b = 0; b < kBufs; ++b) mbar_init(acce0 + 8u * b, 2 * kEpiWarps);
+        for (int s = 0; s < kSlots; ++s) mbar_init(scale0 + 8u * s, 32);
         mbar_init(last0, 1);
         mbar_init(last0 + 8u, 1);
         *abort_flag = 0u;
@@ -151,33 +161,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const int units = unit_count(p, pre);
 
-    // the epilogue's running sums need more registers than an even share: 128
-    // threads keep 40 each, 256 take 232, as many as were launched (384 * 168)
+    // the epilogue's running sums need more registers than an even share: of
+    // 384 threads with 168, 128 keep 40 each and 256 take 232
     if (warp < 4) {
         fewer_registers<40>();
-        if ((warp == 0 || warp == 2) && lane == 0) {
-            // ------------------------------- loads: warp 0 A, warp 2 Bt --
+        if (warp == 0) {
+            // ------------------------------------------------ operand loads --
             pdl_wait();
-            const bool isA = warp == 0;
             const uint64_t pol = policy_evict_normal();
-            const uint32_t dst = isA ? sA : sB, step = isA ? kABytes : R::B_BYTES;
-            const void* map = isA ? &tmA : &tmB;
-            const int off = static_cast<int>(rank) * (isA ? kHalfRows : BN / 2);
             const uint32_t full_leader = peer_address(full0, 0);
             Turn<kStages> at;
             uint32_t issued = 0;
             bool ok = true;
             for (int u = pair; ok && u < units; u += npairs) {
                 const Unit w = unit_at<BN>(u, p, pre);
-                const int y = (isA ? w.arow : w.brow) + off;
+                const int ya = w.arow + static_cast<int>(rank) * kHalfRows;
+                const int yb = w.brow + static_cast<int>(rank) * (BN / 2);
                 for (int kb = w.kb_lo; kb < w.kb_hi; ++kb, ++issued) {
                     // the stage is free once the block that was in it has been multiplied
-                    if (!wait_step(done0 + 8u * at.i, at.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutProducer)) {
+                    if (!wait_warp(done0 + 8u * at.i, at.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutProducer)) {
                         ok = false;
                         break;
                     }
-                    if (leader) mbar_arrive_expect_tx(full0 + 8u * at.i, 2 * step);
-                    load_2d_pair(dst + at.i * step, map, kb * kF8Block, y, full_leader + 8u * at.i, pol);
+                    if (elect_one()) {
+                        const uint32_t fb = full_leader + 8u * at.i;
+                        if (leader) mbar_arrive_expect_tx(full0 + 8u * at.i, 2 * R::STAGE);
+                        load_2d_pair(sA + at.i * kABytes, &tmA, kb * kF8Block, ya, fb, pol);
+                        load_2d_pair(sB + at.i * R::B_BYTES, &tmB, kb * kF8Block, yb, fb, pol);
+                    }
+                    __syncwarp();
                     at.next();
                 }
             }
@@ -186,7 +198,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t j = issued > kStages ? issued - kStages : 0u; j < issued; ++j)
                     wait_bounded(full0 + 8u * (j % kStages), (j / kStages) & 1u, nullptr, p.err, kDevErrTimeoutTeardown);
         }
-        if ((warp == 1 || warp == 3) && lane == 0 && leader) {
+        if (warp == 2) {
+            // -------------------------------------------------------- scales --
+            // The CTA's 128 row scales of each block, and the block scales of
+            // the tile's column blocks (or its columns' scales).
+            pdl_wait();
+            Turn<kStages> at;   // block i - AHEAD, from i = AHEAD on
+            Turn<kSlots> slot;
+            uint32_t n = 0;
+            bool ok = true;
+            for (int u = pair; ok && u < units; u += npairs) {
+                const Unit w = unit_at<BN>(u, p, pre);
+                const int row0 = w.arow + static_cast<int>(rank) * kHalfRows + lane;
+                const float* sa = p.a_scale + static_cast<int64_t>(w.kb_lo) * p.rows_a;
+                const float* sb = BROWS ? p.b_scale + static_cast<int64_t>(w.kb_lo) * p.rows_b + w.brow + lane
+                                        : p.b_scale + static_cast<int64_t>(w.sblock + (lane & 1)) * p.kb + w.kb_lo;
+                const bool sb_in = w.col / kF8Block + (lane & 1) < p.nb;
+                for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
+                    if (n >= R::AHEAD) {
+                        if (!wait_warp(done0 + 8u * at.i, at.ph, abort_flag, p.err, kDevErrTimeoutProducer)) {
+                            ok = false;
+                            break;
+                        }
+                        at.next();
+                    }
+                    ++n;
+                    const uint32_t dst = sScale + slot.i * R::SLOT + 4 * lane;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = row0 + 32 * i < p.rows_a;
+                        copy4_async(dst + 128 * i, in ? sa + row0 + 32 * i : p.a_scale, in);
+                    }
+                    if constexpr (BROWS) {
+#pragma unroll
+                        for (int i = 0; i < BN / 32; ++i) {
+                            const bool in = w.col + lane + 32 * i < p.n;
+                            copy4_async(dst + 512 + 128 * i, in ? sb + 32 * i : p.b_scale, in);
+                        }
+                        sb += p.rows_b;
+                    } else {
+                        if (lane < 2) copy4_async(dst + 512, sb_in ? sb : p.b_scale, sb_in);
+                        sb += 1;
+                    }
+                    sa += p.rows_a;
+                    copies_arrive(scale0 + 8u * slot.i);
+                    slot.next();
+                }
+            }
+            copies_wait_all();
+        }
+        if ((warp == 1 || warp == 3) && leader) {
             // ------------ MMAs: warps 1 and 3 take the K blocks in turn --
             const uint32_t turn = warp >> 1;
             Turn<kStages> st;
@@ -199,133 +260,95 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t blocks = static_cast<uint32_t>(w.kb_hi - w.kb_lo);
                 uint32_t j = skip;
                 for (; j < blocks; j += 2) {
-                    if (!wait_step(acce0 + 8u * buf.i, buf.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutMma) ||
-                        !wait_step(full0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutMma)) {
+                    if (!wait_warp(acce0 + 8u * buf.i, buf.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutMma) ||
+                        !wait_warp(full0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutMma)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t ad = smem_desc_sw128_kmajor(sA + st.i * kABytes);
                     const uint64_t bd = smem_desc_sw128_kmajor(sB + st.i * R::B_BYTES);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kF8Block / kF8MmaK; ++kk)
-                        mma_f8<2>(tmem + buf.i * BN, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0 ? 1u : 0u);
-                    commit_pair(done0 + 8u * st.i);
+                        for (int kk = 0; kk < kF8Block / kF8MmaK; ++kk)
+                            mma_f8<2>(tmem + buf.i * BN, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0 ? 1u : 0u);
+                        commit_pair(done0 + 8u * st.i);
+                    }
+                    __syncwarp();
                     st.next(2);
                     buf.next(2);
                 }
                 skip = j - blocks;
             }
-            commit_pair(last0 + 8u * turn);
+            if (elect_one()) commit_pair(last0 + 8u * turn);
+            __syncwarp();
             wait_bounded(last0 + 8u * turn, 0u, nullptr, p.err, kDevErrTimeoutTeardown);
         }
     } else {
+        // ------------------------------------------- scale, add and store --
         more_registers<232>();
         pdl_wait();
         const int e = warp - 4, q = warp & 3, h = e >> 2;
-        const uint32_t stg = sEpi + e * 4096, scl = sScale + e * R::SCALES;
+        const uint32_t stg = sEpi + e * kStageRowsBytes;
         const uint32_t acce = peer_address(acce0, 0);
+        const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kCols;
+        const uint32_t row_scale = sScale + 4 * (q * 32 + lane);
+        const uint32_t col_scale = sScale + 512 + (BROWS ? h * kCols * 4 : (h * kCols / kF8Block) * 4);
         Turn<kStages> st;
         Turn<kBufs> buf;
+        Turn<kSlots> slot;
         bool ok = true;
         for (int u = pair; ok && u < units; u += npairs) {
             const Unit w = unit_at<BN>(u, p, pre);
             const int in_tile = static_cast<int>(rank) * kHalfRows + q * 32;   // the warp's first row
-            const int arow = min(w.arow + in_tile + lane, static_cast<int>(p.rows_a) - 1);
             const int col = w.col + h * kCols;
-            const float* sa = p.a_scale + arow;
-            // column scales: one per block of 128 columns, or one per column
-            const float* sb = BROWS ? p.b_scale + (w.brow - w.col) + col
-                                    : p.b_scale + static_cast<int64_t>(w.sblock + (BN == 256 ? h : 0)) * p.kb;
-            const bool col_in = BROWS || col / kF8Block < p.nb;
             uint64_t acc[kCols / 2];   // pairs of columns
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
-            // The scales of four blocks are loaded while the four before are
-            // added: a load takes longer than a block.  Loads past the last
-            // block repeat it.
-            float cur[4], sa_next[4], sb_next[4];
-            const int last = max(w.kb_hi - 1, w.kb_lo);
-            auto load_scales = [&](int kb) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t x = min(kb + i, last);
-                    sa_next[i] = __ldg(sa + x * p.rows_a);
-                    if constexpr (!BROWS) sb_next[i] = col_in ? __ldg(sb + x) : 0.f;
-                }
-            };
-            auto take_scales = [&] {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) cur[i] = BROWS ? sa_next[i] : sa_next[i] * sb_next[i];
-            };
-            // column scales: through the warp's shared memory, two blocks deep
-            float sc_next[BROWS ? kCols / 32 : 1];
-            auto load_cols = [&](int kb) {
-                const float* x = sb + static_cast<int64_t>(min(kb, last)) * p.rows_b + lane;
-#pragma unroll
-                for (int i = 0; i < (BROWS ? kCols / 32 : 0); ++i) sc_next[i] = col + lane + 32 * i < p.n ? __ldg(x + 32 * i) : 0.f;
-            };
             constexpr int kChunks = kCols / 32;
-            const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kCols;
             // 32 columns are added while the next 32 are on their way, the
-            // first of the next block included
+            // first of the next block included.  Order matters: what goes
+            // through the shared-memory queue behind a TMEM load waits for it.
             uint32_t v[2][32];
-            if (w.kb_lo < w.kb_hi) {
-                load_scales(w.kb_lo);
-                if constexpr (BROWS) load_cols(w.kb_lo);
-                take_scales();
-                load_scales(w.kb_lo + 4);
-                ok = wait_step(done0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutEpilogue);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+            float sa = 0.f, sb = 1.f;
+            uint32_t cols = 0;
+            auto first_columns = [&] {   // of the block that st, buf and slot point to
                 tc_fence_after();
+                cols = col_scale + slot.i * R::SLOT;
+                sa = ld_shared_f32(row_scale + slot.i * R::SLOT);
+                if constexpr (!BROWS) sb = ld_shared_f32(cols);
                 tmem_ld_32x32b_x32(t0 + buf.i * BN, v[0]);
+            };
+            if (w.kb_lo < w.kb_hi) {
+                ok = wait_warp_both(done0 + 8u * st.i, st.ph, scale0 + 8u * slot.i, slot.ph, abort_flag, p.err,
+                                    kDevErrTimeoutEpilogue);
+                if (!ok) break;
+                first_columns();
             }
-            int left = w.kb_hi - w.kb_lo;   // blocks
-            for (int i = 0; left > 0; ++i, --left) {
-                const bool more = left > 1;
-                float s = i & 2 ? (i & 1 ? cur[3] : cur[2]) : (i & 1 ? cur[1] : cur[0]);
-                const uint32_t cols = scl + (i & 1) * (kCols * 4);
-                if constexpr (BROWS) {
-#pragma unroll
-                    for (int x = 0; x < kCols / 32; ++x) st_shared_u32(cols + 4 * (lane + 32 * x), __float_as_uint(sc_next[x]));
-                    __syncwarp();
-                    load_cols(w.kb_lo + i + 1);
-                }
-                if ((i & 3) == 3) {
-                    take_scales();
-                    load_scales(w.kb_lo + i + 5);
-                }
-                const uint64_t s2 = pair_of(__float_as_uint(s), __float_as_uint(s));
-                const uint32_t tb = t0 + buf.i * BN, free_bar = acce + 8u * buf.i;
+            for (int left = w.kb_hi - w.kb_lo; left > 0; --left) {
+                const uint32_t tb = t0 + buf.i * BN, free_bar = acce + 8u * buf.i, cols_now = cols;
                 st.next();
                 buf.next();
-                bool ready = true;
+                slot.next();
                 wait_tmem(v[0]);
+                const float s = BROWS ? sa : sa * sb;
+                const uint64_t s2 = pair_of(__float_as_uint(s), __float_as_uint(s));
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    if (c + 1 < kChunks) {
-                        tmem_ld_32x32b_x32(tb + (c + 1) * 32, v[(c + 1) & 1]);
-                        if (c + 2 == kChunks && more) ready = mbar_try_wait(done0 + 8u * st.i, st.ph);   // asked early
-                        add_scaled<BROWS>(acc + c * 16, v[c & 1], s2, cols + c * 128);
-                        wait_tmem(v[(c + 1) & 1]);
-                    } else {
-                        // all columns are in registers: the accumulator is free
-                        tc_fence_before();
-                        if (lane == 0) arrive_in_cluster(free_bar);
-                        if (more) {
-                            if (!__all_sync(0xffffffffu, ready)) {
-                                ok = wait_step(done0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutEpilogue);
-                                ok = __all_sync(0xffffffffu, ok);
-                                if (!ok) break;
-                            }
-                            tc_fence_after();
-                            tmem_ld_32x32b_x32(t0 + buf.i * BN, v[0]);
-                        }
-                        add_scaled<BROWS>(acc + c * 16, v[c & 1], s2, cols + c * 128);
-                    }
+                for (int c = 0; c + 1 < kChunks; ++c) {
+                    tmem_ld_32x32b_x32(tb + (c + 1) * 32, v[(c + 1) & 1]);
+                    add_scaled<BROWS>(acc + c * 16, v[c & 1], s2, cols_now + c * 128);
+                    wait_tmem(v[(c + 1) & 1]);
                 }
-                if (!ok) break;
+                // all columns are in registers: the accumulator is free
+                tc_fence_before();
+                if (lane == 0) arrive_in_cluster(free_bar);
+                if (left > 1) {
+                    ok = wait_warp_both(done0 + 8u * st.i, st.ph, scale0 + 8u * slot.i, slot.ph, abort_flag, p.err,
+                                    kDevErrTimeoutEpilogue);
+                    if (!ok) break;
+                    first_columns();
+                }
+                add_scaled<BROWS>(acc + (kChunks - 1) * 16, v[(kChunks - 1) & 1], s2, cols_now + (kChunks - 1) * 128);
             }
             if (!ok) break;
             if (p.out_f32)
@@ -349,7 +372,7 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 
 template <int BN, bool BROWS>
 cudaError_t launch(const F8Launch& a, cudaStream_t stream) {
-    using R = Ring<BN>;
+    using R = Config<BN, BROWS>;
     CUtensorMap mA, mB;
     if (!encode_f8(&mA, a.A, a.k, a.rows_a, a.lda, kHalfRows) || !encode_f8(&mB, a.Bt, a.k, a.rows_b, a.ldb, BN / 2))
         return cudaErrorInvalidValue;
