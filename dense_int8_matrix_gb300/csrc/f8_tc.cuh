@@ -162,6 +162,13 @@ __device__ __forceinline__ void wait_tmem(uint32_t (&r)[32]) {
                    "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                    "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
+__device__ __forceinline__ void wait_tmem(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void load_tmem(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(taddr, r); }
+__device__ __forceinline__ void load_tmem(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(taddr, r); }
 
 // Two fp32 values in one 64-bit register pair, and a * b + c on both.
 __device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
@@ -186,20 +193,19 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// Adds 32 columns of a block's sums, scaled, to the running sums: by s, or by
-// s and the column scales at shared address `cols`.
-template <bool COLS>
-__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[32], uint64_t s, uint32_t cols) {
+// Adds N columns of a block's sums to the running sums: times s, or times s
+// and the columns' scales c.
+template <int N>
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[N], uint64_t s) {
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-        uint64_t x0 = s, x1 = s;
-        if constexpr (COLS) {
-            const uint4 c = ld_shared_v4(cols + 8 * j);
-            x0 = mul2(s, pair_of(c.x, c.y));
-            x1 = mul2(s, pair_of(c.z, c.w));
-        }
-        acc[j] = fma2(pair_of(v[2 * j], v[2 * j + 1]), x0, acc[j]);
-        acc[j + 1] = fma2(pair_of(v[2 * j + 2], v[2 * j + 3]), x1, acc[j + 1]);
+    for (int j = 0; j < N / 2; ++j) acc[j] = fma2(pair_of(v[2 * j], v[2 * j + 1]), s, acc[j]);
+}
+template <int N>
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[N], uint64_t s, const uint4 (&c)[N / 4]) {
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) {
+        acc[2 * j] = fma2(pair_of(v[4 * j], v[4 * j + 1]), mul2(s, pair_of(c[j].x, c[j].y)), acc[2 * j]);
+        acc[2 * j + 1] = fma2(pair_of(v[4 * j + 2], v[4 * j + 3]), mul2(s, pair_of(c[j].z, c[j].w)), acc[2 * j + 1]);
     }
 }
 

@@ -305,28 +305,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t acc[kCols / 2];   // pairs of columns
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
-            constexpr int kChunks = kCols / 32;
-            // 32 columns are added while the next 32 are on their way, the
-            // first of the next block included.  Order matters: what goes
-            // through the shared-memory queue behind a TMEM load waits for it.
-            uint32_t v[2][32];
+            // One chunk of columns is added while the next is on its way, the
+            // first of the next block included.  With column scales the chunk
+            // is half as wide, for the registers that hold them.  Order
+            // matters: what goes through the shared-memory queue behind a TMEM
+            // load waits for it, so scales are asked for first.
+            constexpr int kChunk = BROWS ? 16 : 32;
+            constexpr int kChunks = kCols / kChunk;
+            uint32_t v[2][kChunk];
+            uint4 sc[2][kChunk / 4];
             float sa = 0.f, sb = 1.f;
-            uint32_t cols = 0;
-            auto first_columns = [&] {   // of the block that st, buf and slot point to
+            auto chunk = [&](int c, uint32_t cols, uint32_t taddr) {
+                if constexpr (BROWS)
+#pragma unroll
+                    for (int i = 0; i < kChunk / 4; ++i) sc[c & 1][i] = ld_shared_v4(cols + (c * kChunk + 4 * i) * 4);
+                load_tmem(taddr + c * kChunk, v[c & 1]);
+            };
+            auto add = [&](int c, uint64_t s2) {
+                if constexpr (BROWS)
+                    add_scaled<kChunk>(acc + c * (kChunk / 2), v[c & 1], s2, sc[c & 1]);
+                else
+                    add_scaled<kChunk>(acc + c * (kChunk / 2), v[c & 1], s2);
+            };
+            auto first_chunk = [&] {   // of the block that st, buf and slot point to
                 tc_fence_after();
-                cols = col_scale + slot.i * R::SLOT;
+                const uint32_t cols = col_scale + slot.i * R::SLOT;
                 sa = ld_shared_f32(row_scale + slot.i * R::SLOT);
                 if constexpr (!BROWS) sb = ld_shared_f32(cols);
-                tmem_ld_32x32b_x32(t0 + buf.i * BN, v[0]);
+                chunk(0, cols, t0 + buf.i * BN);
             };
             if (w.kb_lo < w.kb_hi) {
                 ok = wait_warp_both(done0 + 8u * st.i, st.ph, scale0 + 8u * slot.i, slot.ph, abort_flag, p.err,
                                     kDevErrTimeoutEpilogue);
                 if (!ok) break;
-                first_columns();
+                first_chunk();
             }
             for (int left = w.kb_hi - w.kb_lo; left > 0; --left) {
-                const uint32_t tb = t0 + buf.i * BN, free_bar = acce + 8u * buf.i, cols_now = cols;
+                const uint32_t tb = t0 + buf.i * BN, free_bar = acce + 8u * buf.i, cols = col_scale + slot.i * R::SLOT;
                 st.next();
                 buf.next();
                 slot.next();
@@ -335,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t s2 = pair_of(__float_as_uint(s), __float_as_uint(s));
 #pragma unroll
                 for (int c = 0; c + 1 < kChunks; ++c) {
-                    tmem_ld_32x32b_x32(tb + (c + 1) * 32, v[(c + 1) & 1]);
-                    add_scaled<BROWS>(acc + c * 16, v[c & 1], s2, cols_now + c * 128);
+                    chunk(c + 1, cols, tb);
+                    add(c, s2);
                     wait_tmem(v[(c + 1) & 1]);
                 }
                 // all columns are in registers: the accumulator is free
@@ -344,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) arrive_in_cluster(free_bar);
                 if (left > 1) {
                     ok = wait_warp_both(done0 + 8u * st.i, st.ph, scale0 + 8u * slot.i, slot.ph, abort_flag, p.err,
-                                    kDevErrTimeoutEpilogue);
+                                        kDevErrTimeoutEpilogue);
                     if (!ok) break;
-                    first_columns();
+                    first_chunk();
                 }
-                add_scaled<BROWS>(acc + (kChunks - 1) * 16, v[(kChunks - 1) & 1], s2, cols_now + (kChunks - 1) * 128);
+                add(kChunks - 1, s2);
             }
             if (!ok) break;
             if (p.out_f32)
