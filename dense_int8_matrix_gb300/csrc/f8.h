@@ -30,9 +30,10 @@ struct F8Launch {
     int num_sms, pairs;
 };
 
-cudaError_t launch_f8_simple(const F8Launch& a, cudaStream_t stream);
 // Two-SM tiles of 256 x bn (gemm_f8_tc2.cu).
 cudaError_t launch_f8_tc2(const F8Launch& a, cudaStream_t stream);
+// Tiles of bm (16, 32, 64, 128) rows x 128 columns of D, split_k CTAs each (gemm_f8_skinny.cu).
+cudaError_t launch_f8_skinny(const F8Launch& a, cudaStream_t stream);
 
 // ---- quantisation (quantize.cu) ----------------------------------------------
 struct F8Quant {

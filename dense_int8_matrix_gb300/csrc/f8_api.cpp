@@ -30,6 +30,35 @@ gemm_status check_f8_shape(int32_t mode, int32_t groups, int64_t m, int64_t k, i
     return GEMM_OK;
 }
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The tile and split of a product from its sizes.
+void choose_config(gemm_plan_f8* p) {
+    const int64_t kb = ceil_div(p->k, kF8Block);
+    const bool by_rows = p->group_mode == GEMM_GROUP_ROWS;
+    const int64_t rows = by_rows ? ceil_div(p->m, p->groups) : p->m;   // of a group, on average
+    if (rows <= 128) {
+        // few rows: stream Bt through tiles of 128 of its rows
+        p->path = GEMM_PATH_SKINNY;
+        p->bm = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+        p->bn = 128;
+        const int64_t groups = by_rows ? (p->m < p->groups ? p->m : p->groups) : p->group_mode == GEMM_GROUP_K ? p->groups : 1;
+        const int64_t tiles = groups * ceil_div(rows, p->bm) * ceil_div(p->n, 128);
+        const int64_t room = (p->bm == 128 ? 1 : 2) * static_cast<int64_t>(p->num_sms);
+        int s = 1;
+        while (s < 8 && tiles * s * 2 <= room && kb / (s * 2) >= 4) s *= 2;
+        p->split_k = s;
+        return;
+    }
+    p->path = GEMM_PATH_TENSOR;
+    p->bm = 256;
+    p->split_k = 1;
+    const int64_t pairs = p->num_sms / 2 > 0 ? p->num_sms / 2 : 1;
+    const int64_t tm = (by_rows ? p->groups : 1) * ceil_div(rows, 256) * (p->group_mode == GEMM_GROUP_K ? p->groups : 1);
+    const int64_t w256 = ceil_div(tm * ceil_div(p->n, 256), pairs), w128 = ceil_div(tm * ceil_div(p->n, 128), pairs);
+    p->bn = 3 * w256 <= 2 * w128 ? 256 : 128;   // a 128-column tile takes two thirds of a 256-column one
+}
+
 gemm_status make_f8_plan(int32_t mode, int32_t groups, int64_t m, int64_t k, int64_t n, int32_t a_type, int32_t b_type,
                          int32_t b_scale, int32_t num_sms, gemm_plan_f8* out) {
     if (!out || num_sms < 1) return GEMM_ERR_INVALID_ARG;
@@ -46,9 +75,7 @@ gemm_status make_f8_plan(int32_t mode, int32_t groups, int64_t m, int64_t k, int
     out->a_type = a_type;
     out->b_type = b_type;
     out->b_scale = b_scale;
-    out->path = GEMM_PATH_TENSOR;
-    out->bm = out->bn = 256;
-    out->split_k = 1;
+    choose_config(out);
     return GEMM_OK;
 }
 
@@ -119,7 +146,7 @@ gemm_status run_f8(const gemm_plan_f8* p, const uint8_t* A, int64_t lda, const f
     const int kind = p->path == GEMM_PATH_SKINNY ? GEMM_KERNEL_SKINNY : GEMM_KERNEL_TC;
     const bool sampled = trace_begin_call();
     void* unit = trace_unit_begin(kind, stream, sampled);
-    const cudaError_t e = p->path == GEMM_PATH_SKINNY ? launch_f8_simple(L, stream) : launch_f8_tc2(L, stream);
+    const cudaError_t e = p->path == GEMM_PATH_SKINNY ? launch_f8_skinny(L, stream) : launch_f8_tc2(L, stream);
     trace_unit_end(unit, stream);
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     trace_launch(kind);
