@@ -361,33 +361,46 @@ def gemm_f8_padded_k(rows: int, groups: int = 1) -> int:
     return load().gemm_f8_padded_k(rows, groups)
 
 
+_f8_types = None   # torch's dtype of each GEMM_F8_* value
+
+
 def _f8_dtype(f8_type):
-    import torch
-    return torch.float8_e4m3fn if f8_type == GEMM_F8_E4M3 else torch.float8_e5m2
+    global _f8_types
+    if _f8_types is None:
+        import torch
+        _f8_types = (torch.float8_e4m3fn, torch.float8_e5m2)
+    return _f8_types[f8_type]
 
 
 def _f8_type(q):
-    import torch
-    if q.dtype == torch.float8_e4m3fn:
-        return GEMM_F8_E4M3
-    if q.dtype == torch.float8_e5m2:
-        return GEMM_F8_E5M2
+    for f8_type in (GEMM_F8_E4M3, GEMM_F8_E5M2):
+        if q.dtype is _f8_dtype(f8_type):
+            return f8_type
     raise TypeError("expected torch.float8_e4m3fn or torch.float8_e5m2, got %s" % q.dtype)
 
 
 def _real_type(x):
     import torch
-    if x.dtype == torch.bfloat16:
+    if x.dtype is torch.bfloat16:
         return GEMM_DTYPE_BF16
-    if x.dtype == torch.float32:
+    if x.dtype is torch.float32:
         return GEMM_DTYPE_F32
     raise TypeError("expected torch.bfloat16 or torch.float32, got %s" % x.dtype)
+
+
+def _stream_of(x, stream):
+    """The CUDA stream handle; by default the current stream of x's device
+    (looked up by its raw handle: a small call is as long as its launch)."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(x.get_device())
 
 
 def _matrix(x, dtype, shape):
     """(address, row pitch) of a CUDA tensor whose rows are contiguous; the
     leading dimensions before the last two lie one after the other."""
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError("expected %s, got %s" % (dtype, x.dtype))
     if x.shape != shape:
         raise ValueError("expected shape %s, got %s" % (tuple(shape), tuple(x.shape)))
@@ -408,27 +421,43 @@ def _matrix(x, dtype, shape):
     return x.data_ptr(), pitch
 
 
+def _dense(x, dtype, shape):
+    """Address of a contiguous CUDA tensor."""
+    if x.dtype is not dtype:
+        raise TypeError("expected %s, got %s" % (dtype, x.dtype))
+    if x.shape != shape:
+        raise ValueError("expected shape %s, got %s" % (tuple(shape), tuple(x.shape)))
+    if not x.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    if not x.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return x.data_ptr()
+
+
 def _f8_run(plan, A, a_scale, Bt, b_scale, offsets, D, stream):
     import torch
-    m, k, n, g = plan.m, plan.k, plan.n, plan.groups
+    lib = _lib or load()
+    m, k, n, g, mode = plan.m, plan.k, plan.n, plan.groups, plan.group_mode
     kb = (k + 127) // 128
     f32 = torch.float32
     a, lda = _matrix(A, _f8_dtype(plan.a_type), (m, k))
-    rows = plan.group_mode == GEMM_GROUP_ROWS
+    rows = mode == GEMM_GROUP_ROWS
     b, ldb = _matrix(Bt, _f8_dtype(plan.b_type), (g, n, k) if rows else (n, k))
     if plan.b_scale == GEMM_SCALE_BLOCKS:
-        sb = _addr(b_scale, f32, (g, (n + 127) // 128, kb) if rows else ((n + 127) // 128, kb))
+        sb = _dense(b_scale, f32, (g, (n + 127) // 128, kb) if rows else ((n + 127) // 128, kb))
     else:
-        sb = _addr(b_scale, f32, (kb, g * n) if rows else (kb, n))
-    sa = _addr(a_scale, f32, (kb, m))
-    if D.dtype != f32 and D.dtype != torch.bfloat16:
-        raise TypeError("expected a torch.bfloat16 or torch.float32 output, got %s" % D.dtype)
-    d, ldd = _matrix(D, D.dtype, (g, m, n) if plan.group_mode == GEMM_GROUP_K else (m, n))
-    out = GEMM_OUT_F32 if D.dtype == f32 else GEMM_OUT_BF16
+        sb = _dense(b_scale, f32, (kb, g * n) if rows else (kb, n))
+    sa = _dense(a_scale, f32, (kb, m))
+    out_dtype = D.dtype
+    if out_dtype is not f32 and out_dtype is not torch.bfloat16:
+        raise TypeError("expected a torch.bfloat16 or torch.float32 output, got %s" % out_dtype)
+    d, ldd = _matrix(D, out_dtype, (g, m, n) if mode == GEMM_GROUP_K else (m, n))
+    out = GEMM_OUT_F32 if out_dtype is f32 else GEMM_OUT_BF16
+    s = _stream_of(A, stream)
     if offsets is None:
-        return load().gemm_f8_run(ctypes.byref(plan), a, lda, sa, b, ldb, sb, out, d, ldd, _stream(stream))
-    off = _addr(offsets, torch.int32, (g + 1,))
-    return load().gemm_f8_grouped_run(ctypes.byref(plan), a, lda, sa, b, ldb, sb, off, out, d, ldd, _stream(stream))
+        return lib.gemm_f8_run(plan, a, lda, sa, b, ldb, sb, out, d, ldd, s)
+    off = _dense(offsets, torch.int32, (g + 1,))
+    return lib.gemm_f8_grouped_run(plan, a, lda, sa, b, ldb, sb, off, out, d, ldd, s)
 
 
 def gemm_f8_run(plan: gemm_plan_f8, A, a_scale, Bt, b_scale, D, stream=None) -> None:
@@ -461,7 +490,7 @@ def gemm_f8_quantize(X, Q, scale, scale_mode: int = GEMM_SCALE_ROWS, stream=None
     kb = (cols + 127) // 128
     shape = (kb, rows) if scale_mode == GEMM_SCALE_ROWS else ((rows + 127) // 128, kb)
     st = load().gemm_f8_quantize(x, _real_type(X), rows, cols, ldx, _f8_type(Q), scale_mode, q, ldq,
-                                 _addr(scale, torch.float32, shape), _stream(stream))
+                                 _dense(scale, torch.float32, shape), _stream_of(X, stream))
     _check(st, "gemm_f8_quantize")
 
 
@@ -475,9 +504,9 @@ def gemm_f8_quantize_cols(X, Q, scale, offsets=None, stream=None) -> None:
     kp = gemm_f8_padded_k(rows, groups)
     x, ldx = _matrix(X, X.dtype, (rows, cols))
     q, ldq = _matrix(Q, Q.dtype, (cols, kp))
-    off = None if offsets is None else _addr(offsets, torch.int32, (groups + 1,))
+    off = None if offsets is None else _dense(offsets, torch.int32, (groups + 1,))
     st = load().gemm_f8_quantize_cols(x, _real_type(X), rows, cols, ldx, _f8_type(Q), off, groups, q, ldq,
-                                      _addr(scale, torch.float32, (kp // 128, cols)), _stream(stream))
+                                      _dense(scale, torch.float32, (kp // 128, cols)), _stream_of(X, stream))
     _check(st, "gemm_f8_quantize_cols")
 
 
@@ -489,8 +518,9 @@ def _norm(name, X, R, W, eps, H, rstd, Q, q_dtype, scale, scale_shape, stream):
     h, ldh = (None, 0) if H is None else _matrix(H, X.dtype, (rows, d))
     q, ldq = _matrix(Q, q_dtype, (rows, d))
     f32 = torch.float32
-    st = getattr(load(), name)(x, ldx, r, ldr, _addr(W, f32, (d,)), eps, _real_type(X), rows, d, h, ldh,
-                               _addr(rstd, f32, (rows,)), q, ldq, _addr(scale, f32, scale_shape), _stream(stream))
+    st = getattr(load(), name)(x, ldx, r, ldr, _dense(W, f32, (d,)), eps, _real_type(X), rows, d, h, ldh,
+                               None if rstd is None else _dense(rstd, f32, (rows,)), q, ldq,
+                               _dense(scale, f32, scale_shape), _stream_of(X, stream))
     _check(st, name)
 
 
@@ -518,8 +548,9 @@ def gemm_norm_backward(dY, H, W, rstd, dR, dX, dW, stream=None) -> None:
     h, ldh = _matrix(H, dt, (rows, d))
     r, lddr = (None, 0) if dR is None else _matrix(dR, dt, (rows, d))
     dx, lddx = _matrix(dX, dt, (rows, d))
-    st = load().gemm_norm_backward(dy, lddy, h, ldh, _addr(W, f32, (d,)), _addr(rstd, f32, (rows,)), r, lddr,
-                                   _real_type(dY), rows, d, dx, lddx, _addr(dW, f32, (d,)), _stream(stream))
+    st = load().gemm_norm_backward(dy, lddy, h, ldh, _dense(W, f32, (d,)), _dense(rstd, f32, (rows,)), r, lddr,
+                                   _real_type(dY), rows, d, dx, lddx, None if dW is None else _dense(dW, f32, (d,)),
+                                   _stream_of(dY, stream))
     _check(st, "gemm_norm_backward")
 
 
