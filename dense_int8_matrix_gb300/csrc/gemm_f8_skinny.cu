@@ -8,10 +8,11 @@
 // and the epilogue thread that owns a row of Bt multiplies them by the row's
 // and the columns' scales and adds them to fp32 sums in registers.
 //
-// With few tiles, a cluster of split_k CTAs shares a tile along K.  Each
-// leaves its sums in its shared memory; after a cluster barrier every CTA adds
-// up all of them, in rank order, for its share of the rows of A: no scratch,
-// no second launch, and the same bits every time.
+// With few tiles, a cluster of split_k CTAs shares a tile along K.  Each sends
+// its sums to the CTAs that finish them (one share of the rows of A each)
+// through distributed shared memory, and these add them up in rank order: no
+// scratch, no second launch, and the same bits every time.  Sent, not fetched:
+// remote stores need no answer, and fetching took 3 us where sending takes 1.
 //
 // Grouped by rows: the tiles of all groups are numbered on the device from the
 // offsets; the grid is as large as any split of the rows could need, and
@@ -30,30 +31,30 @@ namespace {
 constexpr int kTileRows = 128;                          // rows of Bt per tile
 constexpr int kWBytes = kTileRows * kF8RowBytes;
 constexpr int kPreBytes = (GEMM_F8_MAX_GROUPS + 1) * 4 + 12;
-constexpr int kCtrlBytes = 256;
+constexpr int kCtrlBytes = 512;
 
 template <int NT, bool BROWS>
 struct Config {
-    static constexpr int EPI_WARPS = NT == 128 ? 8 : 4;
+    // epilogue warps per lane quarter and rows of A per thread: at most 32, so
+    // that several warps share a scheduler and hide each other's waits
+    static constexpr int PARTS = NT == 16 ? 1 : NT == 128 ? 4 : 2;
+    static constexpr int EPI_WARPS = 4 * PARTS;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-    static constexpr int COLS = NT == 128 ? 64 : NT;    // rows of A per epilogue thread
-    static constexpr int CHUNK = NT == 16 ? 16 : 32;
+    static constexpr int COLS = NT / PARTS;
     static constexpr int A_BYTES = NT * kF8RowBytes;
     static constexpr int STAGE = kWBytes + A_BYTES;
     static constexpr int STAGES = NT <= 32 ? 5 : NT == 64 ? 4 : 6;   // NT = 128: one CTA per SM, by registers
-    static constexpr int BUFS = 2;
+    static constexpr int BUFS = 4;                     // TMEM accumulators: the epilogue's latency spans several blocks
     static constexpr int TMEM = NT * BUFS < 32 ? 32 : NT * BUFS;
     static constexpr int SLOTS = 8;                     // blocks whose scales are in shared memory
     static constexpr int SLOT = NT * 4 + (BROWS ? kTileRows * 4 : 16);
     static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + SLOTS * SLOT + kPreBytes + kCtrlBytes + 1024;
-    static_assert(static_cast<size_t>(STAGES) * STAGE >= static_cast<size_t>(NT) * kTileRows * 4, "sums fit in the ring");
+    static_assert(STAGES * STAGE >= NT * kTileRows * 4, "the sums of a split tile fit in the ring");
     static_assert(SMEM <= (NT == 128 ? 227 : 113) * 1024 && SMEM > 24 * 1024, "one or two CTAs per SM");
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 template <int NT, bool BROWS>
@@ -80,30 +81,30 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmA);
+    }
     const int rank = static_cast<int>(blockIdx.x) % split;
     const int id = static_cast<int>(blockIdx.x) / split;
 
-    // Nothing before this line but arithmetic: TMEM is taken only once the
-    // kernel before has ended, so that neither waits for the other's.
+    if (warp == 0) {   // one barrier per lane: full, done, acce, scale, used
+        constexpr int kBars = 2 * kStages + kBufs + 2 * kSlots;
+        for (int i = lane; i < kBars; i += 32) {
+            const bool scale = i >= 2 * kStages + kBufs && i < kBars - kSlots;
+            mbar_init(full0 + 8u * i, i < 2 * kStages ? 1 : scale ? 32 : R::EPI_WARPS);
+        }
+        if (lane == 0) *abort_flag = 0u;
+        fence_barrier_init();
+    }
+    // TMEM is taken only once the kernel before has ended, so that neither
+    // waits for the other's.
     pdl_wait();
     if (warp == 1 && p.mode != GEMM_GROUP_NONE) {
         if (p.mode == GEMM_GROUP_ROWS)
             group_prefix(p.offsets, p.groups, p.m, NT, p.pieces, lane, pre);
         else
             group_prefix(p.offsets, p.groups, p.kb * kF8Block, kF8Block, p.kb, lane, pre);
-    }
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(full0 + 8u * s, 1);
-            mbar_init(done0 + 8u * s, 1);
-        }
-        for (int b = 0; b < kBufs; ++b) mbar_init(acce0 + 8u * b, R::EPI_WARPS);
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(scale0 + 8u * s, 32);
-            mbar_init(used0 + 8u * s, R::EPI_WARPS);
-        }
-        *abort_flag = 0u;
-        fence_barrier_init();
     }
     __syncthreads();
 
@@ -144,15 +145,20 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
     }
     const int blocks = kb_hi - kb_lo;
 
+    // TMEM: taken by the MMA warp, whose address the epilogue waits for; the
+    // loads start without it
+    const auto tmem_ready = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 + 32 * R::EPI_WARPS) : "memory"); };
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), R::TMEM);
         tmem_relinquish();
+        pdl_launch_dependents();   // with this CTA's TMEM taken
+        tc_fence_before();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    pdl_launch_dependents();   // with this grid's TMEM taken
-    const uint32_t tmem = *tmem_slot;
+    if (warp == 1 || warp >= 4) {
+        tmem_ready();
+        tc_fence_after();
+    }
+    const uint32_t tmem = *tmem_slot;   // (the loading warps do not use it)
 
     uint64_t acc[kCols / 2];
 #pragma unroll
@@ -233,7 +239,6 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
         // --------------------------------------------------- scale and add --
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kCols;
-        constexpr int kChunk = R::CHUNK;
         Turn<kStages> st;
         Turn<kBufs> buf;
         Turn<kSlots> slot;
@@ -244,21 +249,15 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
             tc_fence_after();
             const uint32_t at = sScale + slot.i * R::SLOT;
             const float s = ld_shared_f32(at + NT * 4 + (BROWS ? 4 * (q * 32 + lane) : 0));
-            const uint64_t s2 = pair_of(__float_as_uint(s), __float_as_uint(s));
+            uint32_t v[kCols];
+            uint4 sc[kCols / 4];
 #pragma unroll
-            for (int c = 0; c < kCols / kChunk; ++c) {
-                uint32_t v[kChunk];
-                uint4 sc[kChunk / 4];
-#pragma unroll
-                for (int i = 0; i < kChunk / 4; ++i) sc[i] = ld_shared_v4(at + (h * kCols + c * kChunk + 4 * i) * 4);
-                load_tmem(t0 + buf.i * NT + c * kChunk, v);
-                wait_tmem(v);
-                if (c + 1 == kCols / kChunk) {
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive(acce0 + 8u * buf.i);
-                }
-                add_scaled<kChunk>(acc + c * (kChunk / 2), v, s2, sc);
-            }
+            for (int i = 0; i < kCols / 4; ++i) sc[i] = ld_shared_v4(at + (h * kCols + 4 * i) * 4);
+            load_tmem(t0 + buf.i * NT, v);
+            wait_tmem(v);
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(acce0 + 8u * buf.i);
+            add_scaled<kCols>(acc, v, pair_of(__float_as_uint(s), __float_as_uint(s)), sc);
             __syncwarp();   // every lane has read the block's scales
             if (lane == 0) mbar_arrive(used0 + 8u * slot.i);
             st.next();
@@ -291,30 +290,31 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
             }
         }
     } else {
-        // sums[r][c]: row r of A, row c of Bt
+        // Row r of A is finished by CTA r / share, whose ring (idle in every
+        // CTA after the first barrier) holds sums[sender][row][row of Bt]; a
+        // warp's store is 128 contiguous bytes.
+        const int c = threadIdx.x & 127, h = (warp - 4) >> 2;
+        const int share = NT / split;
+        cluster_barrier();
         if (warp >= 4) {
-            const int h = (warp - 4) >> 2;
-            const uint32_t at = base + (h * kCols * kTileRows + (threadIdx.x & 127)) * 4;
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) {
-                float a, b;
-                unpair(acc[j], a, b);
-                st_shared_u32(at + 2 * j * kTileRows * 4, __float_as_uint(a));
-                st_shared_u32(at + (2 * j + 1) * kTileRows * 4, __float_as_uint(b));
+                float x, y;
+                unpair(acc[j], x, y);   // rows 2j and 2j + 1: an even share keeps them together
+                const int r = h * kCols + 2 * j, owner = r / share;
+                const uint32_t at = peer_address(base + ((rank * share + r - owner * share) * kTileRows + c) * 4, owner);
+                st_cluster_f32(at, x);
+                st_cluster_f32(at + kTileRows * 4, y);
             }
         }
-        __syncthreads();
         cluster_barrier();
-        const int r0 = NT * rank / split, r1 = NT * (rank + 1) / split;
         if (warp >= 4) {
-            for (int r = r0 + ((warp - 4) >> 2); r < r1; r += R::EPI_WARPS / 4) {
-                const uint32_t at = base + (r * kTileRows + (threadIdx.x & 127)) * 4;
+            for (int r = h; r < share; r += R::EPI_WARPS / 4) {
                 float v = 0.f;
-                for (int c = 0; c < split; ++c) v += ld_cluster_f32(peer_address(at, c));
-                put(r, v);
+                for (int s = 0; s < split; ++s) v += ld_shared_f32(base + ((s * share + r) * kTileRows + c) * 4);
+                put(share * rank + r, v);
             }
         }
-        cluster_barrier();   // the other CTAs have read this one's sums
     }
     tc_fence_before();
     __syncthreads();

@@ -134,16 +134,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
-    if (warp == 0 && lane == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(full0 + 8u * s, 1);
-            mbar_init(done0 + 8u * s, 1);
+    if (warp == 0) {   // one barrier per lane: full, done, acce, scale, last
+        constexpr int kBars = 2 * kStages + kBufs + kSlots + 2;
+        for (int i = lane; i < kBars; i += 32) {
+            const bool acce = i >= 2 * kStages && i < 2 * kStages + kBufs, scale = !acce && i >= 2 * kStages && i < kBars - 2;
+            mbar_init(full0 + 8u * i, acce ? 2 * kEpiWarps : scale ? 32 : 1);
         }
-        for (int b = 0; b < kBufs; ++b) mbar_init(acce0 + 8u * b, 2 * kEpiWarps);
-        for (int s = 0; s < kSlots; ++s) mbar_init(scale0 + 8u * s, 32);
-        mbar_init(last0, 1);
-        mbar_init(last0 + 8u, 1);
-        *abort_flag = 0u;
+        if (lane == 0) {
+            tma_prefetch_desc(&tmA);
+            tma_prefetch_desc(&tmB);
+            *abort_flag = 0u;
+        }
         fence_barrier_init();
     }
     if (warp == 1) alloc_pair(smem_u32(tmem_slot), 512);

@@ -7,6 +7,7 @@
 //
 // Both are bound by DRAM: every element is read and written once.
 #include "f8.cuh"
+#include "internal.h"
 #include "ptx.cuh"
 
 namespace gemm {
@@ -32,6 +33,8 @@ __device__ __forceinline__ float cta_reduce(float v, float* red) {
 template <typename T, int V, bool I8>
 __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool vec, bool qvec, bool wvec) {
     __shared__ float red[2][32];
+    pdl_launch_dependents();
+    pdl_wait();
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(p.X) + row * p.ldx;
     const T* r = p.R ? static_cast<const T*>(p.R) + row * p.ldr : nullptr;
@@ -110,79 +113,112 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool ve
     }
 }
 
-// Persistent CTAs over the rows; dw's running sums of the CTA's rows stay in
-// shared memory (each thread owns its columns), and go to `partial`, which
-// dw_reduce_kernel adds up in CTA order.
-template <typename T, int V>
+// Persistent CTAs over the rows.  A thread owns the same columns of every row
+// (eight per vector), and dw's running sums of the CTA's rows stay in shared
+// memory, one word per thread and column so that no two lanes share a bank.
+// They go to `partial`, which dw_reduce_kernel adds up in CTA order.  PRE: the
+// next row is on its way while this one is reduced.
+template <typename T, int V, bool PRE>
 __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool vec, bool wvec) {
-    extern __shared__ float dw[];
+    extern __shared__ float dw[];   // [V * 8][threads]
     __shared__ float red[2][32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int threads = blockDim.x, t = threadIdx.x;
     if (p.dW)
-        for (int64_t c = threadIdx.x; c < p.d; c += blockDim.x) dw[c] = 0.f;
-    __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8 * V; ++i) dw[i * threads + t] = 0.f;
+    auto column = [&](int v) { return 8 * (static_cast<int64_t>(v) * threads + t); };
+    struct Row {
+        Vec8<T> dy[V], h[V], dr[V];
+        float rstd;
+    };
+    auto fetch = [&](int64_t row, Row& x) {
+        x.rstd = __ldg(p.rstd + row);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x.dy[v] = load8(static_cast<const T*>(p.dY) + row * p.lddy, column(v), p.d, vec);
+            x.h[v] = load8(static_cast<const T*>(p.H) + row * p.ldh, column(v), p.d, vec);
+            if (p.dR)
+                x.dr[v] = load8(static_cast<const T*>(p.dR) + row * p.lddr, column(v), p.d, vec);
+            else
+                x.dr[v].zero();
+        }
+    };
+    Row x, next;
+    if (blockIdx.x < p.rows) fetch(blockIdx.x, x);
     int turn = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-        Vec8<T> dy[V], h[V];
-        const float rstd = __ldg(p.rstd + row);
+        const bool more = row + gridDim.x < p.rows;
+        if (PRE && more) fetch(row + gridDim.x, next);
         float dot = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int64_t c = 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x);
-            dy[v] = load8(static_cast<const T*>(p.dY) + row * p.lddy, c, p.d, vec);
-            h[v] = load8(static_cast<const T*>(p.H) + row * p.ldh, c, p.d, vec);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int64_t c = 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x);
             float w[8], a[8], b[8];
-            load8_f32(p.W, c, p.d, wvec, w);
-            dy[v].get(a);
-            h[v].get(b);
+            load8_f32(p.W, column(v), p.d, wvec, w);
+            x.dy[v].get(a);
+            x.h[v].get(b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dot += a[i] * w[i] * (b[i] * rstd);
+            for (int i = 0; i < 8; ++i) dot += a[i] * w[i] * (b[i] * x.rstd);
         }
         const float mean = cta_reduce<false>(dot, red[turn]) / static_cast<float>(p.d);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int64_t c = 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x);
             float w[8], a[8], b[8], o[8];
-            load8_f32(p.W, c, p.d, wvec, w);
-            dy[v].get(a);
-            h[v].get(b);
-            if (p.dR) {
-                load8(static_cast<const T*>(p.dR) + row * p.lddr, c, p.d, vec).get(o);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = 0.f;
-            }
+            load8_f32(p.W, column(v), p.d, wvec, w);
+            x.dy[v].get(a);
+            x.h[v].get(b);
+            x.dr[v].get(o);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 // written out so that dX has the same bits with and without dW
-                const float xhat = __fmul_rn(b[i], rstd);
-                o[i] = __fmaf_rn(rstd, __fmaf_rn(a[i], w[i], -__fmul_rn(xhat, mean)), o[i]);
-                if (p.dW && c + i < p.d) dw[c + i] = __fmaf_rn(a[i], xhat, dw[c + i]);
+                const float xhat = __fmul_rn(b[i], x.rstd);
+                o[i] = __fmaf_rn(x.rstd, __fmaf_rn(a[i], w[i], -__fmul_rn(xhat, mean)), o[i]);
+                float* s = dw + (v * 8 + i) * threads + t;
+                if (p.dW) *s = __fmaf_rn(a[i], xhat, *s);
             }
             Vec8<T> out;
             out.set(o);
-            store8(static_cast<T*>(p.dX) + row * p.lddx, c, p.d, vec, out);
+            store8(static_cast<T*>(p.dX) + row * p.lddx, column(v), p.d, vec, out);
+        }
+        if (more) {
+            if constexpr (PRE)
+                x = next;
+            else
+                fetch(row + gridDim.x, x);
         }
     }
     if (p.dW) {
         float* out = gridDim.x > 1 ? p.partial + static_cast<int64_t>(blockIdx.x) * p.d : p.dW;
-        __syncthreads();
-        for (int64_t c = threadIdx.x; c < p.d; c += blockDim.x) out[c] = dw[c];
+#pragma unroll
+        for (int i = 0; i < 8 * V; ++i) {
+            const int64_t c = column(i / 8) + i % 8;
+            if (c < p.d) out[c] = dw[i * threads + t];
+        }
     }
 }
 
 // dW_j = sum of the CTAs' sums: a warp's lanes take 32 columns, the eight
-// warps of a CTA every eighth partial, joined in warp order.
+// warps of a CTA every eighth partial (four loads at a time), joined in warp
+// order.
 __global__ void __launch_bounds__(256) dw_reduce_kernel(const float* partial, int parts, int64_t d, float* dW) {
     __shared__ float red[8][32];
+    pdl_launch_dependents();
+    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float s = 0.f;
-    if (c < d)
-        for (int i = warp; i < parts; i += 8) s += partial[static_cast<int64_t>(i) * d + c];
+    if (c < d) {
+        int i = warp;
+        for (; i + 24 < parts; i += 32) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = partial[static_cast<int64_t>(i + 8 * j) * d + c];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s += v[j];
+        }
+        for (; i < parts; i += 8) s += partial[static_cast<int64_t>(i) * d + c];
+    }
     red[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < d) {
@@ -197,34 +233,44 @@ bool al16(const void* p, int64_t pitch_bytes) {
 }
 
 // Threads and vectors per thread of a row of d elements: 4 vectors per thread
-// keep enough loads in flight when many rows run at once; a few rows run
-// sooner with one vector per thread.
-void row_shape(int64_t rows, int64_t d, int num_sms, int* threads, int* vecs) {
+// keep enough loads in flight when many rows run at once; a few rows, or rows
+// that are loaded element by element, run sooner with one vector per thread.
+void row_shape(int64_t rows, int64_t d, bool vec, int num_sms, int* threads, int* vecs) {
     const int64_t nv = (d + 7) / 8;
-    int v = rows > 2 * static_cast<int64_t>(num_sms) ? 4 : 1;
+    int v = vec && rows > 2 * static_cast<int64_t>(num_sms) ? 4 : 1;
     while (v < 4 && (nv + v - 1) / v > 1024) v *= 2;
-    int64_t t = ((nv + v - 1) / v + 31) / 32 * 32;
-    *threads = static_cast<int>(t);
+    *threads = static_cast<int>(((nv + v - 1) / v + 31) / 32 * 32);
     *vecs = v;
 }
 
-template <typename T, int V>
-cudaError_t fwd_launch(const NormFwd& a, int threads, cudaStream_t stream) {
+template <typename T>
+bool fwd_vec(const NormFwd& a) {
     const int64_t es = sizeof(T);
-    const bool vec = al16(a.X, a.ldx * es) && (!a.R || al16(a.R, a.ldr * es)) && (!a.H || al16(a.H, a.ldh * es));
-    const bool qvec = reinterpret_cast<uintptr_t>(a.Q) % 8 == 0 && a.ldq % 8 == 0;
-    const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0;
-    if (a.to_i8)
-        norm_fwd_kernel<T, V, true><<<static_cast<unsigned>(a.rows), threads, 0, stream>>>(a, vec, qvec, wvec);
-    else
-        norm_fwd_kernel<T, V, false><<<static_cast<unsigned>(a.rows), threads, 0, stream>>>(a, vec, qvec, wvec);
-    return cudaGetLastError();
+    return al16(a.X, a.ldx * es) && (!a.R || al16(a.R, a.ldr * es)) && (!a.H || al16(a.H, a.ldh * es));
 }
 
+template <typename T, int V>
+cudaError_t fwd_launch(const NormFwd& a, int threads, bool vec, cudaStream_t stream) {
+    const bool qvec = reinterpret_cast<uintptr_t>(a.Q) % 8 == 0 && a.ldq % 8 == 0;
+    const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0;
+    return launch_chained(a.to_i8 ? norm_fwd_kernel<T, V, true> : norm_fwd_kernel<T, V, false>,
+                          dim3(static_cast<unsigned>(a.rows)), threads, 0, stream, a, vec, qvec, wvec);
+}
+
+template <typename T>
+cudaError_t fwd_type(const NormFwd& a, cudaStream_t stream) {
+    int t, v;
+    const bool vec = fwd_vec<T>(a);
+    row_shape(a.rows, a.d, vec, a.num_sms, &t, &v);
+    return v == 1 ? fwd_launch<T, 1>(a, t, vec, stream) : v == 2 ? fwd_launch<T, 2>(a, t, vec, stream)
+                                                                 : fwd_launch<T, 4>(a, t, vec, stream);
+}
+
+// One vector per thread up to 8192 columns.
 void bwd_shape(int64_t d, int* threads, int* vecs) {
     const int64_t nv = (d + 7) / 8;
     int v = 1;
-    while (v < 4 && (nv + v - 1) / v > 512) v *= 2;
+    while ((nv + v - 1) / v > 1024) v *= 2;
     *threads = static_cast<int>(((nv + v - 1) / v + 31) / 32 * 32);
     *vecs = v;
 }
@@ -235,47 +281,42 @@ cudaError_t bwd_launch(const NormBwd& a, int threads, cudaStream_t stream) {
     const bool vec = al16(a.dY, a.lddy * es) && al16(a.H, a.ldh * es) && (!a.dR || al16(a.dR, a.lddr * es)) &&
                      al16(a.dX, a.lddx * es);
     const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0;
-    const size_t smem = a.dW ? static_cast<size_t>(a.d) * 4 : 0;
+    const size_t smem = a.dW ? static_cast<size_t>(8 * V) * threads * 4 : 0;
+    const auto kern = norm_bwd_kernel<T, V, V * sizeof(T) <= 2>;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   GEMM_NORM_MAX_D * 4);
+        const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), GEMM_NORM_MAX_D * 4, false);
         if (e != cudaSuccess) return e;
     }
-    norm_bwd_kernel<T, V><<<a.grid, threads, smem, stream>>>(a, vec, wvec);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && a.dW && a.grid > 1) {
-        dw_reduce_kernel<<<static_cast<unsigned>((a.d + 31) / 32), 256, 0, stream>>>(a.partial, a.grid, a.d, a.dW);
-        e = cudaGetLastError();
-    }
+    cudaError_t e = launch_chained(kern, dim3(static_cast<unsigned>(a.grid)), threads, smem, stream, a, vec, wvec);
+    if (e == cudaSuccess && a.dW && a.grid > 1)
+        e = launch_chained(dw_reduce_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), 256, 0, stream, a.partial, a.grid,
+                           a.d, a.dW);
     return e;
+}
+
+template <typename T>
+cudaError_t bwd_type(const NormBwd& a, cudaStream_t stream) {
+    int t, v;
+    bwd_shape(a.d, &t, &v);
+    return v == 1 ? bwd_launch<T, 1>(a, t, stream) : v == 2 ? bwd_launch<T, 2>(a, t, stream) : bwd_launch<T, 4>(a, t, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_fwd(const NormFwd& a, cudaStream_t stream) {
-    int t, v;
-    row_shape(a.rows, a.d, a.num_sms, &t, &v);
-    if (a.x_type == GEMM_DTYPE_BF16)
-        return v == 1 ? fwd_launch<__nv_bfloat16, 1>(a, t, stream)
-               : v == 2 ? fwd_launch<__nv_bfloat16, 2>(a, t, stream) : fwd_launch<__nv_bfloat16, 4>(a, t, stream);
-    return v == 1 ? fwd_launch<float, 1>(a, t, stream)
-           : v == 2 ? fwd_launch<float, 2>(a, t, stream) : fwd_launch<float, 4>(a, t, stream);
+    return a.x_type == GEMM_DTYPE_BF16 ? fwd_type<__nv_bfloat16>(a, stream) : fwd_type<float>(a, stream);
 }
 
+// As many CTAs as run at once (1024 threads per SM): each keeps its own dw.
 int norm_bwd_grid(int64_t rows, int64_t d, int num_sms) {
-    (void)d;
-    const int64_t g = 2 * static_cast<int64_t>(num_sms);
+    int t, v;
+    bwd_shape(d, &t, &v);
+    const int64_t g = static_cast<int64_t>(num_sms) * (1024 / t);
     return static_cast<int>(rows < g ? rows : g);
 }
 
 cudaError_t launch_norm_bwd(const NormBwd& a, cudaStream_t stream) {
-    int t, v;
-    bwd_shape(a.d, &t, &v);
-    if (a.x_type == GEMM_DTYPE_BF16)
-        return v == 1 ? bwd_launch<__nv_bfloat16, 1>(a, t, stream)
-               : v == 2 ? bwd_launch<__nv_bfloat16, 2>(a, t, stream) : bwd_launch<__nv_bfloat16, 4>(a, t, stream);
-    return v == 1 ? bwd_launch<float, 1>(a, t, stream)
-           : v == 2 ? bwd_launch<float, 2>(a, t, stream) : bwd_launch<float, 4>(a, t, stream);
+    return a.x_type == GEMM_DTYPE_BF16 ? bwd_type<__nv_bfloat16>(a, stream) : bwd_type<float>(a, stream);
 }
 
 }  // namespace gemm

@@ -7,30 +7,41 @@ namespace gemm {
 namespace {
 
 // 1 x 128 blocks: half a warp takes one block of one row, eight values per
-// lane.  Reads rows * cols elements, writes as many bytes: bound by DRAM.
+// lane; a warp takes eight neighbouring blocks of a row, all loads first.
+// Reads every element once and writes a byte for it: bound by DRAM.
+constexpr int kRowBlocks = 8;   // blocks of a row per warp
 template <typename T, int F8>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const F8Quant p, bool vec, bool qvec) {
-    const int64_t kb = (p.cols + kF8Block - 1) / kF8Block;
-    const int64_t items = p.rows * kb;
+    pdl_launch_dependents();
+    pdl_wait();
     constexpr float M = F8 == GEMM_F8_E4M3 ? kE4M3Max : kE5M2Max;
-    const int sub = threadIdx.x & 15;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x / 16);
-    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 16); i0 < items; i0 += stride) {
-        const int64_t i = i0 + threadIdx.x / 16;
-        const bool on = i < items;   // uniform in each half warp; every lane takes part in the shuffles
-        const int64_t row = on ? i / kb : 0, b = on ? i - row * kb : 0;
-        const int64_t c = on ? b * kF8Block + sub * 8 : p.cols;
-        float f[8];
-        load8(static_cast<const T*>(p.X) + row * p.ldx, c, p.cols, vec).get(f);
-        float a = 0.f;
+    constexpr int kLoads = kRowBlocks / 2;
+    const int64_t kb = (p.cols + kF8Block - 1) / kF8Block;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= p.rows) return;   // whole warps
+    const T* x = static_cast<const T*>(p.X) + row * p.ldx;
+    uint8_t* q = p.Q + row * p.ldq;
+    const int half = (threadIdx.x >> 4) & 1, sub = threadIdx.x & 15;
+    for (int64_t b0 = static_cast<int64_t>(blockIdx.y) * kRowBlocks; b0 < kb; b0 += static_cast<int64_t>(gridDim.y) * kRowBlocks) {
+        Vec8<T> v[kLoads];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(f[j]));
-        const float s = block_scale(half_warp_max(a), M);
-        const float inv = __frcp_rn(s);
-        if (!on) continue;
-        store8_bytes(p.Q + row * p.ldq, c, p.cols, qvec, f8x4<F8>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                     f8x4<F8>(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-        if (sub == 0) p.scale[b * p.rows + row] = s;
+        for (int i = 0; i < kLoads; ++i) v[i] = load8(x, (b0 + 2 * i + half) * kF8Block + sub * 8, p.cols, vec);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int64_t b = b0 + 2 * i + half, c = b * kF8Block + sub * 8;
+            float f[8];
+            v[i].get(f);
+            float a = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(f[j]));
+            const float s = block_scale(half_warp_max(a), M);   // every lane takes part in the shuffles
+            const float inv = __frcp_rn(s);
+            if (b < kb) {
+                store8_bytes(q, c, p.cols, qvec, f8x4<F8>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                             f8x4<F8>(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+                if (sub == 0) p.scale[b * p.rows + row] = s;
+            }
+        }
     }
 }
 
@@ -39,6 +50,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const F8Quant p, bool v
 template <typename T, int F8>
 __global__ void __launch_bounds__(256) quant_blocks_kernel(const F8Quant p, bool vec, bool qvec) {
     __shared__ float red[8];
+    pdl_launch_dependents();
+    pdl_wait();
     constexpr float M = F8 == GEMM_F8_E4M3 ? kE4M3Max : kE5M2Max;
     const int64_t kb = (p.cols + kF8Block - 1) / kF8Block;
     const int64_t rb = blockIdx.x / kb, b = blockIdx.x - rb * kb;
@@ -118,13 +131,16 @@ __device__ void find_block_rows(const F8Quant& p, int pb, int lane, int& row, in
 
 // Transposed 1 x 128 blocks: one CTA turns 128 rows x 128 columns of X into
 // 128 rows of 128 bytes of Q.  A thread holds eight rows of eight columns, so
-// that a column's eight values pack into two words of shared memory; the
-// bytes leave as 128-byte rows.
-constexpr int kColsPitch = 144;   // bytes per column in shared memory (16-byte aligned, spreads the banks)
+// that a column's eight values pack into eight bytes of shared memory; the
+// bytes leave as 128-byte rows.  The tile's 8-byte pieces are swizzled by the
+// column group, so that neither side has bank conflicts beyond its width.
 template <typename T, int F8>
 __global__ void __launch_bounds__(256) quant_cols_kernel(const F8Quant p, bool vec) {
-    __shared__ __align__(16) uint8_t tile[kF8Block * kColsPitch];
-    __shared__ float red[8][kF8Block];
+    __shared__ __align__(16) uint8_t tile[kF8Block * kF8Block];
+    __shared__ __align__(16) float red[8][kF8Block];
+    __shared__ __align__(16) float inverse[kF8Block];
+    pdl_launch_dependents();
+    pdl_wait();
     constexpr float M = F8 == GEMM_F8_E4M3 ? kE4M3Max : kE5M2Max;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kF8Block;
@@ -155,41 +171,42 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const F8Quant p, bool v
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) am[j] = fmaxf(am[j], __shfl_xor_sync(0xffffffffu, am[j], 16));
-        if (lane < 16)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) red[warp][cg * 8 + j] = am[j];
+        if (lane < 16) {
+            *reinterpret_cast<float4*>(&red[warp][cg * 8]) = make_float4(am[0], am[1], am[2], am[3]);
+            *reinterpret_cast<float4*>(&red[warp][cg * 8 + 4]) = make_float4(am[4], am[5], am[6], am[7]);
+        }
         __syncthreads();
-        float s[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        if (threadIdx.x < kF8Block) {   // one thread per column
             float a = 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) a = fmaxf(a, red[w][cg * 8 + j]);
-            s[j] = block_scale(a, M);
+            for (int w = 0; w < 8; ++w) a = fmaxf(a, red[w][threadIdx.x]);
+            const float s = block_scale(a, M);
+            inverse[threadIdx.x] = __frcp_rn(s);
+            if (c0 + threadIdx.x < p.cols) p.scale[static_cast<int64_t>(pb) * p.cols + c0 + threadIdx.x] = s;
         }
-        if (rg == 0)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < p.cols) p.scale[static_cast<int64_t>(pb) * p.cols + c + j] = s[j];
-        uint32_t w0[8], w1[8];
-        float f[8][8];
+        __syncthreads();
+        float f[8][8], inv[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i].get(f[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float inv = __frcp_rn(s[j]);
-            w0[j] = f8x4<F8>(f[0][j] * inv, f[1][j] * inv, f[2][j] * inv, f[3][j] * inv);
-            w1[j] = f8x4<F8>(f[4][j] * inv, f[5][j] * inv, f[6][j] * inv, f[7][j] * inv);
-            *reinterpret_cast<uint2*>(tile + (cg * 8 + j) * kColsPitch + rg * 8) = make_uint2(w0[j], w1[j]);
+        for (int j = 0; j < 8; j += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(&inverse[cg * 8 + j]);
+            inv[j] = x.x; inv[j + 1] = x.y; inv[j + 2] = x.z; inv[j + 3] = x.w;
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint2*>(tile + (cg * 8 + j) * kF8Block + ((rg ^ cg) << 3)) =
+                make_uint2(f8x4<F8>(f[0][j] * inv[j], f[1][j] * inv[j], f[2][j] * inv[j], f[3][j] * inv[j]),
+                           f8x4<F8>(f[4][j] * inv[j], f[5][j] * inv[j], f[6][j] * inv[j], f[7][j] * inv[j]));
         __syncthreads();
         // eight lanes write one column's 128 bytes
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int col = (threadIdx.x >> 3) + 32 * i, part = threadIdx.x & 7;
+            const int col = (threadIdx.x >> 3) + 32 * i, part = threadIdx.x & 7, g = col >> 3;
+            uint4 x = *reinterpret_cast<const uint4*>(tile + col * kF8Block + (((2 * part) ^ (g & ~1)) << 3));
+            if (g & 1) x = make_uint4(x.z, x.w, x.x, x.y);
             if (c0 + col < p.cols)
-                *reinterpret_cast<uint4*>(p.Q + (c0 + col) * p.ldq + static_cast<int64_t>(pb) * kF8Block + part * 16) =
-                    *reinterpret_cast<const uint4*>(tile + col * kColsPitch + part * 16);
+                *reinterpret_cast<uint4*>(p.Q + (c0 + col) * p.ldq + static_cast<int64_t>(pb) * kF8Block + part * 16) = x;
         }
         __syncthreads();   // the tile and the column maxima are reused
     }
@@ -202,28 +219,24 @@ bool vec_ok(const void* p, int64_t pitch) {
 
 template <typename T, int F8>
 cudaError_t rows_launch(const F8Quant& q, cudaStream_t stream) {
-    const int64_t items = q.rows * ((q.cols + kF8Block - 1) / kF8Block);
-    const int64_t grid = (items + 15) / 16, cap = static_cast<int64_t>(q.num_sms) * 64;
-    quant_rows_kernel<T, F8><<<static_cast<unsigned>(grid < cap ? grid : cap), 256, 0, stream>>>(
-        q, vec_ok<T>(q.X, q.ldx), reinterpret_cast<uintptr_t>(q.Q) % 8 == 0 && q.ldq % 8 == 0);
-    return cudaGetLastError();
+    const int64_t gx = (q.rows + 7) / 8, gy = (q.cols + kF8Block * kRowBlocks - 1) / (kF8Block * kRowBlocks);
+    return launch_chained(quant_rows_kernel<T, F8>, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535)),
+                          256, 0, stream, q, vec_ok<T>(q.X, q.ldx), reinterpret_cast<uintptr_t>(q.Q) % 8 == 0 && q.ldq % 8 == 0);
 }
 
 template <typename T, int F8>
 cudaError_t blocks_launch(const F8Quant& q, cudaStream_t stream) {
     const int64_t grid = ((q.rows + kF8Block - 1) / kF8Block) * ((q.cols + kF8Block - 1) / kF8Block);
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    quant_blocks_kernel<T, F8><<<static_cast<unsigned>(grid), 256, 0, stream>>>(
-        q, vec_ok<T>(q.X, q.ldx), reinterpret_cast<uintptr_t>(q.Q) % 8 == 0 && q.ldq % 8 == 0);
-    return cudaGetLastError();
+    return launch_chained(quant_blocks_kernel<T, F8>, dim3(static_cast<unsigned>(grid)), 256, 0, stream, q,
+                          vec_ok<T>(q.X, q.ldx), reinterpret_cast<uintptr_t>(q.Q) % 8 == 0 && q.ldq % 8 == 0);
 }
 
 template <typename T, int F8>
 cudaError_t cols_launch(const F8Quant& q, cudaStream_t stream) {
     const int64_t gx = (q.cols + kF8Block - 1) / kF8Block, gy = q.kp / kF8Block;
-    quant_cols_kernel<T, F8><<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535)), 256, 0,
-                               stream>>>(q, vec_ok<T>(q.X, q.ldx));
-    return cudaGetLastError();
+    return launch_chained(quant_cols_kernel<T, F8>, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535)),
+                          256, 0, stream, q, vec_ok<T>(q.X, q.ldx));
 }
 
 }  // namespace
