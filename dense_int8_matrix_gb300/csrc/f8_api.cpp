@@ -44,7 +44,7 @@ void choose_config(gemm_plan_f8* p) {
         p->bn = 128;
         const int64_t groups = by_rows ? (p->m < p->groups ? p->m : p->groups) : p->group_mode == GEMM_GROUP_K ? p->groups : 1;
         const int64_t tiles = groups * ceil_div(rows, p->bm) * ceil_div(p->n, 128);
-        const int64_t room = (p->bm == 128 ? 1 : 2) * static_cast<int64_t>(p->num_sms);
+        const int64_t room = (p->bm >= 64 ? 1 : 2) * static_cast<int64_t>(p->num_sms);
         int s = 1;
         while (s < 8 && tiles * s * 2 <= room && kb / (s * 2) >= 4) s *= 2;
         p->split_k = s;

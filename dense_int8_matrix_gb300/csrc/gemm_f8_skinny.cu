@@ -145,16 +145,16 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
     }
     const int blocks = kb_hi - kb_lo;
 
-    // TMEM: taken by the MMA warp, whose address the epilogue waits for; the
-    // loads start without it
-    const auto tmem_ready = [] { asm volatile("bar.sync 1, %0;" ::"n"(32 + 32 * R::EPI_WARPS) : "memory"); };
+    // TMEM: the MMA warps and the epilogue wait for its address; the loads
+    // start without it
+    const auto tmem_ready = [] { asm volatile("bar.sync 1, %0;" ::"n"(64 + 32 * R::EPI_WARPS) : "memory"); };
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), R::TMEM);
         tmem_relinquish();
         pdl_launch_dependents();   // with this CTA's TMEM taken
         tc_fence_before();
     }
-    if (warp == 1 || warp >= 4) {
+    if (warp == 1 || warp >= 3) {
         tmem_ready();
         tc_fence_after();
     }
@@ -183,12 +183,14 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
         if (issued < blocks)   // after a time-out the copies still in flight land before the CTA ends
             for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j)
                 wait_bounded(full0 + 8u * (j % kStages), (j / kStages) & 1u, nullptr, p.err, kDevErrTimeoutTeardown);
-    } else if (warp == 1) {
-        // ------------------------------------------------------------- MMAs --
+    } else if (warp == 1 || warp == 3) {
+        // ---------------- MMAs: warps 1 and 3 take the K blocks in turn, as
+        // waiting and issuing take one warp longer than a block's loads
         Turn<kStages> st;
         Turn<kBufs> buf;
-        int n = 0;
-        for (; n < blocks; ++n) {
+        st.i = buf.i = warp >> 1;
+        int n = warp >> 1;
+        for (; n < blocks; n += 2) {
             if (!wait_warp(acce0 + 8u * buf.i, buf.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutMma) ||
                 !wait_warp(full0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutMma))
                 break;
@@ -202,13 +204,13 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
                 mma_commit(done0 + 8u * st.i);
             }
             __syncwarp();
-            st.next();
-            buf.next();
+            st.next(2);
+            buf.next(2);
         }
         // the epilogue sees the last block done; after a time-out wait here for
         // the MMAs that were issued
-        if (n < blocks && n > 0)
-            wait_bounded(done0 + 8u * ((n - 1) % kStages), ((n - 1) / kStages) & 1u, nullptr, p.err, kDevErrTimeoutTeardown);
+        if (n < blocks && n > 1)
+            wait_bounded(done0 + 8u * ((n - 2) % kStages), ((n - 2) / kStages) & 1u, nullptr, p.err, kDevErrTimeoutTeardown);
     } else if (warp == 2) {
         // ----------------------------------------------------------- scales --
         Turn<kSlots> slot;
