@@ -154,6 +154,14 @@ __device__ __forceinline__ float half_warp_max(float v) {
     return v;
 }
 
+// Bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) from
+// global to shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // Launch with programmatic stream serialization: the kernel may start while
 // the one before it ends, and calls pdl_wait() before it touches memory.
 template <typename... P, typename... A>

@@ -76,11 +76,14 @@ struct NormBwd {
     int64_t rows, d, lddy, ldh, lddr, lddx;
     void* dX;
     float* dW;        // d sums, or nullptr
-    float* partial;   // grid x d sums when grid > 1
+    float* partial;   // grid x d sums when grid > 1 (16-byte aligned)
     int grid;
+    int num_sms;
+    int* err;         // device error word
 };
-// CTAs of the backward kernel; with more than one, dW needs grid * d floats of scratch.
-int norm_bwd_grid(int64_t rows, int64_t d, int num_sms);
+// CTAs of the backward kernel for the call's other fields; with more than one,
+// dW needs grid * d floats of scratch.
+int norm_bwd_grid(const NormBwd& a);
 cudaError_t launch_norm_bwd(const NormBwd& a, cudaStream_t stream);
 
 }  // namespace gemm

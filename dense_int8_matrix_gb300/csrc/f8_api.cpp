@@ -349,7 +349,9 @@ gemm_status gemm_norm_backward(const void* dY, int64_t lddy, const void* H, int6
     a.dX = dX;
     a.dW = dW;
     a.partial = nullptr;
-    a.grid = norm_bwd_grid(rows, d, ctx.num_sms);
+    a.num_sms = ctx.num_sms;
+    a.err = ctx.err_word;
+    a.grid = norm_bwd_grid(a);
     void* ws = nullptr;
     if (dW && a.grid > 1) {
         if (cudaMallocFromPoolAsync(&ws, static_cast<size_t>(a.grid) * static_cast<size_t>(d) * 4, ctx.pool, s) !=

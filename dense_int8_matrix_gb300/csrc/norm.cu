@@ -116,9 +116,8 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool ve
 // Persistent CTAs over the rows.  A thread owns the same columns of every row
 // (eight per vector), and dw's running sums of the CTA's rows stay in shared
 // memory, one word per thread and column so that no two lanes share a bank.
-// They go to `partial`, which dw_reduce_kernel adds up in CTA order.  PRE: the
-// next row is on its way while this one is reduced.
-template <typename T, int V, bool PRE>
+// They go to `partial`, which dw_reduce_kernel adds up in CTA order.
+template <typename T, int V>
 __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool vec, bool wvec) {
     extern __shared__ float dw[];   // [V * 8][threads]
     __shared__ float red[2][32];
@@ -145,12 +144,10 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool ve
                 x.dr[v].zero();
         }
     };
-    Row x, next;
+    Row x;
     if (blockIdx.x < p.rows) fetch(blockIdx.x, x);
     int turn = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-        const bool more = row + gridDim.x < p.rows;
-        if (PRE && more) fetch(row + gridDim.x, next);
         float dot = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -181,12 +178,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool ve
             out.set(o);
             store8(static_cast<T*>(p.dX) + row * p.lddx, column(v), p.d, vec, out);
         }
-        if (more) {
-            if constexpr (PRE)
-                x = next;
-            else
-                fetch(row + gridDim.x, x);
-        }
+        if (row + gridDim.x < p.rows) fetch(row + gridDim.x, x);
     }
     if (p.dW) {
         float* out = gridDim.x > 1 ? p.partial + static_cast<int64_t>(blockIdx.x) * p.d : p.dW;
@@ -195,6 +187,140 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool ve
             const int64_t c = column(i / 8) + i % 8;
             if (c < p.d) out[c] = dw[i * threads + t];
         }
+    }
+}
+
+// The same for aligned bfloat16 rows of at most 1024 vectors, as training has
+// them: w and dw's running sums stay in registers (512 threads
+// at most, V vectors each), and the rows come through a ring in shared memory,
+// copied several rows ahead by one thread (bulk copies of whole rows, so that
+// up to 200 KB per SM are on their way).
+constexpr int kBwdThreads = 512;
+constexpr int kBwdRingBytes = 200 * 1024;
+constexpr int kBwdSlots = 8;
+template <int V>
+__global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_ring_kernel(const NormBwd p, bool wvec, int slots, int* err) {
+    using T = __nv_bfloat16;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float red[2][32];
+    __shared__ __align__(8) uint64_t bars[kBwdSlots];
+    __shared__ uint32_t abort_flag;
+    const int threads = blockDim.x, t = threadIdx.x;
+    const uint32_t row_bytes = static_cast<uint32_t>(p.d) * 2;
+    const uint32_t slot_bytes = row_bytes * (p.dR ? 3 : 2);
+    const uint32_t ring0 = smem_u32(ring), bar0 = smem_u32(bars);
+    if (t == 0) {
+        for (int s = 0; s < slots; ++s) mbar_init(bar0 + 8u * s, 1);
+        abort_flag = 0u;
+        fence_barrier_init();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    __syncthreads();
+    auto column = [&](int v) { return 8 * (v * threads + t); };
+    const int d = static_cast<int>(p.d);
+    // copies row `row` into slot s (one thread)
+    auto copy_row = [&](int64_t row, int s) {
+        const uint32_t bar = bar0 + 8u * s, dst = ring0 + s * slot_bytes;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load(dst, static_cast<const T*>(p.dY) + row * p.lddy, row_bytes, bar);
+        bulk_load(dst + row_bytes, static_cast<const T*>(p.H) + row * p.ldh, row_bytes, bar);
+        if (p.dR) bulk_load(dst + 2 * row_bytes, static_cast<const T*>(p.dR) + row * p.lddr, row_bytes, bar);
+    };
+    const int64_t step = gridDim.x;
+    if (t == 0)
+        for (int s = 0; s < slots && blockIdx.x + s * step < p.rows; ++s) copy_row(blockIdx.x + s * step, s);
+    float w[V][8], dw[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        load8_f32(p.W, column(v), p.d, wvec, w[v]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
+    }
+    const float inv_d = 1.f / static_cast<float>(p.d);
+    int s = 0, turn = 0;
+    uint32_t ph = 0;
+    float rs = blockIdx.x < p.rows ? __ldg(p.rstd + blockIdx.x) : 0.f;
+    for (int64_t row = blockIdx.x; row < p.rows; row += step, turn ^= 1) {
+        const float rstd = rs;
+        if (row + step < p.rows) rs = __ldg(p.rstd + row + step);
+        // a wait that gives up is recorded; the rows are then wrong, and every
+        // copy still lands in the ring before the CTA ends (see below)
+        wait_bounded(bar0 + 8u * s, ph, &abort_flag, err, kDevErrTimeoutProducer);
+        Vec8<T> dy[V], h[V], dr[V];
+        const uint8_t* src = ring + s * slot_bytes;
+        float dot = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (column(v) < d) {
+                dy[v].u = *reinterpret_cast<const uint4*>(src + column(v) * 2);
+                h[v].u = *reinterpret_cast<const uint4*>(src + row_bytes + column(v) * 2);
+                if (p.dR)
+                    dr[v].u = *reinterpret_cast<const uint4*>(src + 2 * row_bytes + column(v) * 2);
+                else
+                    dr[v].zero();
+            } else {
+                dy[v].zero();
+                h[v].zero();
+                dr[v].zero();
+            }
+            float a[8], x[8];
+            dy[v].get(a);
+            h[v].get(x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dot += a[i] * w[v][i] * (x[i] * rstd);
+        }
+        // every thread has read the slot once it is past this reduction
+        dot = warp_sum(dot);
+        if ((t & 31) == 0) red[turn][t >> 5] = dot;
+        __syncthreads();
+        if (t == 0 && row + slots * step < p.rows) copy_row(row + slots * step, s);
+        dot = (t & 31) < (threads >> 5) ? red[turn][t & 31] : 0.f;
+        const float mean = warp_sum(dot) * inv_d;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float a[8], x[8], o[8];
+            dy[v].get(a);
+            h[v].get(x);
+            dr[v].get(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // written out so that dX has the same bits with and without dW
+                const float xhat = __fmul_rn(x[i], rstd);
+                o[i] = __fmaf_rn(rstd, __fmaf_rn(a[i], w[v][i], -__fmul_rn(xhat, mean)), o[i]);
+                dw[v][i] = __fmaf_rn(a[i], xhat, dw[v][i]);
+            }
+            Vec8<T> out;
+            out.set(o);
+            if (column(v) < d) out.store(static_cast<T*>(p.dX) + row * p.lddx + column(v));
+        }
+        if (++s == slots) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+    // Every copy has been waited for above, unless a wait gave up: then the
+    // last phase of each slot once more, so that nothing lands after the end.
+    if (abort_flag && t == 0) {
+        const int64_t mine = blockIdx.x < p.rows ? (p.rows - blockIdx.x + step - 1) / step : 0;
+        for (int64_t j = mine > slots ? mine - slots : 0; j < mine; ++j)
+            wait_bounded(bar0 + 8u * static_cast<uint32_t>(j % slots), static_cast<uint32_t>(j / slots) & 1u, nullptr, err,
+                         kDevErrTimeoutTeardown);
+    }
+    if (p.dW) {
+        float* out = gridDim.x > 1 ? p.partial + static_cast<int64_t>(blockIdx.x) * p.d : p.dW;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (column(v) < d) {
+                float4* o = reinterpret_cast<float4*>(out + column(v));
+                if (reinterpret_cast<uintptr_t>(out) % 16 == 0) {
+                    o[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+                    o[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) out[column(v) + i] = dw[v][i];
+                }
+            }
     }
 }
 
@@ -232,12 +358,13 @@ bool al16(const void* p, int64_t pitch_bytes) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && pitch_bytes % 16 == 0;
 }
 
-// Threads and vectors per thread of a row of d elements: 4 vectors per thread
-// keep enough loads in flight when many rows run at once; a few rows, or rows
-// that are loaded element by element, run sooner with one vector per thread.
+// Threads and vectors per thread of a row of d elements.  Many rows at once
+// run best with two vectors per thread (8192 x 8192 bfloat16 on GB300: 1, 2 and
+// 4 vectors 92, 79 and 88 us); a few rows, or rows that are loaded element by
+// element, run sooner with one.
 void row_shape(int64_t rows, int64_t d, bool vec, int num_sms, int* threads, int* vecs) {
     const int64_t nv = (d + 7) / 8;
-    int v = vec && rows > 2 * static_cast<int64_t>(num_sms) ? 4 : 1;
+    int v = vec && rows > 2 * static_cast<int64_t>(num_sms) ? 2 : 1;
     while (v < 4 && (nv + v - 1) / v > 1024) v *= 2;
     *threads = static_cast<int>(((nv + v - 1) / v + 31) / 32 * 32);
     *vecs = v;
@@ -275,30 +402,56 @@ void bwd_shape(int64_t d, int* threads, int* vecs) {
     *vecs = v;
 }
 
+// Whether the ring kernel takes the call: aligned bfloat16 rows of whole
+// vectors, enough of them to fill the ring.
+bool bwd_ring(const NormBwd& a) {
+    return a.x_type == GEMM_DTYPE_BF16 && a.d % 8 == 0 && a.d <= 16 * kBwdThreads && a.rows > a.num_sms &&
+           al16(a.dY, a.lddy * 2) && al16(a.H, a.ldh * 2) && (!a.dR || al16(a.dR, a.lddr * 2)) && al16(a.dX, a.lddx * 2);
+}
+
+// Threads of a ring CTA, CTAs per SM (two vectors per thread take 128
+// registers) and rows in its ring.
+void ring_shape(const NormBwd& a, int* threads, int* per_sm, int* slots) {
+    const int64_t nv = a.d / 8;
+    const int v = nv <= kBwdThreads ? 1 : 2;
+    *threads = static_cast<int>(((nv + v - 1) / v + 31) / 32 * 32);
+    *per_sm = v == 1 ? 1024 / *threads : 1;
+    const int64_t fit = kBwdRingBytes / *per_sm / (a.d * 2 * (a.dR ? 3 : 2));
+    *slots = static_cast<int>(fit < kBwdSlots ? fit : kBwdSlots);
+}
+
+template <int V>
+cudaError_t ring_launch(const NormBwd& a, cudaStream_t stream) {
+    int threads, per_sm, slots;
+    ring_shape(a, &threads, &per_sm, &slots);
+    const auto kern = norm_bwd_ring_kernel<V>;
+    const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), kBwdRingBytes, true);
+    if (e != cudaSuccess) return e;
+    return launch_chained(kern, dim3(static_cast<unsigned>(a.grid)), threads,
+                          static_cast<size_t>(slots) * static_cast<size_t>(a.d) * 2 * (a.dR ? 3 : 2), stream, a,
+                          reinterpret_cast<uintptr_t>(a.W) % 16 == 0, slots, a.err);
+}
+
 template <typename T, int V>
-cudaError_t bwd_launch(const NormBwd& a, int threads, cudaStream_t stream) {
+cudaError_t rows_launch(const NormBwd& a, int threads, cudaStream_t stream) {
     const int64_t es = sizeof(T);
     const bool vec = al16(a.dY, a.lddy * es) && al16(a.H, a.ldh * es) && (!a.dR || al16(a.dR, a.lddr * es)) &&
                      al16(a.dX, a.lddx * es);
-    const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0;
     const size_t smem = a.dW ? static_cast<size_t>(8 * V) * threads * 4 : 0;
-    const auto kern = norm_bwd_kernel<T, V, V * sizeof(T) <= 2>;
+    const auto kern = norm_bwd_kernel<T, V>;
     if (smem > 48 * 1024) {
         const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), GEMM_NORM_MAX_D * 4, false);
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = launch_chained(kern, dim3(static_cast<unsigned>(a.grid)), threads, smem, stream, a, vec, wvec);
-    if (e == cudaSuccess && a.dW && a.grid > 1)
-        e = launch_chained(dw_reduce_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), 256, 0, stream, a.partial, a.grid,
-                           a.d, a.dW);
-    return e;
+    return launch_chained(kern, dim3(static_cast<unsigned>(a.grid)), threads, smem, stream, a, vec,
+                          reinterpret_cast<uintptr_t>(a.W) % 16 == 0);
 }
 
 template <typename T>
-cudaError_t bwd_type(const NormBwd& a, cudaStream_t stream) {
+cudaError_t rows_type(const NormBwd& a, cudaStream_t stream) {
     int t, v;
     bwd_shape(a.d, &t, &v);
-    return v == 1 ? bwd_launch<T, 1>(a, t, stream) : v == 2 ? bwd_launch<T, 2>(a, t, stream) : bwd_launch<T, 4>(a, t, stream);
+    return v == 1 ? rows_launch<T, 1>(a, t, stream) : v == 2 ? rows_launch<T, 2>(a, t, stream) : rows_launch<T, 4>(a, t, stream);
 }
 
 }  // namespace
@@ -307,16 +460,27 @@ cudaError_t launch_norm_fwd(const NormFwd& a, cudaStream_t stream) {
     return a.x_type == GEMM_DTYPE_BF16 ? fwd_type<__nv_bfloat16>(a, stream) : fwd_type<float>(a, stream);
 }
 
-// As many CTAs as run at once (1024 threads per SM): each keeps its own dw.
-int norm_bwd_grid(int64_t rows, int64_t d, int num_sms) {
+// As many CTAs as run at once: each keeps its own dw.
+int norm_bwd_grid(const NormBwd& a) {
+    if (bwd_ring(a)) {
+        int threads, per_sm, slots;
+        ring_shape(a, &threads, &per_sm, &slots);
+        const int64_t g = static_cast<int64_t>(a.num_sms) * per_sm;
+        return static_cast<int>(a.rows < g ? a.rows : g);
+    }
     int t, v;
-    bwd_shape(d, &t, &v);
-    const int64_t g = static_cast<int64_t>(num_sms) * (1024 / t);
-    return static_cast<int>(rows < g ? rows : g);
+    bwd_shape(a.d, &t, &v);
+    const int64_t g = static_cast<int64_t>(a.num_sms) * (1024 / t);
+    return static_cast<int>(a.rows < g ? a.rows : g);
 }
 
 cudaError_t launch_norm_bwd(const NormBwd& a, cudaStream_t stream) {
-    return a.x_type == GEMM_DTYPE_BF16 ? bwd_type<__nv_bfloat16>(a, stream) : bwd_type<float>(a, stream);
+    cudaError_t e = bwd_ring(a) ? (a.d <= 8 * kBwdThreads ? ring_launch<1>(a, stream) : ring_launch<2>(a, stream))
+                    : a.x_type == GEMM_DTYPE_BF16 ? rows_type<__nv_bfloat16>(a, stream) : rows_type<float>(a, stream);
+    if (e == cudaSuccess && a.dW && a.grid > 1)
+        e = launch_chained(dw_reduce_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), 256, 0, stream, a.partial, a.grid,
+                           a.d, a.dW);
+    return e;
 }
 
 }  // namespace gemm
