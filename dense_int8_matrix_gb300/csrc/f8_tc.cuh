@@ -234,20 +234,25 @@ __device__ __forceinline__ void more_registers() {
 }
 
 // A warp's 32 rows (lane = row) x C columns of sums leave for D in slices of
-// 64 bytes per row: through the warp's 2 KiB staging buffer (16-byte chunks
-// swizzled by row >> 1, free of bank conflicts both ways), so that four lanes
-// write one row's 64 bytes.  row0: D's row of lane 0; rows at or past row_end
-// and columns at or past n are not written.
-constexpr int kStageRowsBytes = 32 * 64;
+// 128 bytes per row: through the warp's 4 KiB staging buffer (16-byte chunks
+// swizzled by row & 7, free of bank conflicts both ways), so that eight lanes
+// write one row's 128 bytes.  All of a slice is read back before the first
+// store, as each would wait for its own read otherwise.  row0: D's row of lane
+// 0; rows at or past row_end and columns at or past n are not written.
+constexpr int kStageRowsBytes = 32 * 128;
 template <bool F32, int C>
 __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_t stg, int lane, uint8_t* D, int64_t ldd,
                                            int64_t row0, int64_t row_end, int col0, int n, bool vec) {
-    constexpr int W = F32 ? 16 : 32;   // columns per slice
+    constexpr int W = F32 ? 32 : 64;   // columns per slice
     constexpr int ES = F32 ? 4 : 2;
     static_assert(C % W == 0, "whole slices");
+    const int rows = static_cast<int>(row_end - row0 < 32 ? row_end - row0 : 32);
+    const int r0 = lane >> 3, part = lane & 7;
+    uint8_t* out = D + ((row0 + r0) * ldd + col0 + part * (16 / ES)) * ES;
+    const int64_t step = 4 * ldd * ES;
 #pragma unroll
     for (int s = 0; s < C / W; ++s) {
-        uint32_t r[16];
+        uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
             float a, b;
@@ -260,18 +265,15 @@ __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_
             }
         }
         __syncwarp();   // the slice before has been read out
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            st_shared_v4(stg + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        stage_rows32(stg, lane, r);
         __syncwarp();
-        const int c = col0 + s * W + (lane & 3) * (16 / ES);
+        uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int rr = j * 8 + (lane >> 2);
-            const uint4 v = ld_shared_v4(stg + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-            if (row0 + rr < row_end && c < n)
-                store_d16<F32>(D + ((row0 + rr) * ldd + c) * ES, n - c, vec, v);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = ld_shared_v4(stg + (4 * j + r0) * 128 + ((part ^ ((4 * j + r0) & 7)) << 4));
+        const int left = n - (col0 + s * W + part * (16 / ES));
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (4 * j + r0 < rows && left > 0) store_d16<F32>(out + j * step + s * W * ES, left, vec, v[j]);
     }
 }
 
