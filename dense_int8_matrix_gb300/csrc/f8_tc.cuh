@@ -250,6 +250,7 @@ __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_
     const int r0 = lane >> 3, part = lane & 7;
     uint8_t* out = D + ((row0 + r0) * ldd + col0 + part * (16 / ES)) * ES;
     const int64_t step = 4 * ldd * ES;
+    const bool whole = vec && n - col0 >= C;   // the warp's columns are all D's, and 16-byte aligned
 #pragma unroll
     for (int s = 0; s < C / W; ++s) {
         uint32_t r[32];
@@ -268,12 +269,21 @@ __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_
         stage_rows32(stg, lane, r);
         __syncwarp();
         uint4 v[8];
+        if (whole)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = ld_shared_v4(stg + (4 * j + r0) * 128 + ((part ^ ((4 * j + r0) & 7)) << 4));
-        const int left = n - (col0 + s * W + part * (16 / ES));
+            for (int j = 0; j < 8; ++j) v[j] = ld_shared_v4(stg + (4 * j + r0) * 128 + ((part ^ ((4 * j + r0) & 7)) << 4));
+        if (whole) {   // predicated stores and no branch around any
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (4 * j + r0 < rows && left > 0) store_d16<F32>(out + j * step + s * W * ES, left, vec, v[j]);
+            for (int j = 0; j < 8; ++j)
+                if (4 * j + r0 < rows) *reinterpret_cast<uint4*>(out + j * step + s * W * ES) = v[j];
+        } else {
+            const int left = n - (col0 + s * W + part * (16 / ES));
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                const uint4 x = ld_shared_v4(stg + (4 * j + r0) * 128 + ((part ^ ((4 * j + r0) & 7)) << 4));
+                if (4 * j + r0 < rows && left > 0) store_d16<F32>(out + j * step + s * W * ES, left, vec, x);
+            }
+        }
     }
 }
 
