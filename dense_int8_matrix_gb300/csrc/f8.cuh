@@ -11,12 +11,15 @@
 
 namespace gemm {
 
-constexpr float kE4M3Max = 448.f;
-constexpr float kE5M2Max = 57344.f;
+// Reciprocals of the 8-bit types' largest values, rounded to fp32.
+constexpr float kE4M3Step = 1.f / 448.f;
+constexpr float kE5M2Step = 1.f / 57344.f;
+constexpr float kI8Step = 1.f / 127.f;
 constexpr float kScaleMin = 1.17549435e-38f;   // 2^-126: scale of a block of zeros; its reciprocal is finite
 
-// The scale of a block of largest magnitude amax, M the type's largest value.
-__device__ __forceinline__ float block_scale(float amax, float M) { return fmaxf(__fdiv_rn(amax, M), kScaleMin); }
+// The scale of a block of largest magnitude amax, step the reciprocal of the
+// type's largest value.
+__device__ __forceinline__ float block_scale(float amax, float step) { return fmaxf(__fmul_rn(amax, step), kScaleMin); }
 
 // Two fp32 values to two FP8 values (a in the low byte), round to nearest
 // even, clamped to the largest finite value, NaN stays NaN.

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool ve
         if constexpr (I8) {
             amax = fmaxf(amax, a);
         } else {
-            const float s = block_scale(half_warp_max(a), kE4M3Max);
+            const float s = block_scale(half_warp_max(a), kE4M3Step);
             const float inv = __frcp_rn(s);
             if (c < p.d) {
                 store8_bytes(static_cast<uint8_t*>(p.Q) + row * p.ldq, c, p.d, qvec,
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool ve
     }
     if constexpr (I8) {
         amax = cta_reduce<true>(amax, red[1]);
-        const float s = block_scale(amax, 127.f);
+        const float s = block_scale(amax, kI8Step);
         const float inv = __frcp_rn(s);
         // int8 holds no NaN: the row's scale carries it
         if (threadIdx.x == 0) p.scale[row] = isfinite(mean) ? s : __int_as_float(0x7fc00000);

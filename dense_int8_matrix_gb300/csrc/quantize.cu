@@ -14,7 +14,7 @@ template <typename T, int F8>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const F8Quant p, bool vec, bool qvec) {
     pdl_launch_dependents();
     pdl_wait();
-    constexpr float M = F8 == GEMM_F8_E4M3 ? kE4M3Max : kE5M2Max;
+    constexpr float kStep = F8 == GEMM_F8_E4M3 ? kE4M3Step : kE5M2Step;
     constexpr int kLoads = kRowBlocks / 2;
     const int64_t kb = (p.cols + kF8Block - 1) / kF8Block;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const F8Quant p, bool v
             float a = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(f[j]));
-            const float s = block_scale(half_warp_max(a), M);   // every lane takes part in the shuffles
+            const float s = block_scale(half_warp_max(a), kStep);   // every lane takes part in the shuffles
             const float inv = __frcp_rn(s);
             if (b < kb) {
                 store8_bytes(q, c, p.cols, qvec, f8x4<F8>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const F8Quant p, bool
     __shared__ float red[8];
     pdl_launch_dependents();
     pdl_wait();
-    constexpr float M = F8 == GEMM_F8_E4M3 ? kE4M3Max : kE5M2Max;
+    constexpr float kStep = F8 == GEMM_F8_E4M3 ? kE4M3Step : kE5M2Step;
     const int64_t kb = (p.cols + kF8Block - 1) / kF8Block;
     const int64_t rb = blockIdx.x / kb, b = blockIdx.x - rb * kb;
     const int64_t c = b * kF8Block + (threadIdx.x & 15) * 8;
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const F8Quant p, bool
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) a = fmaxf(a, red[i]);
-    const float s = block_scale(a, M);
+    const float s = block_scale(a, kStep);
     const float inv = __frcp_rn(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const F8Quant p, bool v
     __shared__ __align__(16) float inverse[kF8Block];
     pdl_launch_dependents();
     pdl_wait();
-    constexpr float M = F8 == GEMM_F8_E4M3 ? kE4M3Max : kE5M2Max;
+    constexpr float kStep = F8 == GEMM_F8_E4M3 ? kE4M3Step : kE5M2Step;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kF8Block;
     for (int pb = blockIdx.y; pb < p.kp / kF8Block; pb += gridDim.y) {
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const F8Quant p, bool v
             float a = 0.f;
 #pragma unroll
             for (int w = 0; w < 8; ++w) a = fmaxf(a, red[w][threadIdx.x]);
-            const float s = block_scale(a, M);
+            const float s = block_scale(a, kStep);
             inverse[threadIdx.x] = __frcp_rn(s);
             if (c0 + threadIdx.x < p.cols) p.scale[static_cast<int64_t>(pb) * p.cols + c0 + threadIdx.x] = s;
         }

@@ -263,9 +263,10 @@ GEMM_API gemm_status gemm_bf16_run_host(const gemm_plan *plan, const uint16_t *A
  *                      block-major: scale[b * rows + i], b < ceil(k / 128);
  *   GEMM_SCALE_BLOCKS  one scale per 128 x 128 block, stored
  *                      scale[(j / 128) * ceil(k / 128) + b].
- * Quantising takes scale = max(amax / M, 2^-126), amax the block's largest
- * magnitude and M the type's largest value, and rounds x * (1 / scale) to the
- * nearest 8-bit value, ties to even; each step is one fp32 operation.  A
+ * Quantising takes scale = max(amax * (1 / M), 2^-126), amax the block's
+ * largest magnitude and M the type's largest value, and rounds x * (1 / scale)
+ * to the nearest 8-bit value, ties to even; each step, 1 / M among them, is
+ * one fp32 operation.  A
  * block of zeros gets the scale 2^-126.  An infinity in a block makes its
  * scale infinite, its own 8-bit value NaN and the block's others zero, so
  * every product that reads the block is NaN; a NaN element is a NaN of the
@@ -409,8 +410,8 @@ GEMM_API int64_t gemm_f8_padded_k(int64_t rows, int32_t groups);
  *   rstd = 1 / sqrt(mean_j(h_j^2) + eps)   (fp32)
  *   y_j  = h_j * rstd * W[j]
  * gemm_norm_f8 writes y as e4m3 with GEMM_SCALE_ROWS scales, ready as A of
- * gemm_f8_run.  gemm_norm_i8 writes int8 with one scale per row, scale =
- * max(amax / 127, 2^-126), nearest integer, ties to even: ready as A and
+ * gemm_f8_run.  gemm_norm_i8 writes int8 with one scale per row (M = 127),
+ * nearest integer, ties to even: ready as A and
  * row_scale of gemm_i8_run_requant; a row whose mean square is infinite or
  * NaN has a NaN scale.  H (may be NULL if R is NULL) gets h and may be X or R itself (with
  * that one's pitch); rstd (rows floats, may be NULL) is kept for the

@@ -68,7 +68,8 @@ def padded_starts(sizes):
 
 def scale_of(amax, dtype):
     """fp32 scale of a block (fp32 arithmetic, as the operator is defined)."""
-    return torch.clamp_min(amax.float() / torch.tensor(MAXIMUM[dtype] if dtype in MAXIMUM else 127.0), SCALE_MIN)
+    step = torch.tensor(1.0) / torch.tensor(MAXIMUM[dtype])   # the reciprocal, rounded to fp32
+    return torch.clamp_min(amax.float() * step, SCALE_MIN)
 
 
 def quantised(x, scale_full, dtype):
