@@ -209,6 +209,46 @@ __device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[N]
     }
 }
 
+// The fragment form, for tiles whose columns have scales of their own.  With
+// lane = row every lane would need every column's scale, and handing 128 of
+// them to each lane of eight warps takes shared memory's way into the
+// registers longer than the block's MMAs (1024 cycles of 128 bytes).
+// tcgen05.ld's 16x128b shape gives a lane four rows (lane / 4 + 0, 8, 16, 24)
+// and every fourth column (lane % 4), so it needs a quarter of them; it reads
+// at half the rate of 32x32b (16x256b, with pairs of columns, at a quarter).
+// v: 32 columns, [half of the rows][four columns][row + 0, 8].
+__device__ __forceinline__ void load_tmem_frag(uint32_t taddr, uint32_t (&v)[32]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x128b.x8.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(v[16 * h]), "=r"(v[16 * h + 1]), "=r"(v[16 * h + 2]), "=r"(v[16 * h + 3]), "=r"(v[16 * h + 4]),
+              "=r"(v[16 * h + 5]), "=r"(v[16 * h + 6]), "=r"(v[16 * h + 7]), "=r"(v[16 * h + 8]), "=r"(v[16 * h + 9]),
+              "=r"(v[16 * h + 10]), "=r"(v[16 * h + 11]), "=r"(v[16 * h + 12]), "=r"(v[16 * h + 13]),
+              "=r"(v[16 * h + 14]), "=r"(v[16 * h + 15])
+            : "r"(taddr + (static_cast<uint32_t>(16 * h) << 16)));
+}
+// Column scales of a tile in shared memory are ordered so that a lane reads
+// four of its columns at once: within sixteen columns, column c is at place
+// frag_place(c).
+__device__ __forceinline__ int frag_place(int c) { return (c & ~15) + (c & 3) * 4 + ((c >> 2) & 3); }
+// s: the lane's row scales (rows + 0 and + 8, + 16 and + 24); c: the scales of
+// its eight columns.  acc: [four columns][half of the rows].
+__device__ __forceinline__ void add_scaled_frag(uint64_t* acc, const uint32_t (&v)[32], const uint64_t (&s)[2],
+                                                const uint4 (&c)[2]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint4 x = c[j >> 2];
+        const uint32_t y = (j & 3) == 0 ? x.x : (j & 3) == 1 ? x.y : (j & 3) == 2 ? x.z : x.w;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = 16 * h + 2 * j;
+            acc[2 * j + h] = fma2(pair_of(v[i], v[i + 1]), mul2(s[h], pair_of(y, y)), acc[2 * j + h]);
+        }
+    }
+}
+
 // Four bytes from global to shared memory without waiting (zero if !in).
 __device__ __forceinline__ void copy4_async(uint32_t dst, const float* src, bool in) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)),
@@ -237,10 +277,11 @@ __device__ __forceinline__ void more_registers() {
 // 128 bytes per row: through the warp's 4 KiB staging buffer (16-byte chunks
 // swizzled by row & 7, free of bank conflicts both ways), so that eight lanes
 // write one row's 128 bytes.  All of a slice is read back before the first
-// store, as each would wait for its own read otherwise.  row0: D's row of lane
-// 0; rows at or past row_end and columns at or past n are not written.
+// store, as each would wait for its own read otherwise.  acc: pairs of columns
+// of the lane's row, or (FRAG) the fragment form.  row0: D's row of the warp's
+// first; rows at or past row_end and columns at or past n are not written.
 constexpr int kStageRowsBytes = 32 * 128;
-template <bool F32, int C>
+template <bool F32, bool FRAG, int C>
 __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_t stg, int lane, uint8_t* D, int64_t ldd,
                                            int64_t row0, int64_t row_end, int col0, int n, bool vec) {
     constexpr int W = F32 ? 32 : 64;   // columns per slice
@@ -253,20 +294,42 @@ __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_
     const bool whole = vec && n - col0 >= C;   // the warp's columns are all D's, and 16-byte aligned
 #pragma unroll
     for (int s = 0; s < C / W; ++s) {
-        uint32_t r[32];
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            float a, b;
-            unpair(acc[s * W / 2 + i], a, b);
-            if constexpr (F32) {
-                r[2 * i] = __float_as_uint(a);
-                r[2 * i + 1] = __float_as_uint(b);
-            } else {
-                r[i] = bf16x2(a, b);
-            }
-        }
         __syncwarp();   // the slice before has been read out
-        stage_rows32(stg, lane, r);
+        if constexpr (FRAG) {
+#pragma unroll
+            for (int j = 0; j < W / 4; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[2];
+                    unpair(acc[(s * (W / 4) + j) * 2 + h], x[0], x[1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int rr = (lane >> 2) + 16 * h + 8 * k;
+                        const int at = (4 * j + (lane & 3)) * ES;   // byte in the row's 128
+                        const uint32_t p = stg + rr * 128 + (((at >> 4) ^ (rr & 7)) << 4) + (at & 15);
+                        if constexpr (F32)
+                            st_shared_u32(p, __float_as_uint(x[k]));
+                        else
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(p),
+                                         "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x[k])))
+                                         : "memory");
+                    }
+                }
+        } else {
+            uint32_t r[32];
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+                float a, b;
+                unpair(acc[s * W / 2 + i], a, b);
+                if constexpr (F32) {
+                    r[2 * i] = __float_as_uint(a);
+                    r[2 * i + 1] = __float_as_uint(b);
+                } else {
+                    r[i] = bf16x2(a, b);
+                }
+            }
+            stage_rows32(stg, lane, r);
+        }
         __syncwarp();
         uint4 v[8];
         if (whole)

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         at.next();
                     }
                     ++n;
-                    const uint32_t dst = sScale + slot.i * R::SLOT + 4 * lane;
+                    const uint32_t slot_at = sScale + slot.i * R::SLOT, dst = slot_at + 4 * lane;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const bool in = row0 + 32 * i < p.rows_a;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < BN / 32; ++i) {
                             const bool in = w.col + lane + 32 * i < p.n;
-                            copy4_async(dst + 512 + 128 * i, in ? sb + 32 * i : p.b_scale, in);
+                            copy4_async(slot_at + 512 + 4 * frag_place(lane + 32 * i), in ? sb + 32 * i : p.b_scale, in);
                         }
                         sb += p.rows_b;
                     } else {
@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t stg = sEpi + e * kStageRowsBytes;
         const uint32_t acce = peer_address(acce0, 0);
         const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kCols;
-        const uint32_t row_scale = sScale + 4 * (q * 32 + lane);
+        // the lane's row, or the first of its four (eight rows apart)
+        const uint32_t row_scale = sScale + 4 * (q * 32 + (BROWS ? lane >> 2 : lane));
         const uint32_t col_scale = sScale + 512 + (BROWS ? h * kCols * 4 : (h * kCols / kF8Block) * 4);
         Turn<kStages> st;
         Turn<kBufs> buf;
@@ -306,32 +307,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t acc[kCols / 2];   // pairs of columns
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
-            // One chunk of columns is added while the next is on its way, the
-            // first of the next block included.  With column scales the chunk
-            // is half as wide, for the registers that hold them.  Order
-            // matters: what goes through the shared-memory queue behind a TMEM
-            // load waits for it, so scales are asked for first.
-            constexpr int kChunk = BROWS ? 16 : 32;
-            constexpr int kChunks = kCols / kChunk;
-            uint32_t v[2][kChunk];
-            uint4 sc[2][kChunk / 4];
-            float sa = 0.f, sb = 1.f;
+            // One chunk of 32 columns is added while the next is on its way,
+            // the first of the next block included.  Order matters: what goes
+            // through the shared-memory queue behind a TMEM load waits for it,
+            // so scales are asked for first.
+            constexpr int kChunks = kCols / 32;
+            uint32_t v[2][32];
+            uint4 sc[2][2];
+            float sa[BROWS ? 4 : 1], sb = 1.f;
+            uint64_t s2[2];
             auto chunk = [&](int c, uint32_t cols, uint32_t taddr) {
-                if constexpr (BROWS)
+                if constexpr (BROWS) {
 #pragma unroll
-                    for (int i = 0; i < kChunk / 4; ++i) sc[c & 1][i] = ld_shared_v4(cols + (c * kChunk + 4 * i) * 4);
-                load_tmem(taddr + c * kChunk, v[c & 1]);
+                    for (int i = 0; i < 2; ++i) sc[c & 1][i] = ld_shared_v4(cols + (c * 32 + i * 16 + (lane & 3) * 4) * 4);
+                    load_tmem_frag(taddr + c * 32, v[c & 1]);
+                } else {
+                    tmem_ld_32x32b_x32(taddr + c * 32, v[c & 1]);
+                }
             };
-            auto add = [&](int c, uint64_t s2) {
+            auto add = [&](int c) {
                 if constexpr (BROWS)
-                    add_scaled<kChunk>(acc + c * (kChunk / 2), v[c & 1], s2, sc[c & 1]);
+                    add_scaled_frag(acc + c * 16, v[c & 1], s2, sc[c & 1]);
                 else
-                    add_scaled<kChunk>(acc + c * (kChunk / 2), v[c & 1], s2);
+                    add_scaled<32>(acc + c * 16, v[c & 1], s2[0]);
             };
             auto first_chunk = [&] {   // of the block that st, buf and slot point to
                 tc_fence_after();
                 const uint32_t cols = col_scale + slot.i * R::SLOT;
-                sa = ld_shared_f32(row_scale + slot.i * R::SLOT);
+#pragma unroll
+                for (int k = 0; k < (BROWS ? 4 : 1); ++k) sa[k] = ld_shared_f32(row_scale + slot.i * R::SLOT + 32 * k);
                 if constexpr (!BROWS) sb = ld_shared_f32(cols);
                 chunk(0, cols, t0 + buf.i * BN);
             };
@@ -347,12 +351,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 buf.next();
                 slot.next();
                 wait_tmem(v[0]);
-                const float s = BROWS ? sa : sa * sb;
-                const uint64_t s2 = pair_of(__float_as_uint(s), __float_as_uint(s));
+                if constexpr (BROWS) {
+                    s2[0] = pair_of(__float_as_uint(sa[0]), __float_as_uint(sa[1]));
+                    s2[1] = pair_of(__float_as_uint(sa[2]), __float_as_uint(sa[3]));
+                } else {
+                    const uint32_t s = __float_as_uint(sa[0] * sb);
+                    s2[0] = pair_of(s, s);
+                }
 #pragma unroll
                 for (int c = 0; c + 1 < kChunks; ++c) {
                     chunk(c + 1, cols, tb);
-                    add(c, s2);
+                    add(c);
                     wait_tmem(v[(c + 1) & 1]);
                 }
                 // all columns are in registers: the accumulator is free
@@ -364,14 +373,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     first_chunk();
                 }
-                add(kChunks - 1, s2);
+                add(kChunks - 1);
             }
             if (!ok) break;
             if (p.out_f32)
-                store_rows<true, kCols>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
+                store_rows<true, BROWS, kCols>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
                                  p.d_vec != 0);
             else
-                store_rows<false, kCols>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
+                store_rows<false, BROWS, kCols>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
                                   p.d_vec != 0);
         }
     }
