@@ -41,6 +41,9 @@ struct Config {
     static constexpr int EPI_WARPS = 4 * PARTS;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
     static constexpr int COLS = NT / PARTS;
+    // 32 columns per thread and more: TMEM read as fragments, so that a lane
+    // needs the scales of eight columns instead of 32 (f8_tc.cuh)
+    static constexpr bool FRAG = COLS == 32;
     static constexpr int A_BYTES = NT * kF8RowBytes;
     static constexpr int STAGE = kWBytes + A_BYTES;
     static constexpr int STAGES = NT <= 32 ? 5 : NT == 64 ? 4 : 6;   // NT = 128: one CTA per SM, by registers
@@ -217,12 +220,14 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
         for (int n = 0; n < blocks; ++n) {
             if (!wait_warp(used0 + 8u * slot.i, slot.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutProducer)) break;
             const int64_t kb = kb_lo + n;
-            const uint32_t dst = sScale + slot.i * R::SLOT + 4 * lane;
+            const uint32_t slot_at = sScale + slot.i * R::SLOT, dst = slot_at + 4 * lane;
 #pragma unroll
             for (int i = 0; i < (NT + 31) / 32; ++i) {
                 const int r = arow + lane + 32 * i;
                 const bool in = r < p.rows_a;
-                if (NT >= 32 || lane < NT) copy4_async(dst + 128 * i, in ? p.a_scale + kb * p.rows_a + r : p.a_scale, in);
+                const int c = lane + 32 * i;
+                if (NT >= 32 || lane < NT)
+                    copy4_async(slot_at + 4 * (R::FRAG ? frag_place(c) : c), in ? p.a_scale + kb * p.rows_a + r : p.a_scale, in);
             }
             if constexpr (BROWS) {
 #pragma unroll
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
                     copy4_async(dst + NT * 4 + 128 * i, in ? p.b_scale + kb * p.rows_b + brow + lane + 32 * i : p.b_scale, in);
                 }
             } else if (lane == 0) {
-                copy4_async(dst + NT * 4, p.b_scale + static_cast<int64_t>(sblock) * p.kb + kb, true);
+                copy4_async(slot_at + NT * 4, p.b_scale + static_cast<int64_t>(sblock) * p.kb + kb, true);
             }
             copies_arrive(scale0 + 8u * slot.i);
             slot.next();
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
         copies_wait_all();
     } else if (warp >= 4) {
         // --------------------------------------------------- scale and add --
-        const int q = warp & 3, h = (warp - 4) >> 2;
+        const int q = warp & 3, h = (warp - 4) >> 2;   // lane quarter, part of the columns
         const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kCols;
         Turn<kStages> st;
         Turn<kBufs> buf;
@@ -250,16 +255,35 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
                 break;
             tc_fence_after();
             const uint32_t at = sScale + slot.i * R::SLOT;
-            const float s = ld_shared_f32(at + NT * 4 + (BROWS ? 4 * (q * 32 + lane) : 0));
             uint32_t v[kCols];
-            uint4 sc[kCols / 4];
+            if constexpr (R::FRAG) {
+                float s[4];
+                uint4 sc[2];
 #pragma unroll
-            for (int i = 0; i < kCols / 4; ++i) sc[i] = ld_shared_v4(at + (h * kCols + 4 * i) * 4);
-            load_tmem(t0 + buf.i * NT, v);
-            wait_tmem(v);
-            tc_fence_before();
-            if (lane == 0) mbar_arrive(acce0 + 8u * buf.i);
-            add_scaled<kCols>(acc, v, pair_of(__float_as_uint(s), __float_as_uint(s)), sc);
+                for (int k = 0; k < (BROWS ? 4 : 1); ++k)
+                    s[k] = ld_shared_f32(at + NT * 4 + (BROWS ? 4 * (q * 32 + (lane >> 2) + 8 * k) : 0));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) sc[i] = ld_shared_v4(at + (h * kCols + i * 16 + (lane & 3) * 4) * 4);
+                load_tmem_frag(t0 + buf.i * NT, v);
+                wait_tmem(v);
+                tc_fence_before();
+                if (lane == 0) mbar_arrive(acce0 + 8u * buf.i);
+                uint64_t s2[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    s2[i] = pair_of(__float_as_uint(s[BROWS ? 2 * i : 0]), __float_as_uint(s[BROWS ? 2 * i + 1 : 0]));
+                add_scaled_frag(acc, v, s2, sc);
+            } else {
+                const float s = ld_shared_f32(at + NT * 4 + (BROWS ? 4 * (q * 32 + lane) : 0));
+                uint4 sc[kCols / 4];
+#pragma unroll
+                for (int i = 0; i < kCols / 4; ++i) sc[i] = ld_shared_v4(at + (h * kCols + 4 * i) * 4);
+                load_tmem(t0 + buf.i * NT, v);
+                wait_tmem(v);
+                tc_fence_before();
+                if (lane == 0) mbar_arrive(acce0 + 8u * buf.i);
+                add_scaled<kCols>(acc, v, pair_of(__float_as_uint(s), __float_as_uint(s)), sc);
+            }
             __syncwarp();   // every lane has read the block's scales
             if (lane == 0) mbar_arrive(used0 + 8u * slot.i);
             st.next();
@@ -270,51 +294,51 @@ __global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
 
     // ------------------------------------------------------------ join, store --
     // The ring is idle: every block has been multiplied (or the call has failed).
-    const int n_col = col + (threadIdx.x & 127);   // this thread's column of D
-    auto put = [&](int r, float v) {               // row r of the tile
-        if (drow + r < drow + (arow_end - arow) && n_col < p.n) {
-            const int64_t at = (static_cast<int64_t>(drow) + r) * p.ldd + n_col;
+    // put(r, c, v): row r of A, row c of Bt.  each(f): f(r, c, v) of this thread's sums.
+    auto put = [&](int r, int c, float v) {
+        if (r < arow_end - arow && col + c < p.n) {
+            const int64_t at = (static_cast<int64_t>(drow) + r) * p.ldd + col + c;
             if (p.out_f32)
                 static_cast<float*>(p.D)[at] = v;
             else
                 static_cast<__nv_bfloat16*>(p.D)[at] = __float2bfloat16_rn(v);
         }
     };
-    if (split == 1) {
-        if (warp >= 4) {
-            const int h = (warp - 4) >> 2;
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    auto each = [&](auto f) {
 #pragma unroll
-            for (int j = 0; j < kCols / 2; ++j) {
-                float a, b;
-                unpair(acc[j], a, b);
-                put(h * kCols + 2 * j, a);
-                put(h * kCols + 2 * j + 1, b);
+        for (int j = 0; j < kCols / 2; ++j) {
+            float x, y;
+            unpair(acc[j], x, y);
+            if constexpr (R::FRAG) {
+                const int r = h * kCols + 4 * (j >> 1) + (lane & 3), c = q * 32 + (lane >> 2) + 16 * (j & 1);
+                f(r, c, x);
+                f(r, c + 8, y);
+            } else {
+                f(h * kCols + 2 * j, q * 32 + lane, x);
+                f(h * kCols + 2 * j + 1, q * 32 + lane, y);
             }
         }
+    };
+    if (split == 1) {
+        if (warp >= 4) each(put);
     } else {
         // Row r of A is finished by CTA r / share, whose ring (idle in every
-        // CTA after the first barrier) holds sums[sender][row][row of Bt]; a
-        // warp's store is 128 contiguous bytes.
-        const int c = threadIdx.x & 127, h = (warp - 4) >> 2;
-        const int share = NT / split;
+        // CTA after the first barrier) holds sums[sender][row][row of Bt].
+        const int share = NT / split, shift = 31 - __clz(share);   // a power of two
+        cluster_barrier();
+        if (warp >= 4)
+            each([&](int r, int c, float v) {
+                const int owner = r >> shift;
+                st_cluster_f32(peer_address(base + ((rank * share + r - owner * share) * kTileRows + c) * 4, owner), v);
+            });
         cluster_barrier();
         if (warp >= 4) {
-#pragma unroll
-            for (int j = 0; j < kCols / 2; ++j) {
-                float x, y;
-                unpair(acc[j], x, y);   // rows 2j and 2j + 1: an even share keeps them together
-                const int r = h * kCols + 2 * j, owner = r / share;
-                const uint32_t at = peer_address(base + ((rank * share + r - owner * share) * kTileRows + c) * 4, owner);
-                st_cluster_f32(at, x);
-                st_cluster_f32(at + kTileRows * 4, y);
-            }
-        }
-        cluster_barrier();
-        if (warp >= 4) {
+            const int c = threadIdx.x & 127;
             for (int r = h; r < share; r += R::EPI_WARPS / 4) {
                 float v = 0.f;
                 for (int s = 0; s < split; ++s) v += ld_shared_f32(base + ((s * share + r) * kTileRows + c) * 4);
-                put(share * rank + r, v);
+                put(share * rank + r, c, v);
             }
         }
     }

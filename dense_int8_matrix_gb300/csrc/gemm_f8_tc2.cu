@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t v[2][32];
             uint4 sc[2][2];
             float sa[BROWS ? 4 : 1], sb = 1.f;
-            uint64_t s2[2];
+            uint64_t s2[2] = {0, 0};
             auto chunk = [&](int c, uint32_t cols, uint32_t taddr) {
                 if constexpr (BROWS) {
 #pragma unroll
