@@ -46,14 +46,18 @@ struct Config {
     static constexpr bool FRAG = COLS == 32;
     static constexpr int A_BYTES = NT * kF8RowBytes;
     static constexpr int STAGE = kWBytes + A_BYTES;
-    static constexpr int STAGES = NT <= 32 ? 5 : NT == 64 ? 4 : 6;   // NT = 128: one CTA per SM, by registers
+    // The ring covers the latency of Bt: two CTAs per SM with five stages each,
+    // or one with 192 KiB (NT = 64, 64 x 8192 x 8192 on GB300: two CTAs with
+    // four stages 19.8 us, one with eight 16.2 us)
+    static constexpr int STAGES = NT <= 32 ? 5 : NT == 64 ? 8 : 6;
     static constexpr int BUFS = 4;                     // TMEM accumulators: the epilogue's latency spans several blocks
     static constexpr int TMEM = NT * BUFS < 32 ? 32 : NT * BUFS;
     static constexpr int SLOTS = 8;                     // blocks whose scales are in shared memory
     static constexpr int SLOT = NT * 4 + (BROWS ? kTileRows * 4 : 16);
+    static constexpr int PER_SM = NT >= 64 ? 1 : 2;   // for the registers
     static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + SLOTS * SLOT + kPreBytes + kCtrlBytes + 1024;
     static_assert(STAGES * STAGE >= NT * kTileRows * 4, "the sums of a split tile fit in the ring");
-    static_assert(SMEM <= (NT == 128 ? 227 : 113) * 1024 && SMEM > 24 * 1024, "one or two CTAs per SM");
+    static_assert(SMEM <= (PER_SM == 1 ? 227 : 113) * 1024 && SMEM > 24 * 1024, "one or two CTAs per SM");
 };
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
@@ -61,7 +65,7 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 }
 
 template <int NT, bool BROWS>
-__global__ void __launch_bounds__(Config<NT, BROWS>::THREADS)
+__global__ void __launch_bounds__(Config<NT, BROWS>::THREADS, Config<NT, BROWS>::PER_SM)
     f8_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const F8Params p,
                      const uint32_t idesc, const int split) {
     using R = Config<NT, BROWS>;
