@@ -60,6 +60,7 @@ struct Vec8<__nv_bfloat16> {
         }
         u = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    __device__ __forceinline__ void words(const uint32_t (&w)[4]) { u = make_uint4(w[0], w[1], w[2], w[3]); }
     __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
@@ -74,6 +75,10 @@ struct Vec8<float> {
     __device__ __forceinline__ void set(const float (&f)[8]) {
         a = make_float4(f[0], f[1], f[2], f[3]);
         b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ void words(const uint32_t (&w)[8]) {
+        a = make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
+        b = make_float4(__uint_as_float(w[4]), __uint_as_float(w[5]), __uint_as_float(w[6]), __uint_as_float(w[7]));
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void load(const float* p) {
@@ -91,13 +96,43 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float x, float* p) { *p = x; }
 __device__ __forceinline__ void from_f32(float x, __nv_bfloat16* p) { *p = __float2bfloat16_rn(x); }
 
-// Elements [c, c + 8) of a row of d; those at or past d are zero.  vec: the
-// row is aligned for whole-vector access.
-template <typename T>
-__device__ __forceinline__ Vec8<T> load8(const T* row, int64_t c, int64_t d, bool vec) {
+// N words from byte `sh` (a multiple of 2 below 16) of the N + 4 words `in`.
+template <int N>
+__device__ __forceinline__ void shift_words(const uint32_t (&in)[N + 4], int sh, uint32_t (&out)[N]) {
+    uint32_t t[N + 4];
+#pragma unroll
+    for (int i = 0; i < N + 4; ++i) t[i] = in[i];
+#pragma unroll
+    for (int i = 0; i + 1 < N + 4; ++i) t[i] = sh & 4 ? t[i + 1] : t[i];
+#pragma unroll
+    for (int i = 0; i + 2 < N + 4; ++i) t[i] = sh & 8 ? t[i + 2] : t[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = __byte_perm(t[i], t[i + 1], sh & 2 ? 0x5432u : 0x3210u);
+}
+
+// Elements [c, c + 8) of a row of d; those at or past d are zero.  VEC: the
+// row is aligned for whole-vector access (a template parameter, as the code
+// for unaligned rows costs aligned ones registers: 8192 x 8192 forward norm 79
+// us alone, 117 us with both in one kernel).  Otherwise the aligned 16-byte words
+// around the elements are read and shifted together, where all of them lie
+// inside the row; its ends are read element by element.
+template <bool VEC, typename T>
+__device__ __forceinline__ Vec8<T> load8(const T* row, int64_t c, int64_t d) {
     Vec8<T> v;
-    if (vec && c + 8 <= d) {
+    if (VEC && c + 8 <= d) {
         v.load(row + c);
+    } else if (!VEC && c >= 8 && c + 16 <= d) {
+        constexpr int N = sizeof(Vec8<T>) / 4;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+        const uint4* p = reinterpret_cast<const uint4*>(at & ~static_cast<uintptr_t>(15));
+        uint32_t in[N + 4], out[N];
+#pragma unroll
+        for (int i = 0; i < N / 4 + 1; ++i) {
+            const uint4 x = p[i];
+            in[4 * i] = x.x; in[4 * i + 1] = x.y; in[4 * i + 2] = x.z; in[4 * i + 3] = x.w;
+        }
+        shift_words<N>(in, static_cast<int>(at & 15), out);
+        v.words(out);
     } else {
         float f[8];
 #pragma unroll
@@ -106,17 +141,54 @@ __device__ __forceinline__ Vec8<T> load8(const T* row, int64_t c, int64_t d, boo
     }
     return v;
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* row, int64_t c, int64_t d, bool vec, const Vec8<T>& v) {
-    if (vec && c + 8 <= d) {
-        v.store(row + c);
-    } else {
-        float f[8];
-        v.get(f);
+
+// The same, stored.  Called by whole warps whose lanes hold neighbouring
+// vectors.  An unaligned bfloat16 row is written in aligned 16-byte words, each
+// made of the end of the lane's left neighbour and the start of its own
+// vector; the pieces that have no such word (at the warp's and the row's ends)
+// go element by element.
+template <bool VEC, typename T>
+__device__ __forceinline__ void store8(T* row, int64_t c, int64_t d, const Vec8<T>& v) {
+    if constexpr (VEC) {
+        if (c + 8 <= d) {
+            v.store(row + c);
+            return;
+        }
+    } else if constexpr (sizeof(T) == 2) {
+        const int lane = threadIdx.x & 31;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row) + c * 2;
+        const int sh = static_cast<int>(at & 15);   // the same in every lane
+        uint32_t in[8], out[4];
+        in[4] = v.u.x; in[5] = v.u.y; in[6] = v.u.z; in[7] = v.u.w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < d) from_f32(f[i], row + c + i);
+        for (int i = 0; i < 4; ++i) in[i] = __shfl_up_sync(0xffffffffu, in[4 + i], 1);
+        const bool whole = c + 8 <= d;
+        if (sh == 0) {
+            if (whole) {
+                v.store(row + c);
+                return;
+            }
+        } else if (whole) {
+            const bool word = lane > 0;   // its left neighbour holds the columns before c
+            if (word) {
+                shift_words<4>(in, 16 - sh, out);
+                *reinterpret_cast<uint4*>(at - sh) = make_uint4(out[0], out[1], out[2], out[3]);
+            }
+            const int first = word ? 8 - sh / 2 : 0;                         // elements not in that word ...
+            const int last = lane == 31 || c + 16 > d ? 8 : 8 - sh / 2;      // ... nor in the right neighbour's
+            float f[8];
+            v.get(f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= first && i < last) from_f32(f[i], row + c + i);
+            return;
+        }
     }
+    float f[8];
+    v.get(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < d) from_f32(f[i], row + c + i);
 }
 // Eight bytes (two words) to elements [c, c + 8) of a byte row of d.
 __device__ __forceinline__ void store8_bytes(uint8_t* row, int64_t c, int64_t d, bool vec, uint32_t lo, uint32_t hi) {

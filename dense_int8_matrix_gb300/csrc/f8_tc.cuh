@@ -128,26 +128,6 @@ __device__ __forceinline__ int group_of(const int32_t* pre, int groups, int i) {
     return lo;
 }
 
-// Four words of D to columns [c, c + 4 words) of a row; `out` is the row's
-// address of column c, `left` the columns of D from c on.
-template <bool F32>
-__device__ __forceinline__ void store_d16(void* out, int left, bool vec, const uint4 v) {
-    constexpr int N = F32 ? 4 : 8;
-    if (vec && left >= N) {
-        *static_cast<uint4*>(out) = v;
-        return;
-    }
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (i >= left) break;
-        if constexpr (F32)
-            static_cast<uint32_t*>(out)[i] = w[i];
-        else
-            static_cast<uint16_t*>(out)[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-    }
-}
-
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&p);
@@ -292,6 +272,7 @@ __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_
     uint8_t* out = D + ((row0 + r0) * ldd + col0 + part * (16 / ES)) * ES;
     const int64_t step = 4 * ldd * ES;
     const bool whole = vec && n - col0 >= C;   // the warp's columns are all D's, and 16-byte aligned
+    const bool pairs = ldd % 2 == 0 && reinterpret_cast<uintptr_t>(D) % 4 == 0;
 #pragma unroll
     for (int s = 0; s < C / W; ++s) {
         __syncwarp();   // the slice before has been read out
@@ -340,11 +321,26 @@ __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_
             for (int j = 0; j < 8; ++j)
                 if (4 * j + r0 < rows) *reinterpret_cast<uint4*>(out + j * step + s * W * ES) = v[j];
         } else {
-            const int left = n - (col0 + s * W + part * (16 / ES));
-#pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
-                const uint4 x = ld_shared_v4(stg + (4 * j + r0) * 128 + ((part ^ ((4 * j + r0) & 7)) << 4));
-                if (4 * j + r0 < rows && left > 0) store_d16<F32>(out + j * step + s * W * ES, left, vec, x);
+            // ragged columns or unaligned rows: one row at a time, so that every
+            // store is contiguous
+            const int c = col0 + s * W;
+            uint8_t* to = D + (row0 * ldd + c) * ES;
+#pragma unroll 4
+            for (int rr = 0; rr < 32; ++rr) {
+                const uint32_t x = ld_shared_u32(stg + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
+                if (rr >= rows) continue;
+                if constexpr (F32) {
+                    if (c + lane < n) reinterpret_cast<uint32_t*>(to)[rr * ldd + lane] = x;
+                } else if (pairs) {   // rows are 4-byte aligned: both columns of the word at once
+                    if (c + 2 * lane + 1 < n)
+                        reinterpret_cast<uint32_t*>(to + rr * ldd * 2)[lane] = x;
+                    else if (c + 2 * lane < n)
+                        reinterpret_cast<uint16_t*>(to)[rr * ldd + 2 * lane] = static_cast<uint16_t>(x);
+                } else {
+                    uint16_t* o = reinterpret_cast<uint16_t*>(to) + rr * ldd + 2 * lane;
+                    if (c + 2 * lane < n) o[0] = static_cast<uint16_t>(x);
+                    if (c + 2 * lane + 1 < n) o[1] = static_cast<uint16_t>(x >> 16);
+                }
             }
         }
     }

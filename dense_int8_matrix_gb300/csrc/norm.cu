@@ -30,8 +30,8 @@ __device__ __forceinline__ float cta_reduce(float v, float* red) {
 // thread, vector v of thread t at column 8 * (v * blockDim + t), so sixteen
 // neighbouring lanes hold one block of 128 columns).  The mean square is
 // taken of h as it is stored.
-template <typename T, int V, bool I8>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool vec, bool qvec, bool wvec) {
+template <typename T, int V, bool I8, bool VEC>
+__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool qvec, bool wvec) {
     __shared__ float red[2][32];
     pdl_launch_dependents();
     pdl_wait();
@@ -43,11 +43,11 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool ve
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x);
-        h[v] = load8(x, c, p.d, vec);
+        h[v] = load8<VEC>(x, c, p.d);
         if (r) {
             float a[8], b[8];
             h[v].get(a);
-            load8(r, c, p.d, vec).get(b);
+            load8<VEC>(r, c, p.d).get(b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) a[i] += b[i];
             h[v].set(a);
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool ve
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int64_t c = 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x);
-        if (p.H) store8(static_cast<T*>(p.H) + row * p.ldh, c, p.d, vec, h[v]);
+        if (p.H) store8<VEC>(static_cast<T*>(p.H) + row * p.ldh, c, p.d, h[v]);
         float a[8];
         h[v].get(a);
 #pragma unroll
@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool ve
 // (eight per vector), and dw's running sums of the CTA's rows stay in shared
 // memory, one word per thread and column so that no two lanes share a bank.
 // They go to `partial`, which dw_reduce_kernel adds up in CTA order.
-template <typename T, int V>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool vec, bool wvec) {
+template <typename T, int V, bool VEC>
+__global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool wvec) {
     extern __shared__ float dw[];   // [V * 8][threads]
     __shared__ float red[2][32];
     pdl_launch_dependents();
@@ -136,10 +136,10 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool ve
         x.rstd = __ldg(p.rstd + row);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            x.dy[v] = load8(static_cast<const T*>(p.dY) + row * p.lddy, column(v), p.d, vec);
-            x.h[v] = load8(static_cast<const T*>(p.H) + row * p.ldh, column(v), p.d, vec);
+            x.dy[v] = load8<VEC>(static_cast<const T*>(p.dY) + row * p.lddy, column(v), p.d);
+            x.h[v] = load8<VEC>(static_cast<const T*>(p.H) + row * p.ldh, column(v), p.d);
             if (p.dR)
-                x.dr[v] = load8(static_cast<const T*>(p.dR) + row * p.lddr, column(v), p.d, vec);
+                x.dr[v] = load8<VEC>(static_cast<const T*>(p.dR) + row * p.lddr, column(v), p.d);
             else
                 x.dr[v].zero();
         }
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool ve
             }
             Vec8<T> out;
             out.set(o);
-            store8(static_cast<T*>(p.dX) + row * p.lddx, column(v), p.d, vec, out);
+            store8<VEC>(static_cast<T*>(p.dX) + row * p.lddx, column(v), p.d, out);
         }
         if (row + gridDim.x < p.rows) fetch(row + gridDim.x, x);
     }
@@ -190,15 +190,24 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool ve
     }
 }
 
-// The same for aligned bfloat16 rows of at most 1024 vectors, as training has
-// them: w and dw's running sums stay in registers (512 threads
-// at most, V vectors each), and the rows come through a ring in shared memory,
-// copied several rows ahead by one thread (bulk copies of whole rows, so that
-// up to 200 KB per SM are on their way).
+// The same for bfloat16 rows of at most 1024 vectors, as training has them: w
+// and dw's running sums stay in registers (512 threads at most, V vectors
+// each), and the rows come through a ring in shared memory, copied several
+// rows ahead by one thread (bulk copies, up to 200 KB per SM on their way).
+// VEC: rows are 16-byte aligned and of whole vectors.  Otherwise a row is
+// copied with the 16-byte words that it shares with its neighbours and shifted
+// on the way to the registers; a row whose words would reach past the matrix
+// (the first or the last) is loaded without the ring.
 constexpr int kBwdThreads = 512;
 constexpr int kBwdRingBytes = 200 * 1024;
 constexpr int kBwdSlots = 8;
-template <int V>
+
+// Bytes of one array's row in a slot, and of a slot.
+__host__ __device__ inline uint32_t ring_row_bytes(int64_t d, bool vec) {
+    return static_cast<uint32_t>(vec ? d * 2 : (d * 2 + 15) / 16 * 16 + 32);   // + the shared words, + what the last shift reads
+}
+
+template <int V, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_ring_kernel(const NormBwd p, bool wvec, int slots, int* err) {
     using T = __nv_bfloat16;
     extern __shared__ __align__(16) uint8_t ring[];
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_ring_kernel(const Nor
     __shared__ __align__(8) uint64_t bars[kBwdSlots];
     __shared__ uint32_t abort_flag;
     const int threads = blockDim.x, t = threadIdx.x;
-    const uint32_t row_bytes = static_cast<uint32_t>(p.d) * 2;
+    const uint32_t row_bytes = ring_row_bytes(p.d, VEC);
     const uint32_t slot_bytes = row_bytes * (p.dR ? 3 : 2);
     const uint32_t ring0 = smem_u32(ring), bar0 = smem_u32(bars);
     if (t == 0) {
@@ -219,13 +228,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_ring_kernel(const Nor
     __syncthreads();
     auto column = [&](int v) { return 8 * (v * threads + t); };
     const int d = static_cast<int>(p.d);
+    const uintptr_t len = static_cast<uintptr_t>(d) * 2;
+    auto row_at = [&](const void* base, int64_t ld, int64_t row) { return reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * ld); };
+    // the 16-byte words of a row lie inside the matrix if 15 bytes before and
+    // behind it do: all rows but the first and the last few
+    int64_t least = p.lddy < p.ldh ? p.lddy : p.ldh;
+    if (p.dR && p.lddr < least) least = p.lddr;
+    const int64_t margin = (15 + 2 * least - 1) / (2 * least);
+    auto ringed = [&](int64_t row) { return VEC || (row >= margin && row < p.rows - margin); };
     // copies row `row` into slot s (one thread)
     auto copy_row = [&](int64_t row, int s) {
         const uint32_t bar = bar0 + 8u * s, dst = ring0 + s * slot_bytes;
-        mbar_arrive_expect_tx(bar, slot_bytes);
-        bulk_load(dst, static_cast<const T*>(p.dY) + row * p.lddy, row_bytes, bar);
-        bulk_load(dst + row_bytes, static_cast<const T*>(p.H) + row * p.ldh, row_bytes, bar);
-        if (p.dR) bulk_load(dst + 2 * row_bytes, static_cast<const T*>(p.dR) + row * p.lddr, row_bytes, bar);
+        if (!ringed(row)) {
+            mbar_arrive(bar);
+            return;
+        }
+        const uintptr_t a[3] = {row_at(p.dY, p.lddy, row), row_at(p.H, p.ldh, row), p.dR ? row_at(p.dR, p.lddr, row) : 0};
+        uint32_t n[3], all = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            n[i] = i < 2 || p.dR ? static_cast<uint32_t>(((a[i] + len + 15) & ~static_cast<uintptr_t>(15)) - (a[i] & ~static_cast<uintptr_t>(15))) : 0;
+            all += n[i];
+        }
+        mbar_arrive_expect_tx(bar, all);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (n[i]) bulk_load(dst + i * row_bytes, reinterpret_cast<const void*>(a[i] & ~static_cast<uintptr_t>(15)), n[i], bar);
     };
     const int64_t step = gridDim.x;
     if (t == 0)
@@ -248,22 +276,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_ring_kernel(const Nor
         // copy still lands in the ring before the CTA ends (see below)
         wait_bounded(bar0 + 8u * s, ph, &abort_flag, err, kDevErrTimeoutProducer);
         Vec8<T> dy[V], h[V], dr[V];
-        const uint8_t* src = ring + s * slot_bytes;
+        const bool in_ring = ringed(row);
+        auto take = [&](int array, const void* base, int64_t ld, int v, Vec8<T>& x) {
+            const uint8_t* src = ring + s * slot_bytes + array * row_bytes + column(v) * 2;
+            if (column(v) >= d) {
+                x.zero();
+            } else if (VEC) {
+                x.u = *reinterpret_cast<const uint4*>(src);
+            } else if (in_ring) {
+                const uint4 a = reinterpret_cast<const uint4*>(src)[0], b = reinterpret_cast<const uint4*>(src)[1];
+                const uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                uint32_t out[4];
+                shift_words<4>(in, static_cast<int>(row_at(base, ld, row) & 15), out);
+                if (column(v) + 8 > d) {   // what lies behind the row's end is not its own
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (column(v) + 2 * i >= d) out[i] = 0u;
+                        else if (column(v) + 2 * i + 1 >= d) out[i] &= 0xffffu;
+                    }
+                }
+                x.words(out);
+            } else {
+                x = load8<false>(reinterpret_cast<const T*>(row_at(base, ld, row)), column(v), d);
+            }
+        };
         float dot = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            if (column(v) < d) {
-                dy[v].u = *reinterpret_cast<const uint4*>(src + column(v) * 2);
-                h[v].u = *reinterpret_cast<const uint4*>(src + row_bytes + column(v) * 2);
-                if (p.dR)
-                    dr[v].u = *reinterpret_cast<const uint4*>(src + 2 * row_bytes + column(v) * 2);
-                else
-                    dr[v].zero();
-            } else {
-                dy[v].zero();
-                h[v].zero();
+            take(0, p.dY, p.lddy, v, dy[v]);
+            take(1, p.H, p.ldh, v, h[v]);
+            if (p.dR)
+                take(2, p.dR, p.lddr, v, dr[v]);
+            else
                 dr[v].zero();
-            }
             float a[8], x[8];
             dy[v].get(a);
             h[v].get(x);
@@ -292,7 +337,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_ring_kernel(const Nor
             }
             Vec8<T> out;
             out.set(o);
-            if (column(v) < d) out.store(static_cast<T*>(p.dX) + row * p.lddx + column(v));
+            store8<VEC>(static_cast<T*>(p.dX) + row * p.lddx, column(v), p.d, out);
         }
         if (++s == slots) {
             s = 0;
@@ -310,17 +355,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_ring_kernel(const Nor
     if (p.dW) {
         float* out = gridDim.x > 1 ? p.partial + static_cast<int64_t>(blockIdx.x) * p.d : p.dW;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (column(v) < d) {
-                float4* o = reinterpret_cast<float4*>(out + column(v));
-                if (reinterpret_cast<uintptr_t>(out) % 16 == 0) {
-                    o[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-                    o[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
-                } else {
+        for (int v = 0; v < V; ++v) {
+            float4* o = reinterpret_cast<float4*>(out + column(v));
+            if (column(v) + 8 <= d && reinterpret_cast<uintptr_t>(o) % 16 == 0) {
+                o[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+                o[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) out[column(v) + i] = dw[v][i];
-                }
+                for (int i = 0; i < 8; ++i)
+                    if (column(v) + i < d) out[column(v) + i] = dw[v][i];
             }
+        }
     }
 }
 
@@ -360,11 +405,10 @@ bool al16(const void* p, int64_t pitch_bytes) {
 
 // Threads and vectors per thread of a row of d elements.  Many rows at once
 // run best with two vectors per thread (8192 x 8192 bfloat16 on GB300: 1, 2 and
-// 4 vectors 92, 79 and 88 us); a few rows, or rows that are loaded element by
-// element, run sooner with one.
-void row_shape(int64_t rows, int64_t d, bool vec, int num_sms, int* threads, int* vecs) {
+// 4 vectors 92, 79 and 88 us); a few rows run sooner with one.
+void row_shape(int64_t rows, int64_t d, int num_sms, int* threads, int* vecs) {
     const int64_t nv = (d + 7) / 8;
-    int v = vec && rows > 2 * static_cast<int64_t>(num_sms) ? 2 : 1;
+    int v = rows > 2 * static_cast<int64_t>(num_sms) ? 2 : 1;
     while (v < 4 && (nv + v - 1) / v > 1024) v *= 2;
     *threads = static_cast<int>(((nv + v - 1) / v + 31) / 32 * 32);
     *vecs = v;
@@ -376,21 +420,25 @@ bool fwd_vec(const NormFwd& a) {
     return al16(a.X, a.ldx * es) && (!a.R || al16(a.R, a.ldr * es)) && (!a.H || al16(a.H, a.ldh * es));
 }
 
-template <typename T, int V>
-cudaError_t fwd_launch(const NormFwd& a, int threads, bool vec, cudaStream_t stream) {
+template <typename T, int V, bool VEC>
+cudaError_t fwd_launch(const NormFwd& a, int threads, cudaStream_t stream) {
     const bool qvec = reinterpret_cast<uintptr_t>(a.Q) % 8 == 0 && a.ldq % 8 == 0;
     const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0;
-    return launch_chained(a.to_i8 ? norm_fwd_kernel<T, V, true> : norm_fwd_kernel<T, V, false>,
-                          dim3(static_cast<unsigned>(a.rows)), threads, 0, stream, a, vec, qvec, wvec);
+    return launch_chained(a.to_i8 ? norm_fwd_kernel<T, V, true, VEC> : norm_fwd_kernel<T, V, false, VEC>,
+                          dim3(static_cast<unsigned>(a.rows)), threads, 0, stream, a, qvec, wvec);
+}
+
+template <typename T, bool VEC>
+cudaError_t fwd_aligned(const NormFwd& a, cudaStream_t stream) {
+    int t, v;
+    row_shape(a.rows, a.d, a.num_sms, &t, &v);
+    return v == 1 ? fwd_launch<T, 1, VEC>(a, t, stream) : v == 2 ? fwd_launch<T, 2, VEC>(a, t, stream)
+                                                                 : fwd_launch<T, 4, VEC>(a, t, stream);
 }
 
 template <typename T>
 cudaError_t fwd_type(const NormFwd& a, cudaStream_t stream) {
-    int t, v;
-    const bool vec = fwd_vec<T>(a);
-    row_shape(a.rows, a.d, vec, a.num_sms, &t, &v);
-    return v == 1 ? fwd_launch<T, 1>(a, t, vec, stream) : v == 2 ? fwd_launch<T, 2>(a, t, vec, stream)
-                                                                 : fwd_launch<T, 4>(a, t, vec, stream);
+    return fwd_vec<T>(a) ? fwd_aligned<T, true>(a, stream) : fwd_aligned<T, false>(a, stream);
 }
 
 // One vector per thread up to 8192 columns.
@@ -402,56 +450,68 @@ void bwd_shape(int64_t d, int* threads, int* vecs) {
     *vecs = v;
 }
 
-// Whether the ring kernel takes the call: aligned bfloat16 rows of whole
-// vectors, enough of them to fill the ring.
-bool bwd_ring(const NormBwd& a) {
-    return a.x_type == GEMM_DTYPE_BF16 && a.d % 8 == 0 && a.d <= 16 * kBwdThreads && a.rows > a.num_sms &&
-           al16(a.dY, a.lddy * 2) && al16(a.H, a.ldh * 2) && (!a.dR || al16(a.dR, a.lddr * 2)) && al16(a.dX, a.lddx * 2);
+// Whether the ring kernel takes the call: bfloat16 rows that fit its registers
+// and enough of them to fill its rings.
+bool bwd_ring(const NormBwd& a) { return a.x_type == GEMM_DTYPE_BF16 && a.d <= 16 * kBwdThreads && a.rows > a.num_sms; }
+
+template <typename T>
+bool bwd_vec(const NormBwd& a) {
+    const int64_t es = sizeof(T);
+    return al16(a.dY, a.lddy * es) && al16(a.H, a.ldh * es) && (!a.dR || al16(a.dR, a.lddr * es)) && al16(a.dX, a.lddx * es);
 }
+bool ring_vec(const NormBwd& a) { return a.d % 8 == 0 && bwd_vec<__nv_bfloat16>(a); }
 
 // Threads of a ring CTA, CTAs per SM (two vectors per thread take 128
 // registers) and rows in its ring.
 void ring_shape(const NormBwd& a, int* threads, int* per_sm, int* slots) {
-    const int64_t nv = a.d / 8;
+    const int64_t nv = (a.d + 7) / 8;
     const int v = nv <= kBwdThreads ? 1 : 2;
     *threads = static_cast<int>(((nv + v - 1) / v + 31) / 32 * 32);
     *per_sm = v == 1 ? 1024 / *threads : 1;
-    const int64_t fit = kBwdRingBytes / *per_sm / (a.d * 2 * (a.dR ? 3 : 2));
+    const int64_t fit = kBwdRingBytes / *per_sm / (static_cast<int64_t>(ring_row_bytes(a.d, ring_vec(a))) * (a.dR ? 3 : 2));
     *slots = static_cast<int>(fit < kBwdSlots ? fit : kBwdSlots);
 }
 
-template <int V>
+template <int V, bool VEC>
 cudaError_t ring_launch(const NormBwd& a, cudaStream_t stream) {
     int threads, per_sm, slots;
     ring_shape(a, &threads, &per_sm, &slots);
-    const auto kern = norm_bwd_ring_kernel<V>;
+    const auto kern = norm_bwd_ring_kernel<V, VEC>;
     const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), kBwdRingBytes, true);
     if (e != cudaSuccess) return e;
     return launch_chained(kern, dim3(static_cast<unsigned>(a.grid)), threads,
-                          static_cast<size_t>(slots) * static_cast<size_t>(a.d) * 2 * (a.dR ? 3 : 2), stream, a,
+                          static_cast<size_t>(slots) * ring_row_bytes(a.d, VEC) * (a.dR ? 3 : 2), stream, a,
                           reinterpret_cast<uintptr_t>(a.W) % 16 == 0, slots, a.err);
 }
 
-template <typename T, int V>
+template <typename T, int V, bool VEC>
 cudaError_t rows_launch(const NormBwd& a, int threads, cudaStream_t stream) {
-    const int64_t es = sizeof(T);
-    const bool vec = al16(a.dY, a.lddy * es) && al16(a.H, a.ldh * es) && (!a.dR || al16(a.dR, a.lddr * es)) &&
-                     al16(a.dX, a.lddx * es);
     const size_t smem = a.dW ? static_cast<size_t>(8 * V) * threads * 4 : 0;
-    const auto kern = norm_bwd_kernel<T, V>;
+    const auto kern = norm_bwd_kernel<T, V, VEC>;
     if (smem > 48 * 1024) {
         const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), GEMM_NORM_MAX_D * 4, false);
         if (e != cudaSuccess) return e;
     }
-    return launch_chained(kern, dim3(static_cast<unsigned>(a.grid)), threads, smem, stream, a, vec,
+    return launch_chained(kern, dim3(static_cast<unsigned>(a.grid)), threads, smem, stream, a,
                           reinterpret_cast<uintptr_t>(a.W) % 16 == 0);
+}
+
+template <typename T, bool VEC>
+cudaError_t rows_aligned(const NormBwd& a, cudaStream_t stream) {
+    int t, v;
+    bwd_shape(a.d, &t, &v);
+    return v == 1 ? rows_launch<T, 1, VEC>(a, t, stream) : v == 2 ? rows_launch<T, 2, VEC>(a, t, stream)
+                                                                  : rows_launch<T, 4, VEC>(a, t, stream);
 }
 
 template <typename T>
 cudaError_t rows_type(const NormBwd& a, cudaStream_t stream) {
-    int t, v;
-    bwd_shape(a.d, &t, &v);
-    return v == 1 ? rows_launch<T, 1>(a, t, stream) : v == 2 ? rows_launch<T, 2>(a, t, stream) : rows_launch<T, 4>(a, t, stream);
+    return bwd_vec<T>(a) ? rows_aligned<T, true>(a, stream) : rows_aligned<T, false>(a, stream);
+}
+
+cudaError_t ring_type(const NormBwd& a, cudaStream_t stream) {
+    if (ring_vec(a)) return a.d <= 8 * kBwdThreads ? ring_launch<1, true>(a, stream) : ring_launch<2, true>(a, stream);
+    return a.d <= 8 * kBwdThreads ? ring_launch<1, false>(a, stream) : ring_launch<2, false>(a, stream);
 }
 
 }  // namespace
@@ -475,7 +535,7 @@ int norm_bwd_grid(const NormBwd& a) {
 }
 
 cudaError_t launch_norm_bwd(const NormBwd& a, cudaStream_t stream) {
-    cudaError_t e = bwd_ring(a) ? (a.d <= 8 * kBwdThreads ? ring_launch<1>(a, stream) : ring_launch<2>(a, stream))
+    cudaError_t e = bwd_ring(a) ? ring_type(a, stream)
                     : a.x_type == GEMM_DTYPE_BF16 ? rows_type<__nv_bfloat16>(a, stream) : rows_type<float>(a, stream);
     if (e == cudaSuccess && a.dW && a.grid > 1)
         e = launch_chained(dw_reduce_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), 256, 0, stream, a.partial, a.grid,

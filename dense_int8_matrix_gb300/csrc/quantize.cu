@@ -10,8 +10,8 @@ namespace {
 // lane; a warp takes eight neighbouring blocks of a row, all loads first.
 // Reads every element once and writes a byte for it: bound by DRAM.
 constexpr int kRowBlocks = 8;   // blocks of a row per warp
-template <typename T, int F8>
-__global__ void __launch_bounds__(256) quant_rows_kernel(const F8Quant p, bool vec, bool qvec) {
+template <typename T, int F8, bool VEC>
+__global__ void __launch_bounds__(256) quant_rows_kernel(const F8Quant p, bool qvec) {
     pdl_launch_dependents();
     pdl_wait();
     constexpr float kStep = F8 == GEMM_F8_E4M3 ? kE4M3Step : kE5M2Step;
@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const F8Quant p, bool v
     for (int64_t b0 = static_cast<int64_t>(blockIdx.y) * kRowBlocks; b0 < kb; b0 += static_cast<int64_t>(gridDim.y) * kRowBlocks) {
         Vec8<T> v[kLoads];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) v[i] = load8(x, (b0 + 2 * i + half) * kF8Block + sub * 8, p.cols, vec);
+        for (int i = 0; i < kLoads; ++i) v[i] = load8<VEC>(x, (b0 + 2 * i + half) * kF8Block + sub * 8, p.cols);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int64_t b = b0 + 2 * i + half, c = b * kF8Block + sub * 8;
@@ -47,8 +47,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const F8Quant p, bool v
 
 // 128 x 128 blocks: one CTA per block; sixteen lanes cover 128 columns, a
 // thread takes eight rows.
-template <typename T, int F8>
-__global__ void __launch_bounds__(256) quant_blocks_kernel(const F8Quant p, bool vec, bool qvec) {
+template <typename T, int F8, bool VEC>
+__global__ void __launch_bounds__(256) quant_blocks_kernel(const F8Quant p, bool qvec) {
     __shared__ float red[8];
     pdl_launch_dependents();
     pdl_wait();
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const F8Quant p, bool
     for (int i = 0; i < 8; ++i) {
         const int64_t row = rb * kF8Block + (threadIdx.x >> 4) + 16 * i;
         if (row < p.rows)
-            v[i] = load8(static_cast<const T*>(p.X) + row * p.ldx, c, p.cols, vec);
+            v[i] = load8<VEC>(static_cast<const T*>(p.X) + row * p.ldx, c, p.cols);
         else
             v[i].zero();
     }
@@ -134,8 +134,8 @@ __device__ void find_block_rows(const F8Quant& p, int pb, int lane, int& row, in
 // that a column's eight values pack into eight bytes of shared memory; the
 // bytes leave as 128-byte rows.  The tile's 8-byte pieces are swizzled by the
 // column group, so that neither side has bank conflicts beyond its width.
-template <typename T, int F8>
-__global__ void __launch_bounds__(256) quant_cols_kernel(const F8Quant p, bool vec) {
+template <typename T, int F8, bool VEC>
+__global__ void __launch_bounds__(256) quant_cols_kernel(const F8Quant p) {
     __shared__ __align__(16) uint8_t tile[kF8Block * kF8Block];
     __shared__ __align__(16) float red[8][kF8Block];
     __shared__ __align__(16) float inverse[kF8Block];
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const F8Quant p, bool v
         for (int i = 0; i < 8; ++i) {
             const int r = rg * 8 + i;
             if (r < n)
-                v[i] = load8(static_cast<const T*>(p.X) + (row + r) * p.ldx, c, p.cols, vec);
+                v[i] = load8<VEC>(static_cast<const T*>(p.X) + (row + r) * p.ldx, c, p.cols);
             else
                 v[i].zero();
         }
@@ -217,46 +217,54 @@ bool vec_ok(const void* p, int64_t pitch) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (pitch * sizeof(T)) % 16 == 0;
 }
 
-template <typename T, int F8>
-cudaError_t rows_launch(const F8Quant& q, cudaStream_t stream) {
-    const int64_t gx = (q.rows + 7) / 8, gy = (q.cols + kF8Block * kRowBlocks - 1) / (kF8Block * kRowBlocks);
-    return launch_chained(quant_rows_kernel<T, F8>, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535)),
-                          256, 0, stream, q, vec_ok<T>(q.X, q.ldx), reinterpret_cast<uintptr_t>(q.Q) % 8 == 0 && q.ldq % 8 == 0);
+bool q_vec(const F8Quant& q) { return reinterpret_cast<uintptr_t>(q.Q) % 8 == 0 && q.ldq % 8 == 0; }
+
+struct RowsForm {
+    template <typename T, int F8, bool VEC>
+    static cudaError_t launch(const F8Quant& q, cudaStream_t stream) {
+        const int64_t gx = (q.rows + 7) / 8, gy = (q.cols + kF8Block * kRowBlocks - 1) / (kF8Block * kRowBlocks);
+        return launch_chained(quant_rows_kernel<T, F8, VEC>,
+                              dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535)), 256, 0, stream, q,
+                              q_vec(q));
+    }
+};
+
+struct BlocksForm {
+    template <typename T, int F8, bool VEC>
+    static cudaError_t launch(const F8Quant& q, cudaStream_t stream) {
+        const int64_t grid = ((q.rows + kF8Block - 1) / kF8Block) * ((q.cols + kF8Block - 1) / kF8Block);
+        if (grid > INT32_MAX) return cudaErrorInvalidValue;
+        return launch_chained(quant_blocks_kernel<T, F8, VEC>, dim3(static_cast<unsigned>(grid)), 256, 0, stream, q, q_vec(q));
+    }
+};
+
+struct ColsForm {
+    template <typename T, int F8, bool VEC>
+    static cudaError_t launch(const F8Quant& q, cudaStream_t stream) {
+        const int64_t gx = (q.cols + kF8Block - 1) / kF8Block, gy = q.kp / kF8Block;
+        return launch_chained(quant_cols_kernel<T, F8, VEC>,
+                              dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535)), 256, 0, stream, q);
+    }
+};
+
+template <typename Form, typename T, int F8>
+cudaError_t by_alignment(const F8Quant& q, cudaStream_t stream) {
+    return vec_ok<T>(q.X, q.ldx) ? Form::template launch<T, F8, true>(q, stream) : Form::template launch<T, F8, false>(q, stream);
 }
 
-template <typename T, int F8>
-cudaError_t blocks_launch(const F8Quant& q, cudaStream_t stream) {
-    const int64_t grid = ((q.rows + kF8Block - 1) / kF8Block) * ((q.cols + kF8Block - 1) / kF8Block);
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_chained(quant_blocks_kernel<T, F8>, dim3(static_cast<unsigned>(grid)), 256, 0, stream, q,
-                          vec_ok<T>(q.X, q.ldx), reinterpret_cast<uintptr_t>(q.Q) % 8 == 0 && q.ldq % 8 == 0);
-}
-
-template <typename T, int F8>
-cudaError_t cols_launch(const F8Quant& q, cudaStream_t stream) {
-    const int64_t gx = (q.cols + kF8Block - 1) / kF8Block, gy = q.kp / kF8Block;
-    return launch_chained(quant_cols_kernel<T, F8>, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535)),
-                          256, 0, stream, q, vec_ok<T>(q.X, q.ldx));
+template <typename Form>
+cudaError_t quantise(const F8Quant& q, cudaStream_t stream) {
+    const bool e4 = q.f8_type == GEMM_F8_E4M3;
+    if (q.x_type == GEMM_DTYPE_BF16)
+        return e4 ? by_alignment<Form, __nv_bfloat16, GEMM_F8_E4M3>(q, stream)
+                  : by_alignment<Form, __nv_bfloat16, GEMM_F8_E5M2>(q, stream);
+    return e4 ? by_alignment<Form, float, GEMM_F8_E4M3>(q, stream) : by_alignment<Form, float, GEMM_F8_E5M2>(q, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_f8_quant_rows(const F8Quant& q, cudaStream_t stream) {
-    const bool bf = q.x_type == GEMM_DTYPE_BF16, e4 = q.f8_type == GEMM_F8_E4M3;
-    return bf ? (e4 ? rows_launch<__nv_bfloat16, GEMM_F8_E4M3>(q, stream) : rows_launch<__nv_bfloat16, GEMM_F8_E5M2>(q, stream))
-              : (e4 ? rows_launch<float, GEMM_F8_E4M3>(q, stream) : rows_launch<float, GEMM_F8_E5M2>(q, stream));
-}
-
-cudaError_t launch_f8_quant_blocks(const F8Quant& q, cudaStream_t stream) {
-    const bool bf = q.x_type == GEMM_DTYPE_BF16, e4 = q.f8_type == GEMM_F8_E4M3;
-    return bf ? (e4 ? blocks_launch<__nv_bfloat16, GEMM_F8_E4M3>(q, stream) : blocks_launch<__nv_bfloat16, GEMM_F8_E5M2>(q, stream))
-              : (e4 ? blocks_launch<float, GEMM_F8_E4M3>(q, stream) : blocks_launch<float, GEMM_F8_E5M2>(q, stream));
-}
-
-cudaError_t launch_f8_quant_cols(const F8Quant& q, cudaStream_t stream) {
-    const bool bf = q.x_type == GEMM_DTYPE_BF16, e4 = q.f8_type == GEMM_F8_E4M3;
-    return bf ? (e4 ? cols_launch<__nv_bfloat16, GEMM_F8_E4M3>(q, stream) : cols_launch<__nv_bfloat16, GEMM_F8_E5M2>(q, stream))
-              : (e4 ? cols_launch<float, GEMM_F8_E4M3>(q, stream) : cols_launch<float, GEMM_F8_E5M2>(q, stream));
-}
+cudaError_t launch_f8_quant_rows(const F8Quant& q, cudaStream_t stream) { return quantise<RowsForm>(q, stream); }
+cudaError_t launch_f8_quant_blocks(const F8Quant& q, cudaStream_t stream) { return quantise<BlocksForm>(q, stream); }
+cudaError_t launch_f8_quant_cols(const F8Quant& q, cudaStream_t stream) { return quantise<ColsForm>(q, stream); }
 
 }  // namespace gemm
