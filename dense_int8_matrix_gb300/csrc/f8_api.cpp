@@ -53,10 +53,7 @@ void choose_config(gemm_plan_f8* p) {
     p->path = GEMM_PATH_TENSOR;
     p->bm = 256;
     p->split_k = 1;
-    const int64_t pairs = p->num_sms / 2 > 0 ? p->num_sms / 2 : 1;
-    const int64_t tm = (by_rows ? p->groups : 1) * ceil_div(rows, 256) * (p->group_mode == GEMM_GROUP_K ? p->groups : 1);
-    const int64_t w256 = ceil_div(tm * ceil_div(p->n, 256), pairs), w128 = ceil_div(tm * ceil_div(p->n, 128), pairs);
-    p->bn = 3 * w256 <= 2 * w128 ? 256 : 128;   // a 128-column tile takes two thirds of a 256-column one
+    p->bn = 256;
 }
 
 gemm_status make_f8_plan(int32_t mode, int32_t groups, int64_t m, int64_t k, int64_t n, int32_t a_type, int32_t b_type,

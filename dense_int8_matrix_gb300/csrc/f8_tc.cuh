@@ -23,6 +23,7 @@ struct F8Params {
     int tiles_m, tiles_n; // tiles of one group's D (GEMM_GROUP_ROWS: tiles_n alone)
     int out_f32;
     int d_vec;            // rows of D are 16-byte aligned
+    int halves;           // two-SM kernel: every tile in halves of 128 columns
     int pieces;           // row tiles that all groups together can have (GEMM_GROUP_ROWS)
 };
 
@@ -253,7 +254,7 @@ __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A warp's 32 rows (lane = row) x C columns of sums leave for D in slices of
+// A warp's 32 rows (lane = row) x `cols` of C columns of sums leave for D in slices of
 // 128 bytes per row: through the warp's 4 KiB staging buffer (16-byte chunks
 // swizzled by row & 7, free of bank conflicts both ways), so that eight lanes
 // write one row's 128 bytes.  All of a slice is read back before the first
@@ -262,7 +263,7 @@ __device__ __forceinline__ void more_registers() {
 // first; rows at or past row_end and columns at or past n are not written.
 constexpr int kStageRowsBytes = 32 * 128;
 template <bool F32, bool FRAG, int C>
-__device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_t stg, int lane, uint8_t* D, int64_t ldd,
+__device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], int cols, uint32_t stg, int lane, uint8_t* D, int64_t ldd,
                                            int64_t row0, int64_t row_end, int col0, int n, bool vec) {
     constexpr int W = F32 ? 32 : 64;   // columns per slice
     constexpr int ES = F32 ? 4 : 2;
@@ -271,10 +272,11 @@ __device__ __forceinline__ void store_rows(const uint64_t (&acc)[C / 2], uint32_
     const int r0 = lane >> 3, part = lane & 7;
     uint8_t* out = D + ((row0 + r0) * ldd + col0 + part * (16 / ES)) * ES;
     const int64_t step = 4 * ldd * ES;
-    const bool whole = vec && n - col0 >= C;   // the warp's columns are all D's, and 16-byte aligned
+    const bool whole = vec && n - col0 >= cols;   // the warp's columns are all D's, and 16-byte aligned
     const bool pairs = ldd % 2 == 0 && reinterpret_cast<uintptr_t>(D) % 4 == 0;
 #pragma unroll
     for (int s = 0; s < C / W; ++s) {
+        if (s * W >= cols) break;
         __syncwarp();   // the slice before has been read out
         if constexpr (FRAG) {
 #pragma unroll

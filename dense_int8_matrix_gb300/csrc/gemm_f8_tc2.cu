@@ -2,20 +2,27 @@
 //
 //   D[i][j] = sum_b (sa[b][i] * sb[..]) * (sum of block b of A[i] * Bt[j])
 //
-// A cluster of two CTAs computes a 256 x BN tile; each CTA loads 128 rows of
-// A and BN / 2 rows of Bt per K block with TMA, and one tcgen05.mma (M = 256,
-// N = BN, K = 32, four per block) leaves its 128 rows in its own TMEM.  The
+// A cluster of two CTAs computes a 256 x 256 tile (or a half, 256 x 128); each
+// CTA loads 128 rows of A and of Bt per K block with TMA, and tcgen05.mma (M =
+// 256, N = 256, K = 32, four per block) leaves its 128 rows in its own TMEM.  The
 // scales change with every block of 128, so a block's sums are not added up
 // in TMEM: the MMA of block b + 1 writes another TMEM buffer while the eight
 // epilogue warps read block b's, multiply by the scales and add to fp32
-// running sums in registers (BN / 2 per thread).  The tensor pipe needs
-// 2 * BN cycles per block; reading BN columns of TMEM and the BN multiply-adds
-// per lane quarter fit beside it.
+// running sums in registers (128 per thread).
 //
-// Roles as in the library's other two-SM kernel: warp 0 loads, warp 1 of the
-// even CTA issues MMAs, warps 4-11 scale, add and store.  Grouped products
-// read the group offsets on the device: warp 2 sums them into shared memory
-// first, and every role walks the same list of tiles.
+// Roles: warp 0 loads operands, warp 2 copies scales, warps 1 and 3 of the even
+// CTA issue the MMAs of alternate blocks, warps 4-11 scale, add and store.
+// Each role's loop is run by whole warps (one elected lane issues): with a
+// single lane running them, waiting and issuing alone took 700 cycles a block.
+// Grouped products read the group offsets on the device: warp 2 sums them into
+// shared memory first, and every role walks the same list of tiles.
+//
+// What bounds it (GB300, bf16 output, 128 x 128 scales of Bt): 8192^3 takes
+// 400 us, 2.75 PFLOP/s; without the epilogue's TMEM reads and multiply-adds
+// 311 us (the MMAs, under the power limit), without the multiply-adds alone
+// 350 us.  The epilogue needs 256 cycles of multiply-adds and 140 of TMEM
+// reads per block and scheduler beside the MMAs' 512.  With column scales
+// (1 x 128 for both) the multiply-adds double: 8192^3 to fp32 570 us.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -34,22 +41,23 @@ constexpr int kCtrlBytes = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 
-template <int BN, bool BROWS>
+constexpr int kTileN = 256;                          // columns of a whole tile
+constexpr int kCols = kTileN / 2;                    // columns of D per epilogue thread
+constexpr int kBBytes = kTileN / 2 * kF8RowBytes;
+constexpr int kStage = kABytes + kBBytes;
+constexpr int kStages = 5;
+constexpr int kBufs = 512 / kTileN;                  // TMEM accumulators
+// Blocks whose scales are in shared memory.  Block i's are copied once block
+// i - kAhead is multiplied: its accumulator was free then, so the block kBufs
+// before it was read and the one before that added.  kAhead is small enough
+// that the barrier it looks at cannot be a round further: block i - 1 + kBufs
+// is the last that can be multiplied without i's scales.
+constexpr int kAhead = kStages - kBufs;
+constexpr int kSlots = kAhead + kBufs + 1;
+template <bool BROWS>
 struct Config {
-    static constexpr int COLS = BN / 2;                      // columns of D per epilogue thread
-    static constexpr int B_BYTES = BN / 2 * kF8RowBytes;
-    static constexpr int STAGE = kABytes + B_BYTES;
-    static constexpr int STAGES = BN == 256 ? 5 : 7;
-    static constexpr int BUFS = 512 / BN;                    // TMEM accumulators
-    // Blocks whose scales are in shared memory.  Block i's are copied once
-    // block i - AHEAD is multiplied: its accumulator was free then, so the
-    // block BUFS before it was read and the one before that added.  AHEAD is
-    // small enough that the barrier it looks at cannot be a round further:
-    // block i - 1 + BUFS is the last that can be multiplied without i's scales.
-    static constexpr int AHEAD = STAGES - BUFS;
-    static constexpr int SLOTS = AHEAD + BUFS + 1;
-    static constexpr int SLOT = kHalfRows * 4 + (BROWS ? BN * 4 : 16);
-    static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + kEpiWarps * kStageRowsBytes + SLOTS * SLOT +
+    static constexpr int SLOT = kHalfRows * 4 + (BROWS ? kTileN * 4 : 16);
+    static constexpr size_t SMEM = static_cast<size_t>(kStages) * kStage + kEpiWarps * kStageRowsBytes + kSlots * SLOT +
                                    kPreBytes + kCtrlBytes + 1024;
     static_assert(SMEM <= 232448, "shared memory");
 };
@@ -62,15 +70,30 @@ struct Unit {
     int col;       // first column of D
     int sblock;    // block-scale row: group * nb + col / 128
     int kb_lo, kb_hi;
+    bool half;     // 128 columns instead of 256
 };
 
-__device__ __forceinline__ int unit_count(const F8Params& p, const int32_t* pre) {
-    if (p.mode == GEMM_GROUP_ROWS) return pre[p.groups] * p.tiles_n;
-    return p.groups * p.tiles_m * p.tiles_n;
+// The list of units that the pairs take in turn: whole tiles, and the tiles of
+// a last round that would leave half of the pairs idle as two halves of 128
+// columns each.  Half a tile takes 0.77 of a whole one's time, so this pays
+// where both halves run at once: 4096^3 (256 tiles on 76 pairs) 64.8 -> 61.3
+// us, 512 x 4096 x 4096 (32 tiles) 18.9 -> 15.8 us.
+struct Units {
+    int whole, count;   // units [0, whole) are tiles, the rest halves
+};
+__device__ __forceinline__ Units list_units(const F8Params& p, const int32_t* pre, int npairs) {
+    const int tiles = p.mode == GEMM_GROUP_ROWS ? pre[p.groups] * p.tiles_n : p.groups * p.tiles_m * p.tiles_n;
+    Units x;
+    x.whole = p.halves ? 0 : tiles / npairs * npairs;
+    if (!p.halves && 2 * (tiles - x.whole) > npairs) x.whole = tiles;
+    x.count = x.whole + 2 * (tiles - x.whole);
+    return x;
 }
 
-template <int BN>
-__device__ __forceinline__ Unit unit_at(int u, const F8Params& p, const int32_t* pre) {
+__device__ __forceinline__ Unit unit_at(int u, const Units& list, const F8Params& p, const int32_t* pre) {
+    const bool half = u >= list.whole;
+    const int part = half ? (u - list.whole) & 1 : 0;
+    if (half) u = list.whole + ((u - list.whole) >> 1);
     Unit x;
     int g = 0, tm, tn, lo = 0, hi = p.m;
     if (p.mode == GEMM_GROUP_ROWS) {
@@ -85,7 +108,8 @@ __device__ __forceinline__ Unit unit_at(int u, const F8Params& p, const int32_t*
     x.arow = lo + tm * 256;
     x.drow = x.arow;
     x.dend = hi;
-    x.col = tn * BN;
+    x.half = half;
+    x.col = tn * kTileN + part * kF8Block;
     x.brow = x.col;
     x.sblock = x.col / kF8Block;
     x.kb_lo = 0;
@@ -99,22 +123,21 @@ __device__ __forceinline__ Unit unit_at(int u, const F8Params& p, const int32_t*
         x.kb_lo = min(pre[g], p.kb);
         x.kb_hi = min(pre[g + 1], p.kb);
     }
+    if (x.col >= p.n) x.kb_hi = x.kb_lo;   // a half past D's last column
     return x;
 }
 
-template <int BN, bool BROWS>
+template <bool BROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     f8_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const F8Params p,
-                  const uint32_t idesc) {
-    using R = Config<BN, BROWS>;
-    constexpr int kStages = R::STAGES, kBufs = R::BUFS;
-    constexpr int kSlots = R::SLOTS, kCols = R::COLS;
+                  const uint32_t idesc, const uint32_t idesc_half) {
+    using R = Config<BROWS>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t sA = base;
     const uint32_t sB = base + kStages * kABytes;
-    const uint32_t sEpi = base + kStages * R::STAGE;
+    const uint32_t sEpi = base + kStages * kStage;
     const uint32_t sScale = sEpi + kEpiWarps * kStageRowsBytes;
     uint8_t* ctrl = smem_raw + (sScale - raw) + kSlots * R::SLOT;
     int32_t* pre = reinterpret_cast<int32_t*>(ctrl + kCtrlBytes);
@@ -160,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_barrier();   // barriers and TMEM of both CTAs are ready
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int units = unit_count(p, pre);
+    const Units list = list_units(p, pre, npairs);
+    const int units = list.count;
 
     // the epilogue's running sums need more registers than an even share: of
     // 384 threads with 168, 128 keep 40 each and 256 take 232
@@ -175,9 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t issued = 0;
             bool ok = true;
             for (int u = pair; ok && u < units; u += npairs) {
-                const Unit w = unit_at<BN>(u, p, pre);
+                const Unit w = unit_at(u, list, p, pre);
                 const int ya = w.arow + static_cast<int>(rank) * kHalfRows;
-                const int yb = w.brow + static_cast<int>(rank) * (BN / 2);
+                // (a half's box brings 64 rows more than are multiplied)
+                const int yb = w.brow + static_cast<int>(rank) * (w.half ? kF8Block / 2 : kF8Block);
                 for (int kb = w.kb_lo; kb < w.kb_hi; ++kb, ++issued) {
                     // the stage is free once the block that was in it has been multiplied
                     if (!wait_warp(done0 + 8u * at.i, at.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutProducer)) {
@@ -186,9 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (elect_one()) {
                         const uint32_t fb = full_leader + 8u * at.i;
-                        if (leader) mbar_arrive_expect_tx(full0 + 8u * at.i, 2 * R::STAGE);
+                        if (leader) mbar_arrive_expect_tx(full0 + 8u * at.i, 2 * kStage);
                         load_2d_pair(sA + at.i * kABytes, &tmA, kb * kF8Block, ya, fb, pol);
-                        load_2d_pair(sB + at.i * R::B_BYTES, &tmB, kb * kF8Block, yb, fb, pol);
+                        load_2d_pair(sB + at.i * kBBytes, &tmB, kb * kF8Block, yb, fb, pol);
                     }
                     __syncwarp();
                     at.next();
@@ -209,14 +234,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t n = 0;
             bool ok = true;
             for (int u = pair; ok && u < units; u += npairs) {
-                const Unit w = unit_at<BN>(u, p, pre);
+                const Unit w = unit_at(u, list, p, pre);
                 const int row0 = w.arow + static_cast<int>(rank) * kHalfRows + lane;
                 const float* sa = p.a_scale + static_cast<int64_t>(w.kb_lo) * p.rows_a;
                 const float* sb = BROWS ? p.b_scale + static_cast<int64_t>(w.kb_lo) * p.rows_b + w.brow + lane
                                         : p.b_scale + static_cast<int64_t>(w.sblock + (lane & 1)) * p.kb + w.kb_lo;
                 const bool sb_in = w.col / kF8Block + (lane & 1) < p.nb;
                 for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
-                    if (n >= R::AHEAD) {
+                    if (n >= kAhead) {
                         if (!wait_warp(done0 + 8u * at.i, at.ph, abort_flag, p.err, kDevErrTimeoutProducer)) {
                             ok = false;
                             break;
@@ -232,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if constexpr (BROWS) {
 #pragma unroll
-                        for (int i = 0; i < BN / 32; ++i) {
+                        for (int i = 0; i < kTileN / 32; ++i) {
                             const bool in = w.col + lane + 32 * i < p.n;
                             copy4_async(slot_at + 512 + 4 * frag_place(lane + 32 * i), in ? sb + 32 * i : p.b_scale, in);
                         }
@@ -257,8 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t skip = turn;   // blocks until this warp's next one
             bool ok = true;
             for (int u = pair; ok && u < units; u += npairs) {
-                const Unit w = unit_at<BN>(u, p, pre);
+                const Unit w = unit_at(u, list, p, pre);
                 const uint32_t blocks = static_cast<uint32_t>(w.kb_hi - w.kb_lo);
+                const uint32_t desc = w.half ? idesc_half : idesc;
                 uint32_t j = skip;
                 for (; j < blocks; j += 2) {
                     if (!wait_warp(acce0 + 8u * buf.i, buf.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutMma) ||
@@ -268,11 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     const uint64_t ad = smem_desc_sw128_kmajor(sA + st.i * kABytes);
-                    const uint64_t bd = smem_desc_sw128_kmajor(sB + st.i * R::B_BYTES);
+                    const uint64_t bd = smem_desc_sw128_kmajor(sB + st.i * kBBytes);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < kF8Block / kF8MmaK; ++kk)
-                            mma_f8<2>(tmem + buf.i * BN, ad + 2u * kk, bd + 2u * kk, idesc, kk > 0 ? 1u : 0u);
+                            mma_f8<2>(tmem + buf.i * kTileN, ad + 2u * kk, bd + 2u * kk, desc, kk > 0 ? 1u : 0u);
                         commit_pair(done0 + 8u * st.i);
                     }
                     __syncwarp();
@@ -292,26 +318,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = warp - 4, q = warp & 3, h = e >> 2;
         const uint32_t stg = sEpi + e * kStageRowsBytes;
         const uint32_t acce = peer_address(acce0, 0);
-        const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kCols;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
         // the lane's row, or the first of its four (eight rows apart)
         const uint32_t row_scale = sScale + 4 * (q * 32 + (BROWS ? lane >> 2 : lane));
-        const uint32_t col_scale = sScale + 512 + (BROWS ? h * kCols * 4 : (h * kCols / kF8Block) * 4);
         Turn<kStages> st;
         Turn<kBufs> buf;
         Turn<kSlots> slot;
         bool ok = true;
         for (int u = pair; ok && u < units; u += npairs) {
-            const Unit w = unit_at<BN>(u, p, pre);
+            const Unit w = unit_at(u, list, p, pre);
+            const bool full = !w.half;
             const int in_tile = static_cast<int>(rank) * kHalfRows + q * 32;   // the warp's first row
-            const int col = w.col + h * kCols;
-            uint64_t acc[kCols / 2];   // pairs of columns
+            const int my = h * (full ? kCols : kCols / 2);                     // the thread's first column of the tile
+            const uint32_t t0 = lanes + my;
+            const uint32_t col_scale = sScale + 512 + (BROWS ? my * 4 : (my / kF8Block) * 4);
+            uint64_t acc[kCols / 2];   // pairs of columns, or of rows (fragment form); the first half of them for a half
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
             // One chunk of 32 columns is added while the next is on its way,
             // the first of the next block included.  Order matters: what goes
             // through the shared-memory queue behind a TMEM load waits for it,
             // so scales are asked for first.
-            constexpr int kChunks = kCols / 32;
             uint32_t v[2][32];
             uint4 sc[2][2];
             float sa[BROWS ? 4 : 1], sb = 1.f;
@@ -337,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < (BROWS ? 4 : 1); ++k) sa[k] = ld_shared_f32(row_scale + slot.i * R::SLOT + 32 * k);
                 if constexpr (!BROWS) sb = ld_shared_f32(cols);
-                chunk(0, cols, t0 + buf.i * BN);
+                chunk(0, cols, t0 + buf.i * kTileN);
             };
             if (w.kb_lo < w.kb_hi) {
                 ok = wait_warp_both(done0 + 8u * st.i, st.ph, scale0 + 8u * slot.i, slot.ph, abort_flag, p.err,
@@ -346,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 first_chunk();
             }
             for (int left = w.kb_hi - w.kb_lo; left > 0; --left) {
-                const uint32_t tb = t0 + buf.i * BN, free_bar = acce + 8u * buf.i, cols = col_scale + slot.i * R::SLOT;
+                const uint32_t tb = t0 + buf.i * kTileN, free_bar = acce + 8u * buf.i, cols = col_scale + slot.i * R::SLOT;
                 st.next();
                 buf.next();
                 slot.next();
@@ -358,11 +385,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t s = __float_as_uint(sa[0] * sb);
                     s2[0] = pair_of(s, s);
                 }
-#pragma unroll
-                for (int c = 0; c + 1 < kChunks; ++c) {
-                    chunk(c + 1, cols, tb);
-                    add(c);
-                    wait_tmem(v[(c + 1) & 1]);
+                chunk(1, cols, tb);
+                add(0);
+                wait_tmem(v[1]);
+                if (full) {
+                    chunk(2, cols, tb);
+                    add(1);
+                    wait_tmem(v[0]);
+                    chunk(3, cols, tb);
+                    add(2);
+                    wait_tmem(v[1]);
                 }
                 // all columns are in registers: the accumulator is free
                 tc_fence_before();
@@ -373,15 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     first_chunk();
                 }
-                add(kChunks - 1);
+                if (full)
+                    add(3);
+                else
+                    add(1);
             }
             if (!ok) break;
+            uint8_t* D = static_cast<uint8_t*>(p.D);
+            const int col = w.col + my, cols = full ? kCols : kCols / 2;
             if (p.out_f32)
-                store_rows<true, BROWS, kCols>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
-                                 p.d_vec != 0);
+                store_rows<true, BROWS, kCols>(acc, cols, stg, lane, D, p.ldd, w.drow + in_tile, w.dend, col, p.n, p.d_vec != 0);
             else
-                store_rows<false, BROWS, kCols>(acc, stg, lane, static_cast<uint8_t*>(p.D), p.ldd, w.drow + in_tile, w.dend, col, p.n,
-                                  p.d_vec != 0);
+                store_rows<false, BROWS, kCols>(acc, cols, stg, lane, D, p.ldd, w.drow + in_tile, w.dend, col, p.n, p.d_vec != 0);
         }
     }
     tc_fence_before();
@@ -395,20 +430,23 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-template <int BN, bool BROWS>
+template <bool BROWS>
 cudaError_t launch(const F8Launch& a, cudaStream_t stream) {
-    using R = Config<BN, BROWS>;
+    using R = Config<BROWS>;
     CUtensorMap mA, mB;
-    if (!encode_f8(&mA, a.A, a.k, a.rows_a, a.lda, kHalfRows) || !encode_f8(&mB, a.Bt, a.k, a.rows_b, a.ldb, BN / 2))
+    if (!encode_f8(&mA, a.A, a.k, a.rows_a, a.lda, kHalfRows) || !encode_f8(&mB, a.Bt, a.k, a.rows_b, a.ldb, kTileN / 2))
         return cudaErrorInvalidValue;
-    F8Params p = f8_params(a, 256, BN);
-    const int64_t units = a.group_mode == GEMM_GROUP_ROWS ? static_cast<int64_t>(p.pieces) * p.tiles_n
+    F8Params p = f8_params(a, 256, kTileN);
+    p.halves = a.bn == kF8Block ? 1 : 0;
+    const int64_t tiles = a.group_mode == GEMM_GROUP_ROWS ? static_cast<int64_t>(p.pieces) * p.tiles_n
                                                           : static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.groups;
-    if (units > INT32_MAX) return cudaErrorInvalidValue;
+    if (2 * tiles > INT32_MAX) return cudaErrorInvalidValue;
     int64_t pairs = a.pairs > 0 ? a.pairs : a.num_sms / 2;
-    if (pairs > units) pairs = units;
     if (pairs < 1) pairs = 1;
-    const void* kern = reinterpret_cast<const void*>(f8_tc2_kernel<BN, BROWS>);
+    // (grouped by rows, `tiles` is only the most there can be)
+    const int64_t use = p.halves || 2 * tiles <= pairs || a.group_mode == GEMM_GROUP_ROWS ? 2 * tiles : tiles;
+    if (pairs > use) pairs = use;
+    const void* kern = reinterpret_cast<const void*>(f8_tc2_kernel<BROWS>);
     const cudaError_t e = kernel_attrs_once(kern, static_cast<int>(R::SMEM), true);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
@@ -426,8 +464,8 @@ cudaError_t launch(const F8Launch& a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    uint32_t idesc = idesc_f8(a.a_type, a.b_type, 256, BN);
-    void* args[] = {&mA, &mB, &p, &idesc};
+    uint32_t idesc = idesc_f8(a.a_type, a.b_type, 256, kTileN), idesc_half = idesc_f8(a.a_type, a.b_type, 256, kTileN / 2);
+    void* args[] = {&mA, &mB, &p, &idesc, &idesc_half};
     const cudaError_t r = cudaLaunchKernelExC(&cfg, kern, args);
     return r != cudaSuccess ? r : cudaGetLastError();
 }
@@ -464,6 +502,7 @@ F8Params f8_params(const F8Launch& a, int bm, int bn) {
     p.nb = static_cast<int>((a.n + kF8Block - 1) / kF8Block);
     p.tiles_m = static_cast<int>((a.m + bm - 1) / bm);
     p.tiles_n = static_cast<int>((a.n + bn - 1) / bn);
+    p.halves = 0;
     p.pieces = static_cast<int>(a.m / bm + (a.groups < a.m ? a.groups : a.m));   // each group may end in a part of a tile
     p.out_f32 = a.out_f32 ? 1 : 0;
     p.d_vec = reinterpret_cast<uintptr_t>(a.D) % 16 == 0 && (a.ldd * (a.out_f32 ? 4 : 2)) % 16 == 0;
@@ -471,9 +510,7 @@ F8Params f8_params(const F8Launch& a, int bm, int bn) {
 }
 
 cudaError_t launch_f8_tc2(const F8Launch& a, cudaStream_t stream) {
-    const bool rows = a.b_scale_mode == GEMM_SCALE_ROWS;
-    if (a.bn == 128) return rows ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
-    return rows ? launch<256, true>(a, stream) : launch<256, false>(a, stream);
+    return a.b_scale_mode == GEMM_SCALE_ROWS ? launch<true>(a, stream) : launch<false>(a, stream);
 }
 
 }  // namespace gemm
