@@ -224,7 +224,10 @@ def _addr(x, dtype=None, shape=None, device=True):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        # the same handle without building a Stream object (0.4 us against 2.9)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -361,102 +364,100 @@ def gemm_f8_padded_k(rows: int, groups: int = 1) -> int:
     return load().gemm_f8_padded_k(rows, groups)
 
 
-_f8_types = None   # torch's dtype of each GEMM_F8_* value
+class _Torch:
+    """What the calls below need of torch, looked up once: a small call is as
+    long as its checks and its launch."""
 
-
-def _f8_dtype(f8_type):
-    global _f8_types
-    if _f8_types is None:
+    def __init__(self):
         import torch
-        _f8_types = (torch.float8_e4m3fn, torch.float8_e5m2)
-    return _f8_types[f8_type]
+        self.f32, self.bf16, self.i32, self.i8 = torch.float32, torch.bfloat16, torch.int32, torch.int8
+        self.f8 = (torch.float8_e4m3fn, torch.float8_e5m2)   # by GEMM_F8_*
+        self.f8_type = {d: i for i, d in enumerate(self.f8)}
+        self.real_type = {torch.bfloat16: GEMM_DTYPE_BF16, torch.float32: GEMM_DTYPE_F32}
+        self.out_type = {torch.bfloat16: GEMM_OUT_BF16, torch.float32: GEMM_OUT_F32}
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _f8_type(q):
-    for f8_type in (GEMM_F8_E4M3, GEMM_F8_E5M2):
-        if q.dtype is _f8_dtype(f8_type):
-            return f8_type
-    raise TypeError("expected torch.float8_e4m3fn or torch.float8_e5m2, got %s" % q.dtype)
+_torch_names = None
 
 
-def _real_type(x):
-    import torch
-    if x.dtype is torch.bfloat16:
-        return GEMM_DTYPE_BF16
-    if x.dtype is torch.float32:
-        return GEMM_DTYPE_F32
-    raise TypeError("expected torch.bfloat16 or torch.float32, got %s" % x.dtype)
+def _torch():
+    global _torch_names
+    if _torch_names is None:
+        _torch_names = _Torch()
+    return _torch_names
+
+
+def _type_of(x, types):
+    found = types.get(x.dtype)
+    if found is None:
+        raise TypeError("expected %s, got %s" % (" or ".join(str(d) for d in types), x.dtype))
+    return found
 
 
 def _stream_of(x, stream):
-    """The CUDA stream handle; by default the current stream of x's device
-    (looked up by its raw handle: a small call is as long as its launch)."""
-    if stream is not None:
-        return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(x.get_device())
+    """The CUDA stream handle; by default the current stream of x's device."""
+    if stream is None:
+        return _torch_names.raw_stream(x.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _matrix(x, dtype, shape):
-    """(address, row pitch) of a CUDA tensor whose rows are contiguous; the
-    leading dimensions before the last two lie one after the other."""
+def _wrong(x, dtype, shape):
     if x.dtype is not dtype:
         raise TypeError("expected %s, got %s" % (dtype, x.dtype))
     if x.shape != shape:
         raise ValueError("expected shape %s, got %s" % (tuple(shape), tuple(x.shape)))
     if not x.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
+    raise ValueError("tensor must be contiguous")
+
+
+def _dense(x, dtype, shape):
+    """Address of a contiguous CUDA tensor."""
+    if x.dtype is not dtype or x.shape != shape or not x.is_cuda or not x.is_contiguous():
+        _wrong(x, dtype, shape)
+    return x.data_ptr()
+
+
+def _matrix(x, dtype, shape):
+    """(address, row pitch) of a CUDA tensor whose rows are contiguous; the
+    leading dimensions before the last two lie one after the other."""
+    if x.dtype is not dtype or x.shape != shape or not x.is_cuda:
+        _wrong(x, dtype, shape)
     stride = x.stride()
+    cols = shape[-1]
     groups = shape[0] if len(shape) == 3 else 1
     if shape[-2] > 1:
         pitch = stride[-2]
     elif groups > 1:
         pitch = stride[0]
     else:   # one row: any pitch will do
-        pitch = (shape[-1] + 15) // 16 * 16
-    if (shape[-1] > 1 and stride[-1] != 1) or pitch < shape[-1]:
+        pitch = (cols + 15) // 16 * 16
+    if (cols > 1 and stride[-1] != 1) or pitch < cols:
         raise ValueError("rows must be contiguous and must not overlap")
     if groups > 1 and stride[0] != pitch * shape[1]:
         raise ValueError("groups must lie one after the other")
     return x.data_ptr(), pitch
 
 
-def _dense(x, dtype, shape):
-    """Address of a contiguous CUDA tensor."""
-    if x.dtype is not dtype:
-        raise TypeError("expected %s, got %s" % (dtype, x.dtype))
-    if x.shape != shape:
-        raise ValueError("expected shape %s, got %s" % (tuple(shape), tuple(x.shape)))
-    if not x.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
-    if not x.is_contiguous():
-        raise ValueError("tensor must be contiguous")
-    return x.data_ptr()
-
-
 def _f8_run(plan, A, a_scale, Bt, b_scale, offsets, D, stream):
-    import torch
-    lib = _lib or load()
+    lib, T = _lib or load(), _torch_names or _torch()
     m, k, n, g, mode = plan.m, plan.k, plan.n, plan.groups, plan.group_mode
     kb = (k + 127) // 128
-    f32 = torch.float32
-    a, lda = _matrix(A, _f8_dtype(plan.a_type), (m, k))
+    a, lda = _matrix(A, T.f8[plan.a_type], (m, k))
     rows = mode == GEMM_GROUP_ROWS
-    b, ldb = _matrix(Bt, _f8_dtype(plan.b_type), (g, n, k) if rows else (n, k))
+    b, ldb = _matrix(Bt, T.f8[plan.b_type], (g, n, k) if rows else (n, k))
     if plan.b_scale == GEMM_SCALE_BLOCKS:
-        sb = _dense(b_scale, f32, (g, (n + 127) // 128, kb) if rows else ((n + 127) // 128, kb))
+        sb = _dense(b_scale, T.f32, (g, (n + 127) // 128, kb) if rows else ((n + 127) // 128, kb))
     else:
-        sb = _dense(b_scale, f32, (kb, g * n) if rows else (kb, n))
-    sa = _dense(a_scale, f32, (kb, m))
-    out_dtype = D.dtype
-    if out_dtype is not f32 and out_dtype is not torch.bfloat16:
-        raise TypeError("expected a torch.bfloat16 or torch.float32 output, got %s" % out_dtype)
-    d, ldd = _matrix(D, out_dtype, (g, m, n) if mode == GEMM_GROUP_K else (m, n))
-    out = GEMM_OUT_F32 if out_dtype is f32 else GEMM_OUT_BF16
+        sb = _dense(b_scale, T.f32, (kb, g * n) if rows else (kb, n))
+    sa = _dense(a_scale, T.f32, (kb, m))
+    out = _type_of(D, T.out_type)
+    d, ldd = _matrix(D, D.dtype, (g, m, n) if mode == GEMM_GROUP_K else (m, n))
     s = _stream_of(A, stream)
     if offsets is None:
         return lib.gemm_f8_run(plan, a, lda, sa, b, ldb, sb, out, d, ldd, s)
-    off = _dense(offsets, torch.int32, (g + 1,))
+    off = _dense(offsets, T.i32, (g + 1,))
     return lib.gemm_f8_grouped_run(plan, a, lda, sa, b, ldb, sb, off, out, d, ldd, s)
 
 
@@ -465,7 +466,9 @@ def gemm_f8_run(plan: gemm_plan_f8, A, a_scale, Bt, b_scale, D, stream=None) -> 
     (n x k) with fp32 scales: a_scale (ceil(k/128), m); b_scale
     (ceil(n/128), ceil(k/128)), or (ceil(k/128), n) for a plan with
     GEMM_SCALE_ROWS.  Rows may have a pitch (a multiple of 16 for A and Bt)."""
-    _check(_f8_run(plan, A, a_scale, Bt, b_scale, None, D, stream), "gemm_f8_run")
+    st = _f8_run(plan, A, a_scale, Bt, b_scale, None, D, stream)
+    if st:
+        _check(st, "gemm_f8_run")
 
 
 def gemm_f8_grouped_run(plan: gemm_plan_f8, A, a_scale, Bt, b_scale, offsets, D, stream=None) -> None:
@@ -476,82 +479,87 @@ def gemm_f8_grouped_run(plan: gemm_plan_f8, A, a_scale, Bt, b_scale, offsets, D,
     groups + 1 int32 on the GPU."""
     if offsets is None:
         raise TypeError("offsets are needed")
-    _check(_f8_run(plan, A, a_scale, Bt, b_scale, offsets, D, stream), "gemm_f8_grouped_run")
+    st = _f8_run(plan, A, a_scale, Bt, b_scale, offsets, D, stream)
+    if st:
+        _check(st, "gemm_f8_grouped_run")
 
 
 def gemm_f8_quantize(X, Q, scale, scale_mode: int = GEMM_SCALE_ROWS, stream=None) -> None:
     """Q (float8, like X) and its scales from X (rows x cols, bfloat16 or
     fp32): scale (ceil(cols/128), rows), or (ceil(rows/128), ceil(cols/128))
     for GEMM_SCALE_BLOCKS."""
-    import torch
-    rows, cols = X.shape
-    x, ldx = _matrix(X, X.dtype, (rows, cols))
-    q, ldq = _matrix(Q, Q.dtype, (rows, cols))
+    lib, T = _lib or load(), _torch_names or _torch()
+    rows, cols = shape = X.shape
+    x, ldx = _matrix(X, X.dtype, shape)
+    q, ldq = _matrix(Q, Q.dtype, shape)
     kb = (cols + 127) // 128
-    shape = (kb, rows) if scale_mode == GEMM_SCALE_ROWS else ((rows + 127) // 128, kb)
-    st = load().gemm_f8_quantize(x, _real_type(X), rows, cols, ldx, _f8_type(Q), scale_mode, q, ldq,
-                                 _dense(scale, torch.float32, shape), _stream_of(X, stream))
-    _check(st, "gemm_f8_quantize")
+    st = lib.gemm_f8_quantize(x, _type_of(X, T.real_type), rows, cols, ldx, _type_of(Q, T.f8_type), scale_mode, q, ldq,
+                              _dense(scale, T.f32, (kb, rows) if scale_mode == GEMM_SCALE_ROWS else ((rows + 127) // 128, kb)),
+                              _stream_of(X, stream))
+    if st:
+        _check(st, "gemm_f8_quantize")
 
 
 def gemm_f8_quantize_cols(X, Q, scale, offsets=None, stream=None) -> None:
     """Q (cols x gemm_f8_padded_k(rows, groups), float8) = X^T quantised in
     blocks of 128 rows of each group, scale (padded_k / 128, cols).  offsets:
     groups + 1 int32 on the GPU, None for one group of all rows."""
-    import torch
-    rows, cols = X.shape
+    lib, T = _lib or load(), _torch_names or _torch()
+    rows, cols = shape = X.shape
     groups = 1 if offsets is None else offsets.shape[0] - 1
-    kp = gemm_f8_padded_k(rows, groups)
-    x, ldx = _matrix(X, X.dtype, (rows, cols))
+    kp = (rows + 127 * groups) // 128 * 128
+    x, ldx = _matrix(X, X.dtype, shape)
     q, ldq = _matrix(Q, Q.dtype, (cols, kp))
-    off = None if offsets is None else _dense(offsets, torch.int32, (groups + 1,))
-    st = load().gemm_f8_quantize_cols(x, _real_type(X), rows, cols, ldx, _f8_type(Q), off, groups, q, ldq,
-                                      _dense(scale, torch.float32, (kp // 128, cols)), _stream_of(X, stream))
-    _check(st, "gemm_f8_quantize_cols")
+    off = None if offsets is None else _dense(offsets, T.i32, (groups + 1,))
+    st = lib.gemm_f8_quantize_cols(x, _type_of(X, T.real_type), rows, cols, ldx, _type_of(Q, T.f8_type), off, groups, q,
+                                   ldq, _dense(scale, T.f32, (kp // 128, cols)), _stream_of(X, stream))
+    if st:
+        _check(st, "gemm_f8_quantize_cols")
 
 
-def _norm(name, X, R, W, eps, H, rstd, Q, q_dtype, scale, scale_shape, stream):
-    import torch
-    rows, d = X.shape
-    x, ldx = _matrix(X, X.dtype, (rows, d))
-    r, ldr = (None, 0) if R is None else _matrix(R, X.dtype, (rows, d))
-    h, ldh = (None, 0) if H is None else _matrix(H, X.dtype, (rows, d))
-    q, ldq = _matrix(Q, q_dtype, (rows, d))
-    f32 = torch.float32
-    st = getattr(load(), name)(x, ldx, r, ldr, _dense(W, f32, (d,)), eps, _real_type(X), rows, d, h, ldh,
-                               None if rstd is None else _dense(rstd, f32, (rows,)), q, ldq,
-                               _dense(scale, f32, scale_shape), _stream_of(X, stream))
-    _check(st, name)
+def _norm(call, name, X, R, W, eps, H, rstd, Q, q_dtype, scale, scale_shape, stream):
+    T = _torch_names
+    rows, d = shape = X.shape
+    x, ldx = _matrix(X, X.dtype, shape)
+    r, ldr = (None, 0) if R is None else _matrix(R, X.dtype, shape)
+    h, ldh = (None, 0) if H is None else _matrix(H, X.dtype, shape)
+    q, ldq = _matrix(Q, q_dtype, shape)
+    st = call(x, ldx, r, ldr, _dense(W, T.f32, (d,)), eps, _type_of(X, T.real_type), rows, d, h, ldh,
+              None if rstd is None else _dense(rstd, T.f32, (rows,)), q, ldq, _dense(scale, T.f32, scale_shape),
+              _stream_of(X, stream))
+    if st:
+        _check(st, name)
 
 
 def gemm_norm_f8(X, R, W, eps, H, rstd, Q, scale, stream=None) -> None:
     """h = X + R (kept in H), rstd, and y = h * rstd * W as e4m3 Q with scale
     (ceil(d/128), rows).  R, H and rstd may be None (H only without R)."""
-    import torch
+    lib, T = _lib or load(), _torch_names or _torch()
     rows, d = X.shape
-    _norm("gemm_norm_f8", X, R, W, eps, H, rstd, Q, torch.float8_e4m3fn, scale, ((d + 127) // 128, rows), stream)
+    _norm(lib.gemm_norm_f8, "gemm_norm_f8", X, R, W, eps, H, rstd, Q, T.f8[0], scale, ((d + 127) // 128, rows), stream)
 
 
 def gemm_norm_i8(X, R, W, eps, H, rstd, Q, row_scale, stream=None) -> None:
     """As gemm_norm_f8 with int8 Q and one scale per row."""
-    import torch
-    _norm("gemm_norm_i8", X, R, W, eps, H, rstd, Q, torch.int8, row_scale, (X.shape[0],), stream)
+    lib, T = _lib or load(), _torch_names or _torch()
+    _norm(lib.gemm_norm_i8, "gemm_norm_i8", X, R, W, eps, H, rstd, Q, T.i8, row_scale, (X.shape[0],), stream)
 
 
 def gemm_norm_backward(dY, H, W, rstd, dR, dX, dW, stream=None) -> None:
     """dX (the gradient of h) and dW from dY, the gradient of y; dR (may be
     None) is the gradient that reaches h as the residual, dW may be None."""
-    import torch
-    rows, d = dY.shape
-    dt, f32 = dY.dtype, torch.float32
-    dy, lddy = _matrix(dY, dt, (rows, d))
-    h, ldh = _matrix(H, dt, (rows, d))
-    r, lddr = (None, 0) if dR is None else _matrix(dR, dt, (rows, d))
-    dx, lddx = _matrix(dX, dt, (rows, d))
-    st = load().gemm_norm_backward(dy, lddy, h, ldh, _dense(W, f32, (d,)), _dense(rstd, f32, (rows,)), r, lddr,
-                                   _real_type(dY), rows, d, dx, lddx, None if dW is None else _dense(dW, f32, (d,)),
-                                   _stream_of(dY, stream))
-    _check(st, "gemm_norm_backward")
+    lib, T = _lib or load(), _torch_names or _torch()
+    rows, d = shape = dY.shape
+    dt = dY.dtype
+    dy, lddy = _matrix(dY, dt, shape)
+    h, ldh = _matrix(H, dt, shape)
+    r, lddr = (None, 0) if dR is None else _matrix(dR, dt, shape)
+    dx, lddx = _matrix(dX, dt, shape)
+    st = lib.gemm_norm_backward(dy, lddy, h, ldh, _dense(W, T.f32, (d,)), _dense(rstd, T.f32, (rows,)), r, lddr,
+                                _type_of(dY, T.real_type), rows, d, dx, lddx,
+                                None if dW is None else _dense(dW, T.f32, (d,)), _stream_of(dY, stream))
+    if st:
+        _check(st, "gemm_norm_backward")
 
 
 # ------------------------------------------------------------ convenience --
