@@ -32,28 +32,47 @@ gemm_status check_f8_shape(int32_t mode, int32_t groups, int64_t m, int64_t k, i
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The tile and split of a product from its sizes.
+// The largest split of the skinny path that keeps every CTA on an SM of its
+// own (two per SM below 64 rows) and at least four blocks per CTA.
+int skinny_split(int64_t tiles, int64_t kb, int bm, int num_sms) {
+    const int64_t room = (bm >= 64 ? 1 : 2) * static_cast<int64_t>(num_sms);
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= room && kb / (s * 2) >= 4) s *= 2;
+    return s;
+}
+
+// The tile and split of a product from its sizes.  Up to 128 rows (of a group,
+// on average) stream Bt.  Beyond, both kernels are estimated from the time
+// that a K block of their tiles was measured to take: a two-SM tile 0.47 us
+// (8192^3), a half 0.36 and a 128 x 128 tile 0.38 (the slope from 256 x 4096 x
+// 4096 to 256 x 8192 x 8192), and 4.7 us to split in two and join (512 x 8192 x
+// 1024 against its slope).  The small tiles win where the large ones leave most
+// SMs idle (513 x 7046 x 1206: 26.5 us in two-SM halves, 19.8 in 50 tiles split
+// in two; 300 x 16384 x 640: 43.9 and 17.0 split in eight) and lose where these
+// fill them (2048^3: 13.3 and 21.4).
 void choose_config(gemm_plan_f8* p) {
     const int64_t kb = ceil_div(p->k, kF8Block);
-    const bool by_rows = p->group_mode == GEMM_GROUP_ROWS;
+    const bool by_rows = p->group_mode == GEMM_GROUP_ROWS, by_k = p->group_mode == GEMM_GROUP_K;
     const int64_t rows = by_rows ? ceil_div(p->m, p->groups) : p->m;   // of a group, on average
-    if (rows <= 128) {
-        // few rows: stream Bt through tiles of 128 of its rows
-        p->path = GEMM_PATH_SKINNY;
-        p->bm = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-        p->bn = 128;
-        const int64_t groups = by_rows ? (p->m < p->groups ? p->m : p->groups) : p->group_mode == GEMM_GROUP_K ? p->groups : 1;
-        const int64_t tiles = groups * ceil_div(rows, p->bm) * ceil_div(p->n, 128);
-        const int64_t room = (p->bm >= 64 ? 1 : 2) * static_cast<int64_t>(p->num_sms);
-        int s = 1;
-        while (s < 8 && tiles * s * 2 <= room && kb / (s * 2) >= 4) s *= 2;
-        p->split_k = s;
-        return;
+    const int64_t groups = by_rows ? (p->m < p->groups ? p->m : p->groups) : p->groups;
+    const int64_t blocks = by_k ? ceil_div(kb, p->groups) : kb;          // of a tile
+    const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    const int64_t small = groups * ceil_div(rows, bm) * ceil_div(p->n, 128);
+    const int split = skinny_split(small, blocks, bm, p->num_sms);
+    bool skinny = rows <= 128;
+    if (!skinny) {
+        const int64_t pairs = p->num_sms / 2 > 0 ? p->num_sms / 2 : 1;
+        const int64_t tiles = groups * ceil_div(rows, 256) * ceil_div(p->n, 256);
+        const double two =
+            static_cast<double>(blocks) * (2 * tiles <= pairs ? 0.36 : 0.47 * static_cast<double>(ceil_div(tiles, pairs)));
+        const double rounds = static_cast<double>(ceil_div(small * split, p->num_sms));
+        const double one = 0.38 * static_cast<double>(ceil_div(blocks, split)) * rounds + (split > 1 ? 4.7 : 0.0);
+        skinny = one < two;
     }
-    p->path = GEMM_PATH_TENSOR;
-    p->bm = 256;
-    p->split_k = 1;
-    p->bn = 256;
+    p->path = skinny ? GEMM_PATH_SKINNY : GEMM_PATH_TENSOR;
+    p->bm = skinny ? bm : 256;
+    p->bn = skinny ? 128 : 256;
+    p->split_k = skinny ? split : 1;
 }
 
 gemm_status make_f8_plan(int32_t mode, int32_t groups, int64_t m, int64_t k, int64_t n, int32_t a_type, int32_t b_type,

@@ -35,6 +35,20 @@ def test_plan_struct_and_fields(lib):
                     assert q.bm in (16, 32, 64, 128) and q.bn == 128 and q.split_k in (1, 2, 4, 8)
 
 
+def test_plan_takes_the_tiles_that_fill_the_sms(lib):
+    def plan(m, k, n, mode=B.GEMM_GROUP_NONE, groups=1):
+        return B.gemm_f8_plan_for_sms(mode, groups, m, k, n, 152)
+
+    assert plan(300, 16384, 640).path == B.GEMM_PATH_SKINNY and plan(300, 16384, 640).split_k == 8
+    assert plan(2000, 2000, 2000).path == B.GEMM_PATH_TENSOR       # enough large tiles
+    assert plan(300, 16384, 9000).path == B.GEMM_PATH_TENSOR
+    assert plan(600, 600, 600).path == B.GEMM_PATH_TENSOR          # a sum too short to split
+    assert plan(1000, 4096, 512, B.GEMM_GROUP_ROWS, 3).split_k > 1
+    big = 2 ** 30                                                  # nothing overflows at the limits
+    assert plan(big, big, big).path == B.GEMM_PATH_TENSOR
+    assert plan(big, 128, 1000, B.GEMM_GROUP_ROWS, 1024).path == B.GEMM_PATH_TENSOR
+
+
 def test_plan_refusals(lib):
     def plan(mode=0, groups=1, m=5, k=128, n=5, a=0, b=0, s=1, sms=152, out=True):
         p = B.gemm_plan_f8()

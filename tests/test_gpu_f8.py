@@ -110,6 +110,17 @@ def test_product_exact(m, k, n, dtype, b_scale):
     run_product(m, k, n, dtype=dtype, b_scale=b_scale, seed=m + 7 * k)
 
 
+@pytest.mark.parametrize("b_scale", [B.GEMM_SCALE_BLOCKS, B.GEMM_SCALE_ROWS])
+@pytest.mark.parametrize("m,k,n", [(129, 5000, 200), (300, 8200, 300), (513, 4700, 640)])
+def test_product_long_sums_with_few_tiles(m, k, n, b_scale):
+    # more than 128 rows on the small tiles, with the sum split over CTAs
+    plan = B.gemm_f8_plan(m, k, n, b_scale=b_scale)
+    assert plan.path == B.GEMM_PATH_SKINNY and plan.bm == 128 and plan.split_k > 1
+    run_product(m, k, n, b_scale=b_scale, dtype=torch.float32, seed=13)
+    run_product(m, k, n, b_scale=b_scale, dtype=torch.bfloat16, seed=14, pitch=n + 3, offset=1)
+    run_product(m, k, n, b_scale=b_scale, dtype=torch.bfloat16, whole=False, seed=15)
+
+
 @pytest.mark.parametrize("types", [(R.E4M3, R.E5M2), (R.E5M2, R.E4M3), (R.E5M2, R.E5M2)])
 @pytest.mark.parametrize("m,k,n", [(3, 500, 200), (300, 700, 400)])
 def test_product_types(m, k, n, types):
@@ -259,6 +270,14 @@ def test_grouped_rows_every_configuration(cfg):
     run_grouped_rows([5, 0, 140, 33, 1, 260], 520, 200, edit=_set(**cfg), seed=51)
 
 
+@pytest.mark.parametrize("sizes", [[300, 0, 200], [500, 1, 0], [0, 0, 450]])
+def test_grouped_rows_long_sums_with_few_tiles(sizes):
+    # the plan knows the mean of the groups only: one may hold every row
+    plan = B.gemm_f8_grouped_plan(B.GEMM_GROUP_ROWS, 3, sum(sizes), 4700, 300)
+    assert plan.path == B.GEMM_PATH_SKINNY and plan.bm == 128 and plan.split_k > 1
+    run_grouped_rows(sizes, 4700, 300, seed=52)
+
+
 def test_grouped_rows_spare_capacity_and_first_offset():
     run_grouped_rows([3, 0, 20], 256, 160, extra=50, first=4, seed=61)
     run_grouped_rows([300, 10, 270], 256, 160, extra=500, first=9, seed=62, dtype=torch.bfloat16)
@@ -336,6 +355,14 @@ def run_grouped_k(sizes, n1, n2, *, seed=0, dtype=torch.float32, b_scale=B.GEMM_
 @pytest.mark.parametrize("name", list(SIZES))
 def test_grouped_k(name, n1, n2):
     run_grouped_k(SIZES[name], n1, n2, seed=91)
+
+
+def test_grouped_k_long_sums_with_few_tiles():
+    kp = B.gemm_f8_padded_k(9000, 2)
+    plan = B.gemm_f8_grouped_plan(B.GEMM_GROUP_K, 2, 200, kp, 130, b_scale=B.GEMM_SCALE_ROWS)
+    assert plan.path == B.GEMM_PATH_SKINNY and plan.split_k > 1
+    run_grouped_k([8000, 1000], 200, 130, seed=95)
+    run_grouped_k([0, 9000], 200, 130, seed=96)
 
 
 def test_grouped_k_block_scales_and_bf16():
