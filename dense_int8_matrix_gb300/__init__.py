@@ -1,4 +1,5 @@
-"""GB300-native dense GEMM: int8 x int8 -> int32 and bf16 x bf16 -> fp32.
+"""GB300-native dense GEMM: int8 x int8 -> int32, bf16 x bf16 -> fp32, FP8 with
+block scales (also by expert), and the 8-bit norms and quantisers beside it.
 
 The compute runs in the CUDA shared library ``libgemm_gb300.so`` built from
 ``csrc/`` for sm_103a; ``binding`` is a thin ctypes layer over its C ABI.

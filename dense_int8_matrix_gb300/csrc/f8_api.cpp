@@ -1,4 +1,6 @@
 // C entry points of the 8-bit operators: argument checks, plans, dispatch.
+#include <algorithm>
+#include <cmath>
 #include <cstring>
 
 #include "context.h"
@@ -32,47 +34,62 @@ gemm_status check_f8_shape(int32_t mode, int32_t groups, int64_t m, int64_t k, i
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The largest split of the skinny path that keeps every CTA on an SM of its
-// own (two per SM below 64 rows) and at least four blocks per CTA.
-int skinny_split(int64_t tiles, int64_t kb, int bm, int num_sms) {
-    const int64_t room = (bm >= 64 ? 1 : 2) * static_cast<int64_t>(num_sms);
-    int s = 1;
-    while (s < 8 && tiles * s * 2 <= room && kb / (s * 2) >= 4) s *= 2;
-    return s;
+// Estimated microseconds of a product of `tiles` tiles of bm rows by 128
+// columns and `blocks` K blocks, split_k CTAs to a tile.  The constants were
+// fitted to the times of every configuration on 238 drawn products on GB300
+// (152 SMs): a block of a tile, what a round of CTAs costs besides, and the
+// join of a split.  Two CTAs share an SM below 64 rows and then take 1.9 times
+// as long; clusters of four and eight cannot use every SM (of eight: 15 fit, 300 x
+// 16384 x 640 17 us; 16 do not, 128 x 8192 x 2048 23 us).
+double skinny_time(double tiles, int64_t blocks, int bm, int split, int num_sms) {
+    const double block = bm <= 32 ? 0.17 : bm == 64 ? 0.22 : 0.40;
+    const double part = bm < 64 ? (split == 8 ? 256.0 : 304.0) / 152 : split == 8 ? 120.0 / 152 : split == 4 ? 128.0 / 152 : 1.0;
+    const double ctas = tiles * split, room = std::max(1.0, std::floor(part * num_sms));
+    const double rounds = std::ceil(ctas / room);
+    const double share = bm < 64 && ctas > num_sms ? 1.9 : 1.0;
+    return rounds * ((bm < 64 ? 3.0 : 3.4) + block * share * static_cast<double>(ceil_div(blocks, split))) +
+           (split > 1 ? 1.0 + 2.5 * bm / 128 : 0.0);
 }
 
-// The tile and split of a product from its sizes.  Up to 128 rows (of a group,
-// on average) stream Bt.  Beyond, both kernels are estimated from the time
-// that a K block of their tiles was measured to take: a two-SM tile 0.47 us
-// (8192^3), a half 0.36 and a 128 x 128 tile 0.38 (the slope from 256 x 4096 x
-// 4096 to 256 x 8192 x 8192), and 4.7 us to split in two and join (512 x 8192 x
-// 1024 against its slope).  The small tiles win where the large ones leave most
-// SMs idle (513 x 7046 x 1206: 26.5 us in two-SM halves, 19.8 in 50 tiles split
-// in two; 300 x 16384 x 640: 43.9 and 17.0 split in eight) and lose where these
-// fill them (2048^3: 13.3 and 21.4).
+// The same for two-SM tiles; fewer than fill half the pairs run as halves.
+double pair_time(double tiles, int64_t blocks, int num_sms) {
+    const double pairs = std::max(1, num_sms / 2);
+    const double b = static_cast<double>(blocks);
+    return 3.6 + (2 * tiles <= pairs ? 0.36 * b : std::ceil(tiles / pairs) * (3.4 + 0.47 * b));
+}
+
+// The tile and split of a product: the least estimate.  Rows are those of a
+// group, on average.  On 139 other drawn products the choice took 3.4 % longer
+// than the best configuration of each, against 6.7 % for tiles chosen by the
+// number of rows and split as far as SMs were idle (100 x 8192 x 8192 21.7 us
+// with 128 rows split in two, 19.9 with two tiles of 64; 128 x 8192 x 2048
+// 23.1 split in eight, whose clusters do not fit at once, and 11.4).
 void choose_config(gemm_plan_f8* p) {
     const int64_t kb = ceil_div(p->k, kF8Block);
     const bool by_rows = p->group_mode == GEMM_GROUP_ROWS, by_k = p->group_mode == GEMM_GROUP_K;
-    const int64_t rows = by_rows ? ceil_div(p->m, p->groups) : p->m;   // of a group, on average
-    const int64_t groups = by_rows ? (p->m < p->groups ? p->m : p->groups) : p->groups;
-    const int64_t blocks = by_k ? ceil_div(kb, p->groups) : kb;          // of a tile
-    const int bm = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    const int64_t small = groups * ceil_div(rows, bm) * ceil_div(p->n, 128);
-    const int split = skinny_split(small, blocks, bm, p->num_sms);
-    bool skinny = rows <= 128;
-    if (!skinny) {
-        const int64_t pairs = p->num_sms / 2 > 0 ? p->num_sms / 2 : 1;
-        const int64_t tiles = groups * ceil_div(rows, 256) * ceil_div(p->n, 256);
-        const double two =
-            static_cast<double>(blocks) * (2 * tiles <= pairs ? 0.36 : 0.47 * static_cast<double>(ceil_div(tiles, pairs)));
-        const double rounds = static_cast<double>(ceil_div(small * split, p->num_sms));
-        const double one = 0.38 * static_cast<double>(ceil_div(blocks, split)) * rounds + (split > 1 ? 4.7 : 0.0);
-        skinny = one < two;
+    const int64_t rows = by_rows ? ceil_div(p->m, p->groups) : p->m;
+    const double groups = static_cast<double>(by_rows ? std::min<int64_t>(p->m, p->groups) : p->groups);
+    const int64_t blocks = by_k ? ceil_div(kb, p->groups) : kb;   // of a tile
+    p->path = GEMM_PATH_TENSOR;
+    p->bm = p->bn = 256;
+    p->split_k = 1;
+    double best = rows <= 64 ? 1e300
+                             : pair_time(groups * static_cast<double>(ceil_div(rows, 256) * ceil_div(p->n, 256)), blocks, p->num_sms);
+    for (int bm = 16; bm <= 128; bm *= 2) {
+        if (bm < 128 && (rows > 4 * bm || bm > 2 * std::max<int64_t>(rows, 16))) continue;
+        if (bm == 128 && rows < 64) continue;
+        const double tiles = groups * static_cast<double>(ceil_div(rows, bm)) * static_cast<double>(ceil_div(p->n, 128));
+        for (int s = 1; s <= 8; s *= 2) {
+            if (s > 1 && blocks / s < 2) break;
+            const double t = skinny_time(tiles, blocks, bm, s, p->num_sms);
+            if (t >= best) continue;
+            best = t;
+            p->path = GEMM_PATH_SKINNY;
+            p->bm = bm;
+            p->bn = 128;
+            p->split_k = s;
+        }
     }
-    p->path = skinny ? GEMM_PATH_SKINNY : GEMM_PATH_TENSOR;
-    p->bm = skinny ? bm : 256;
-    p->bn = skinny ? 128 : 256;
-    p->split_k = skinny ? split : 1;
 }
 
 gemm_status make_f8_plan(int32_t mode, int32_t groups, int64_t m, int64_t k, int64_t n, int32_t a_type, int32_t b_type,

@@ -12,7 +12,7 @@
 // its sums to the CTAs that finish them (one share of the rows of A each)
 // through distributed shared memory, and these add them up in rank order: no
 // scratch, no second launch, and the same bits every time.  Sent, not fetched:
-// remote stores need no answer, and fetching took 3 us where sending takes 1.
+// a remote store needs no answer.
 //
 // Grouped by rows: the tiles of all groups are numbered on the device from the
 // offsets; the grid is as large as any split of the rows could need, and

@@ -12,13 +12,14 @@
 //
 // Roles: warp 0 loads operands, warp 2 copies scales, warps 1 and 3 of the even
 // CTA issue the MMAs of alternate blocks, warps 4-11 scale, add and store.
-// Each role's loop is run by whole warps (one elected lane issues): with a
-// single lane running them, waiting and issuing alone took 700 cycles a block.
+// Each role's loop is run by whole warps (one elected lane issues), so that its
+// branches are uniform: together with the scales' own warp and one barrier
+// round trip per block this took 8192^3 from 459 to 405 us.
 // Grouped products read the group offsets on the device: warp 2 sums them into
 // shared memory first, and every role walks the same list of tiles.
 //
 // What bounds it (GB300, bf16 output, 128 x 128 scales of Bt): 8192^3 takes
-// 400 us, 2.75 PFLOP/s; without the epilogue's TMEM reads and multiply-adds
+// 400 us, 2.75 PFLOP/s (446 on quantised data, under the power limit); without the epilogue's TMEM reads and multiply-adds
 // 311 us (the MMAs, under the power limit), without the multiply-adds alone
 // 350 us.  The epilogue needs 256 cycles of multiply-adds and 140 of TMEM
 // reads per block and scheduler beside the MMAs' 512.  With column scales

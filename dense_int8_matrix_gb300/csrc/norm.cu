@@ -5,7 +5,9 @@
 //   dx = dr + rstd * (g - xhat * mean(g * xhat)),  g = dy * w, xhat = h * rstd
 //   dw = sum over rows of dy * xhat
 //
-// Both are bound by DRAM: every element is read and written once.
+// Both are bound by DRAM: every element is read and written once.  GB300,
+// 8192 x 8192 bfloat16: forward with residual 81 us (85 % of the measured
+// copy rate), backward with dw 83 us (95 %); odd row lengths 112 and 140 us.
 #include "f8.cuh"
 #include "internal.h"
 #include "ptx.cuh"

@@ -113,12 +113,13 @@ def test_product_exact(m, k, n, dtype, b_scale):
 @pytest.mark.parametrize("b_scale", [B.GEMM_SCALE_BLOCKS, B.GEMM_SCALE_ROWS])
 @pytest.mark.parametrize("m,k,n", [(129, 5000, 200), (300, 8200, 300), (513, 4700, 640)])
 def test_product_long_sums_with_few_tiles(m, k, n, b_scale):
-    # more than 128 rows on the small tiles, with the sum split over CTAs
+    # more than 128 rows on the small tiles, with the sum split over CTAs: as planned, and with 128 rows a tile
     plan = B.gemm_f8_plan(m, k, n, b_scale=b_scale)
-    assert plan.path == B.GEMM_PATH_SKINNY and plan.bm == 128 and plan.split_k > 1
-    run_product(m, k, n, b_scale=b_scale, dtype=torch.float32, seed=13)
-    run_product(m, k, n, b_scale=b_scale, dtype=torch.bfloat16, seed=14, pitch=n + 3, offset=1)
-    run_product(m, k, n, b_scale=b_scale, dtype=torch.bfloat16, whole=False, seed=15)
+    assert plan.path == B.GEMM_PATH_SKINNY and plan.split_k > 1
+    for edit in (None, _set(path=B.GEMM_PATH_SKINNY, bm=128, bn=128, split_k=8)):
+        run_product(m, k, n, b_scale=b_scale, dtype=torch.float32, seed=13, edit=edit)
+        run_product(m, k, n, b_scale=b_scale, dtype=torch.bfloat16, seed=14, pitch=n + 3, offset=1, edit=edit)
+        run_product(m, k, n, b_scale=b_scale, dtype=torch.bfloat16, whole=False, seed=15, edit=edit)
 
 
 @pytest.mark.parametrize("types", [(R.E4M3, R.E5M2), (R.E5M2, R.E4M3), (R.E5M2, R.E5M2)])
@@ -274,8 +275,9 @@ def test_grouped_rows_every_configuration(cfg):
 def test_grouped_rows_long_sums_with_few_tiles(sizes):
     # the plan knows the mean of the groups only: one may hold every row
     plan = B.gemm_f8_grouped_plan(B.GEMM_GROUP_ROWS, 3, sum(sizes), 4700, 300)
-    assert plan.path == B.GEMM_PATH_SKINNY and plan.bm == 128 and plan.split_k > 1
+    assert plan.path == B.GEMM_PATH_SKINNY and plan.split_k > 1
     run_grouped_rows(sizes, 4700, 300, seed=52)
+    run_grouped_rows(sizes, 4700, 300, seed=52, edit=_set(path=B.GEMM_PATH_SKINNY, bm=128, bn=128, split_k=8))
 
 
 def test_grouped_rows_spare_capacity_and_first_offset():
