@@ -28,23 +28,29 @@ __device__ __forceinline__ float cta_reduce(float v, float* red) {
     return MAX ? warp_max(v) : warp_sum(v);
 }
 
-// One CTA per row; the row stays in registers (V vectors of eight values per
-// thread, vector v of thread t at column 8 * (v * blockDim + t), so sixteen
-// neighbouring lanes hold one block of 128 columns).  The mean square is
-// taken of h as it is stored.
-template <typename T, int V, bool I8, bool VEC>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool qvec, bool wvec) {
+// One CTA per row, or (WARP, rows of at most 768 elements) a warp per row and
+// kWarpRows rows per CTA, which spares the CTA's barriers and most of its
+// launches (bfloat16 on GB300: 46323 x 622 95 -> 72 us, 19018 x 384 22 -> 15; at
+// 1024 elements a CTA per row is faster, 23 against 25).  The row stays in
+// registers (V vectors of eight values per thread, vector v of thread t at
+// column 8 * (v * threads + t), so sixteen neighbouring lanes hold one block of
+// 128 columns).  The mean square is taken of h as it is stored.
+constexpr int kWarpRows = 8;
+template <typename T, int V, bool I8, bool VEC, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) norm_fwd_kernel(const NormFwd p, bool qvec, bool wvec) {
     __shared__ float red[2][32];
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t row = blockIdx.x;
+    const int t = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
+    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    if (WARP && row >= p.rows) return;   // whole warps, and no barrier of the CTA
     const T* x = static_cast<const T*>(p.X) + row * p.ldx;
     const T* r = p.R ? static_cast<const T*>(p.R) + row * p.ldr : nullptr;
     Vec8<T> h[V];
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int64_t c = 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x);
+        const int64_t c = 8 * (static_cast<int64_t>(v) * nt + t);
         h[v] = load8<VEC>(x, c, p.d);
         if (r) {
             float a[8], b[8];
@@ -57,22 +63,22 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool qv
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int64_t c = 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x);
+        const int64_t c = 8 * (static_cast<int64_t>(v) * nt + t);
         if (p.H) store8<VEC>(static_cast<T*>(p.H) + row * p.ldh, c, p.d, h[v]);
         float a[8];
         h[v].get(a);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss += a[i] * a[i];
     }
-    ss = cta_reduce<false>(ss, red[0]);
+    ss = WARP ? warp_sum(ss) : cta_reduce<false>(ss, red[0]);
     const float mean = ss / static_cast<float>(p.d) + p.eps;
     const float rstd = 1.f / sqrtf(mean);
-    if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
+    if (t == 0 && p.rstd) p.rstd[row] = rstd;
     float y[V][8];
     float amax = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int64_t c = 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x);
+        const int64_t c = 8 * (static_cast<int64_t>(v) * nt + t);
         float w[8];
         load8_f32(p.W, c, p.d, wvec, w);
         h[v].get(y[v]);
@@ -91,19 +97,19 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p, bool qv
                 store8_bytes(static_cast<uint8_t*>(p.Q) + row * p.ldq, c, p.d, qvec,
                              f8x4<GEMM_F8_E4M3>(y[v][0] * inv, y[v][1] * inv, y[v][2] * inv, y[v][3] * inv),
                              f8x4<GEMM_F8_E4M3>(y[v][4] * inv, y[v][5] * inv, y[v][6] * inv, y[v][7] * inv));
-                if ((threadIdx.x & 15) == 0) p.scale[(c / kF8Block) * p.rows + row] = s;
+                if ((t & 15) == 0) p.scale[(c / kF8Block) * p.rows + row] = s;
             }
         }
     }
     if constexpr (I8) {
-        amax = cta_reduce<true>(amax, red[1]);
+        amax = WARP ? warp_max(amax) : cta_reduce<true>(amax, red[1]);
         const float s = block_scale(amax, kI8Step);
         const float inv = __frcp_rn(s);
         // int8 holds no NaN: the row's scale carries it
-        if (threadIdx.x == 0) p.scale[row] = isfinite(mean) ? s : __int_as_float(0x7fc00000);
+        if (t == 0) p.scale[row] = isfinite(mean) ? s : __int_as_float(0x7fc00000);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int64_t c = 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x);
+            const int64_t c = 8 * (static_cast<int64_t>(v) * nt + t);
             uint32_t w[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -203,6 +209,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool wv
 constexpr int kBwdThreads = 512;
 constexpr int kBwdRingBytes = 200 * 1024;
 constexpr int kBwdSlots = 8;
+constexpr int kRowsPerCta = 6;
 
 // Bytes of one array's row in a slot, and of a slot.
 __host__ __device__ inline uint32_t ring_row_bytes(int64_t d, bool vec) {
@@ -371,30 +378,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_ring_kernel(const Nor
     }
 }
 
-// dW_j = sum of the CTAs' sums: a warp's lanes take 32 columns, the eight
-// warps of a CTA every eighth partial (four loads at a time), joined in warp
-// order.
+// dW_j = sum of the CTAs' sums.  A CTA takes eight columns (a sector of 32
+// bytes of each partial), so that short rows, which leave many partials and few
+// columns, still use many SMs; its 32 groups of eight lanes take every 32nd
+// partial, four loads at a time, and are joined in a fixed order.
 __global__ void __launch_bounds__(256) dw_reduce_kernel(const float* partial, int parts, int64_t d, float* dW) {
-    __shared__ float red[8][32];
+    constexpr int kLoads = 4, kGroups = 32;
+    __shared__ float red[8][8];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (lane & 7);
     float s = 0.f;
     if (c < d) {
-        int i = warp;
-        for (; i + 24 < parts; i += 32) {
-            float v[4];
+        for (int i = warp * 4 + (lane >> 3); i < parts; i += kLoads * kGroups) {
+            float v[kLoads];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = partial[static_cast<int64_t>(i + 8 * j) * d + c];
+            for (int j = 0; j < kLoads; ++j)
+                v[j] = i + j * kGroups < parts ? partial[static_cast<int64_t>(i + j * kGroups) * d + c] : 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s += v[j];
+            for (int j = 0; j < kLoads; ++j) s += v[j];
         }
-        for (; i < parts; i += 8) s += partial[static_cast<int64_t>(i) * d + c];
     }
-    red[warp][lane] = s;
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (lane < 8) red[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < d) {
+    if (threadIdx.x < 8 && c < d) {
+        s = red[0][lane];
 #pragma unroll
         for (int i = 1; i < 8; ++i) s += red[i][lane];
         dW[c] = s;
@@ -422,20 +433,27 @@ bool fwd_vec(const NormFwd& a) {
     return al16(a.X, a.ldx * es) && (!a.R || al16(a.R, a.ldr * es)) && (!a.H || al16(a.H, a.ldh * es));
 }
 
-template <typename T, int V, bool VEC>
+template <typename T, int V, bool VEC, bool WARP>
 cudaError_t fwd_launch(const NormFwd& a, int threads, cudaStream_t stream) {
     const bool qvec = reinterpret_cast<uintptr_t>(a.Q) % 8 == 0 && a.ldq % 8 == 0;
     const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0;
-    return launch_chained(a.to_i8 ? norm_fwd_kernel<T, V, true, VEC> : norm_fwd_kernel<T, V, false, VEC>,
-                          dim3(static_cast<unsigned>(a.rows)), threads, 0, stream, a, qvec, wvec);
+    const int64_t grid = WARP ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows;
+    return launch_chained(a.to_i8 ? norm_fwd_kernel<T, V, true, VEC, WARP> : norm_fwd_kernel<T, V, false, VEC, WARP>,
+                          dim3(static_cast<unsigned>(grid)), threads, 0, stream, a, qvec, wvec);
 }
 
 template <typename T, bool VEC>
 cudaError_t fwd_aligned(const NormFwd& a, cudaStream_t stream) {
+    // a warp per row, once there is a CTA of such for every SM
+    if (a.d <= 768 && a.rows >= static_cast<int64_t>(kWarpRows) * a.num_sms) {
+        constexpr int kThreads = 32 * kWarpRows;
+        return a.d <= 256 ? fwd_launch<T, 1, VEC, true>(a, kThreads, stream)
+               : a.d <= 512 ? fwd_launch<T, 2, VEC, true>(a, kThreads, stream) : fwd_launch<T, 3, VEC, true>(a, kThreads, stream);
+    }
     int t, v;
     row_shape(a.rows, a.d, a.num_sms, &t, &v);
-    return v == 1 ? fwd_launch<T, 1, VEC>(a, t, stream) : v == 2 ? fwd_launch<T, 2, VEC>(a, t, stream)
-                                                                 : fwd_launch<T, 4, VEC>(a, t, stream);
+    return v == 1 ? fwd_launch<T, 1, VEC, false>(a, t, stream) : v == 2 ? fwd_launch<T, 2, VEC, false>(a, t, stream)
+                                                                        : fwd_launch<T, 4, VEC, false>(a, t, stream);
 }
 
 template <typename T>
@@ -464,12 +482,16 @@ bool bwd_vec(const NormBwd& a) {
 bool ring_vec(const NormBwd& a) { return a.d % 8 == 0 && bwd_vec<__nv_bfloat16>(a); }
 
 // Threads of a ring CTA, CTAs per SM (two vectors per thread take 128
-// registers) and rows in its ring.
+// registers) and rows in its ring.  At least six rows per CTA where two CTAs
+// per SM leave that many: each CTA adds d sums to what dw_reduce_kernel reads
+// (8192 x 512 on GB300: 17.7 us with all 16 CTAs per SM, 13.2 with eight).
 void ring_shape(const NormBwd& a, int* threads, int* per_sm, int* slots) {
     const int64_t nv = (a.d + 7) / 8;
     const int v = nv <= kBwdThreads ? 1 : 2;
     *threads = static_cast<int>(((nv + v - 1) / v + 31) / 32 * 32);
-    *per_sm = v == 1 ? 1024 / *threads : 1;
+    const int64_t enough = a.rows / (kRowsPerCta * static_cast<int64_t>(a.num_sms));
+    const int most = v == 1 ? 1024 / *threads : 1;
+    *per_sm = enough < 2 ? (most < 2 ? most : 2) : enough < most ? static_cast<int>(enough) : most;
     const int64_t fit = kBwdRingBytes / *per_sm / (static_cast<int64_t>(ring_row_bytes(a.d, ring_vec(a))) * (a.dR ? 3 : 2));
     *slots = static_cast<int>(fit < kBwdSlots ? fit : kBwdSlots);
 }
@@ -540,7 +562,7 @@ cudaError_t launch_norm_bwd(const NormBwd& a, cudaStream_t stream) {
     cudaError_t e = bwd_ring(a) ? ring_type(a, stream)
                     : a.x_type == GEMM_DTYPE_BF16 ? rows_type<__nv_bfloat16>(a, stream) : rows_type<float>(a, stream);
     if (e == cudaSuccess && a.dW && a.grid > 1)
-        e = launch_chained(dw_reduce_kernel, dim3(static_cast<unsigned>((a.d + 31) / 32)), 256, 0, stream, a.partial, a.grid,
+        e = launch_chained(dw_reduce_kernel, dim3(static_cast<unsigned>((a.d + 7) / 8)), 256, 0, stream, a.partial, a.grid,
                            a.d, a.dW);
     return e;
 }

@@ -103,6 +103,35 @@ def test_norm_forward(rows, d, dtype, residual):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [1, 8, 129, 256, 257, 512, 515, 768, 769])
+def test_norm_many_short_rows(d, dtype):
+    # a warp per row up to 768 elements; the last CTA has fewer rows than warps
+    test_norm_forward(1301, d, dtype, True)
+    test_norm_backward(1301, d, dtype, True)
+
+
+@pytest.mark.parametrize("rows,d", [(1301, 300), (1216, 256)])
+def test_norm_short_rows_in_place(rows, d):
+    test_norm_pitches_and_in_place(rows, d, torch.bfloat16)
+
+
+def test_norm_short_rows_special():
+    # a row of zeros, and a NaN and an infinity that stay in their rows
+    rows, d = 1301, 300
+    x, r, w = inputs(rows, d, 31, torch.bfloat16)
+    h, rstd, y = R.norm(x, r, w, EPS, torch.bfloat16)
+    bad = [4, 9, 1300]
+    x[bad[0]], r[bad[0]] = 0, 0
+    x[bad[1], 7], x[bad[2], 299] = float("nan"), float("inf")
+    keep = torch.ones(rows, dtype=torch.bool)
+    keep[bad] = False
+    Q, S = torch.empty(rows, d, dtype=R.E4M3, device="cuda"), torch.empty(3, rows, device="cuda")
+    B.gemm_norm_f8(x.cuda(), r.cuda(), w.cuda(), EPS, torch.empty_like(x).cuda(), None, Q, S)
+    check_f8(Q[keep.cuda()].contiguous(), S[:, keep.cuda()].contiguous(), y[keep])
+    assert bool((Q[bad[0]].float() == 0).all()) and bool(torch.isnan(Q[bad[1]].float()).any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,d", [(3, 777), (400, 256)])
 def test_norm_pitches_and_in_place(rows, d, dtype):
     x, r, w = inputs(rows, d, 5, dtype)
