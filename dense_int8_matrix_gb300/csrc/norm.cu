@@ -512,7 +512,7 @@ template <typename T, int V, bool VEC>
 cudaError_t rows_launch(const NormBwd& a, int threads, cudaStream_t stream) {
     const size_t smem = a.dW ? static_cast<size_t>(8 * V) * threads * 4 : 0;
     const auto kern = norm_bwd_kernel<T, V, VEC>;
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) {   // 48 KiB hold the static arrays too
         const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), GEMM_NORM_MAX_D * 4, false);
         if (e != cudaSuccess) return e;
     }

@@ -211,6 +211,14 @@ def test_norm_backward(rows, d, dtype, residual):
     assert torch.equal(dX2, dX)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [12032, 12033, 12288, 12289])
+def test_norm_backward_around_48_kib_of_sums(d, dtype):
+    # dw's sums of one CTA take 48 KiB at 12288 columns, what a kernel has without asking for more
+    test_norm_backward(5, d, dtype, True)
+    test_norm_backward(160, d, dtype, False)
+
+
 def test_norm_backward_in_place_and_pitches():
     rows, d = 350, 300
     h, dr, w = inputs(rows, d, 21, torch.bfloat16)
