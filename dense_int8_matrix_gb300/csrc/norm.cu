@@ -418,10 +418,12 @@ bool al16(const void* p, int64_t pitch_bytes) {
 
 // Threads and vectors per thread of a row of d elements.  Many rows at once
 // run best with two vectors per thread (8192 x 8192 bfloat16 on GB300: 1, 2 and
-// 4 vectors 92, 79 and 88 us); a few rows run sooner with one.
-void row_shape(int64_t rows, int64_t d, int num_sms, int* threads, int* vecs) {
+// 4 vectors 92, 79 and 88 us), int8 ones of more than 6144 elements, which wait
+// at a second barrier, with four (97, 106 and 93; 2048 x 12288 two 56, four 47);
+// a few rows run sooner with one.
+void row_shape(int64_t rows, int64_t d, bool to_i8, int num_sms, int* threads, int* vecs) {
     const int64_t nv = (d + 7) / 8;
-    int v = rows > 2 * static_cast<int64_t>(num_sms) ? 2 : 1;
+    int v = rows <= 2 * static_cast<int64_t>(num_sms) ? 1 : to_i8 && d > 6144 ? 4 : 2;
     while (v < 4 && (nv + v - 1) / v > 1024) v *= 2;
     *threads = static_cast<int>(((nv + v - 1) / v + 31) / 32 * 32);
     *vecs = v;
@@ -451,7 +453,7 @@ cudaError_t fwd_aligned(const NormFwd& a, cudaStream_t stream) {
                : a.d <= 512 ? fwd_launch<T, 2, VEC, true>(a, kThreads, stream) : fwd_launch<T, 3, VEC, true>(a, kThreads, stream);
     }
     int t, v;
-    row_shape(a.rows, a.d, a.num_sms, &t, &v);
+    row_shape(a.rows, a.d, a.to_i8, a.num_sms, &t, &v);
     return v == 1 ? fwd_launch<T, 1, VEC, false>(a, t, stream) : v == 2 ? fwd_launch<T, 2, VEC, false>(a, t, stream)
                                                                         : fwd_launch<T, 4, VEC, false>(a, t, stream);
 }

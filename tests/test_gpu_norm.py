@@ -152,6 +152,12 @@ def test_norm_pitches_and_in_place(rows, d, dtype):
         check_f8(Q[0].contiguous(), S, y)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [6144, 6145, 8191, 12288])
+def test_norm_many_long_rows(d, dtype):
+    test_norm_forward(310, d, dtype, True)
+
+
 def test_norm_special_rows():
     rows, d = 6, 300
     x, _, w = inputs(rows, d, 9, torch.float32)
