@@ -104,7 +104,7 @@ __device__ void find_block_rows(const F8Quant& p, int pb, int lane, int& row, in
         n = row < rows ? min(kF8Block, rows - row) : -1;
         return;
     }
-    int before = 0;   // padded blocks of the groups before this round
+    int before = 0;   // padded blocks of the groups before these 32
     row = 0;
     n = -1;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
