@@ -222,6 +222,17 @@ __device__ __forceinline__ float warp_max(float v) {
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
+// The larger of two values, NaN if either is (fmaxf drops a NaN).
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float warp_max_or_nan(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max_or_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
 // Largest of the 16 lanes of this half warp (one block of 128 columns).
 __device__ __forceinline__ float half_warp_max(float v) {
 #pragma unroll

@@ -16,16 +16,17 @@ namespace gemm {
 
 namespace {
 
-// Sum (or largest) over the CTA; `red` is used by this call alone.
+// Sum (or largest, NaN if any value is) over the CTA; `red` is used by this
+// call alone.
 template <bool MAX>
 __device__ __forceinline__ float cta_reduce(float v, float* red) {
-    v = MAX ? warp_max(v) : warp_sum(v);
+    v = MAX ? warp_max_or_nan(v) : warp_sum(v);
     const int warps = blockDim.x >> 5;
     if (warps == 1) return v;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     v = (threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f;
-    return MAX ? warp_max(v) : warp_sum(v);
+    return MAX ? warp_max_or_nan(v) : warp_sum(v);
 }
 
 // One CTA per row, or (WARP, rows of at most 768 elements) a warp per row and
@@ -86,10 +87,10 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) norm_fwd_kernel(
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             y[v][i] = y[v][i] * rstd * w[i];
-            a = fmaxf(a, fabsf(y[v][i]));
+            a = I8 ? max_or_nan(a, fabsf(y[v][i])) : fmaxf(a, fabsf(y[v][i]));
         }
         if constexpr (I8) {
-            amax = fmaxf(amax, a);
+            amax = max_or_nan(amax, a);
         } else {
             const float s = block_scale(half_warp_max(a), kE4M3Step);
             const float inv = __frcp_rn(s);
@@ -102,11 +103,12 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) norm_fwd_kernel(
         }
     }
     if constexpr (I8) {
-        amax = WARP ? warp_max(amax) : cta_reduce<true>(amax, red[1]);
-        const float s = block_scale(amax, kI8Step);
+        amax = WARP ? warp_max_or_nan(amax) : cta_reduce<true>(amax, red[1]);
+        // int8 holds no NaN: the row's scale carries it, be it of h (mean) or of
+        // y alone (a NaN in w, 0 * inf), and the row's values are then zeros
+        const float s = isfinite(mean) && !isnan(amax) ? block_scale(amax, kI8Step) : __int_as_float(0x7fc00000);
         const float inv = __frcp_rn(s);
-        // int8 holds no NaN: the row's scale carries it
-        if (t == 0) p.scale[row] = isfinite(mean) ? s : __int_as_float(0x7fc00000);
+        if (t == 0) p.scale[row] = s;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int64_t c = 8 * (static_cast<int64_t>(v) * nt + t);

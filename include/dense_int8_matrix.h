@@ -412,8 +412,9 @@ GEMM_API int64_t gemm_f8_padded_k(int64_t rows, int32_t groups);
  * gemm_norm_f8 writes y as e4m3 with GEMM_SCALE_ROWS scales, ready as A of
  * gemm_f8_run.  gemm_norm_i8 writes int8 with one scale per row (M = 127),
  * nearest integer, ties to even: ready as A and
- * row_scale of gemm_i8_run_requant; a row whose mean square is infinite or
- * NaN has a NaN scale.  H (may be NULL if R is NULL) gets h and may be X or R itself (with
+ * row_scale of gemm_i8_run_requant.  int8 holds no NaN, so a row with a NaN
+ * among its y_j (in h or W, 0 * infinity, or a row of zeros with eps = 0), or
+ * whose mean square is infinite, has a NaN scale.  H (may be NULL if R is NULL) gets h and may be X or R itself (with
  * that one's pitch); rstd (rows floats, may be NULL) is kept for the
  * backward pass.  W: d floats.  Pitches ldx, ldr, ldh, ldq in elements.
  * d <= GEMM_NORM_MAX_D; eps >= 0.
