@@ -376,6 +376,7 @@ class _Torch:
         self.real_type = {torch.bfloat16: GEMM_DTYPE_BF16, torch.float32: GEMM_DTYPE_F32}
         self.out_type = {torch.bfloat16: GEMM_OUT_BF16, torch.float32: GEMM_OUT_F32}
         self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.current_device = torch._C._cuda_getDevice
 
 
 _torch_names = None
@@ -395,35 +396,45 @@ def _type_of(x, types):
     return found
 
 
-def _stream_of(x, stream):
-    """The CUDA stream handle; by default the current stream of x's device."""
+def _stream_of(dev, stream):
+    """The CUDA stream handle for a call on tensors of device `dev`; by default
+    its current stream.  The library works on the current device (its SMs, its
+    scratch, its launches), so that is the only one whose tensors it takes."""
+    if dev < 0:
+        raise ValueError("tensor must be on a CUDA device")
+    here = _torch_names.current_device()
+    if dev != here:
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (dev, here))
     if stream is None:
-        return _torch_names.raw_stream(x.get_device())
+        return _torch_names.raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _wrong(x, dtype, shape):
+def _wrong(x, dtype, shape, dev):
     if x.dtype is not dtype:
         raise TypeError("expected %s, got %s" % (dtype, x.dtype))
     if x.shape != shape:
         raise ValueError("expected shape %s, got %s" % (tuple(shape), tuple(x.shape)))
-    if not x.is_cuda:
+    if x.get_device() < 0:
         raise ValueError("tensor must be on a CUDA device")
+    if x.get_device() != dev:   # (dev itself is -1 if the first tensor is on the host)
+        raise ValueError("the tensors of a call must be on one device: %d and %d" % (dev, x.get_device()))
     raise ValueError("tensor must be contiguous")
 
 
-def _dense(x, dtype, shape):
-    """Address of a contiguous CUDA tensor."""
-    if x.dtype is not dtype or x.shape != shape or not x.is_cuda or not x.is_contiguous():
-        _wrong(x, dtype, shape)
+def _dense(x, dtype, shape, dev):
+    """Address of a contiguous tensor of device `dev` (_stream_of checks dev)."""
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != dev or not x.is_contiguous():
+        _wrong(x, dtype, shape, dev)
     return x.data_ptr()
 
 
-def _matrix(x, dtype, shape):
-    """(address, row pitch) of a CUDA tensor whose rows are contiguous; the
-    leading dimensions before the last two lie one after the other."""
-    if x.dtype is not dtype or x.shape != shape or not x.is_cuda:
-        _wrong(x, dtype, shape)
+def _matrix(x, dtype, shape, dev):
+    """(address, row pitch) of a tensor of device `dev` whose rows are
+    contiguous; the leading dimensions before the last two lie one after the
+    other."""
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != dev:
+        _wrong(x, dtype, shape, dev)
     stride = x.stride()
     cols = shape[-1]
     groups = shape[0] if len(shape) == 3 else 1
@@ -444,20 +455,21 @@ def _f8_run(plan, A, a_scale, Bt, b_scale, offsets, D, stream):
     lib, T = _lib or load(), _torch_names or _torch()
     m, k, n, g, mode = plan.m, plan.k, plan.n, plan.groups, plan.group_mode
     kb = (k + 127) // 128
-    a, lda = _matrix(A, T.f8[plan.a_type], (m, k))
+    dev = A.get_device()
+    a, lda = _matrix(A, T.f8[plan.a_type], (m, k), dev)
     rows = mode == GEMM_GROUP_ROWS
-    b, ldb = _matrix(Bt, T.f8[plan.b_type], (g, n, k) if rows else (n, k))
+    b, ldb = _matrix(Bt, T.f8[plan.b_type], (g, n, k) if rows else (n, k), dev)
     if plan.b_scale == GEMM_SCALE_BLOCKS:
-        sb = _dense(b_scale, T.f32, (g, (n + 127) // 128, kb) if rows else ((n + 127) // 128, kb))
+        sb = _dense(b_scale, T.f32, (g, (n + 127) // 128, kb) if rows else ((n + 127) // 128, kb), dev)
     else:
-        sb = _dense(b_scale, T.f32, (kb, g * n) if rows else (kb, n))
-    sa = _dense(a_scale, T.f32, (kb, m))
+        sb = _dense(b_scale, T.f32, (kb, g * n) if rows else (kb, n), dev)
+    sa = _dense(a_scale, T.f32, (kb, m), dev)
     out = _type_of(D, T.out_type)
-    d, ldd = _matrix(D, D.dtype, (g, m, n) if mode == GEMM_GROUP_K else (m, n))
-    s = _stream_of(A, stream)
+    d, ldd = _matrix(D, D.dtype, (g, m, n) if mode == GEMM_GROUP_K else (m, n), dev)
+    s = _stream_of(dev, stream)
     if offsets is None:
         return lib.gemm_f8_run(plan, a, lda, sa, b, ldb, sb, out, d, ldd, s)
-    off = _dense(offsets, T.i32, (g + 1,))
+    off = _dense(offsets, T.i32, (g + 1,), dev)
     return lib.gemm_f8_grouped_run(plan, a, lda, sa, b, ldb, sb, off, out, d, ldd, s)
 
 
@@ -490,12 +502,13 @@ def gemm_f8_quantize(X, Q, scale, scale_mode: int = GEMM_SCALE_ROWS, stream=None
     for GEMM_SCALE_BLOCKS."""
     lib, T = _lib or load(), _torch_names or _torch()
     rows, cols = shape = X.shape
-    x, ldx = _matrix(X, X.dtype, shape)
-    q, ldq = _matrix(Q, Q.dtype, shape)
+    dev = X.get_device()
+    x, ldx = _matrix(X, X.dtype, shape, dev)
+    q, ldq = _matrix(Q, Q.dtype, shape, dev)
     kb = (cols + 127) // 128
+    sshape = (kb, rows) if scale_mode == GEMM_SCALE_ROWS else ((rows + 127) // 128, kb)
     st = lib.gemm_f8_quantize(x, _type_of(X, T.real_type), rows, cols, ldx, _type_of(Q, T.f8_type), scale_mode, q, ldq,
-                              _dense(scale, T.f32, (kb, rows) if scale_mode == GEMM_SCALE_ROWS else ((rows + 127) // 128, kb)),
-                              _stream_of(X, stream))
+                              _dense(scale, T.f32, sshape, dev), _stream_of(dev, stream))
     if st:
         _check(st, "gemm_f8_quantize")
 
@@ -506,13 +519,14 @@ def gemm_f8_quantize_cols(X, Q, scale, offsets=None, stream=None) -> None:
     groups + 1 int32 on the GPU, None for one group of all rows."""
     lib, T = _lib or load(), _torch_names or _torch()
     rows, cols = shape = X.shape
+    dev = X.get_device()
     groups = 1 if offsets is None else offsets.shape[0] - 1
     kp = (rows + 127 * groups) // 128 * 128
-    x, ldx = _matrix(X, X.dtype, shape)
-    q, ldq = _matrix(Q, Q.dtype, (cols, kp))
-    off = None if offsets is None else _dense(offsets, T.i32, (groups + 1,))
+    x, ldx = _matrix(X, X.dtype, shape, dev)
+    q, ldq = _matrix(Q, Q.dtype, (cols, kp), dev)
+    off = None if offsets is None else _dense(offsets, T.i32, (groups + 1,), dev)
     st = lib.gemm_f8_quantize_cols(x, _type_of(X, T.real_type), rows, cols, ldx, _type_of(Q, T.f8_type), off, groups, q,
-                                   ldq, _dense(scale, T.f32, (kp // 128, cols)), _stream_of(X, stream))
+                                   ldq, _dense(scale, T.f32, (kp // 128, cols), dev), _stream_of(dev, stream))
     if st:
         _check(st, "gemm_f8_quantize_cols")
 
@@ -520,13 +534,14 @@ def gemm_f8_quantize_cols(X, Q, scale, offsets=None, stream=None) -> None:
 def _norm(call, name, X, R, W, eps, H, rstd, Q, q_dtype, scale, scale_shape, stream):
     T = _torch_names
     rows, d = shape = X.shape
-    x, ldx = _matrix(X, X.dtype, shape)
-    r, ldr = (None, 0) if R is None else _matrix(R, X.dtype, shape)
-    h, ldh = (None, 0) if H is None else _matrix(H, X.dtype, shape)
-    q, ldq = _matrix(Q, q_dtype, shape)
-    st = call(x, ldx, r, ldr, _dense(W, T.f32, (d,)), eps, _type_of(X, T.real_type), rows, d, h, ldh,
-              None if rstd is None else _dense(rstd, T.f32, (rows,)), q, ldq, _dense(scale, T.f32, scale_shape),
-              _stream_of(X, stream))
+    dev = X.get_device()
+    x, ldx = _matrix(X, X.dtype, shape, dev)
+    r, ldr = (None, 0) if R is None else _matrix(R, X.dtype, shape, dev)
+    h, ldh = (None, 0) if H is None else _matrix(H, X.dtype, shape, dev)
+    q, ldq = _matrix(Q, q_dtype, shape, dev)
+    st = call(x, ldx, r, ldr, _dense(W, T.f32, (d,), dev), eps, _type_of(X, T.real_type), rows, d, h, ldh,
+              None if rstd is None else _dense(rstd, T.f32, (rows,), dev), q, ldq, _dense(scale, T.f32, scale_shape, dev),
+              _stream_of(dev, stream))
     if st:
         _check(st, name)
 
@@ -550,14 +565,14 @@ def gemm_norm_backward(dY, H, W, rstd, dR, dX, dW, stream=None) -> None:
     None) is the gradient that reaches h as the residual, dW may be None."""
     lib, T = _lib or load(), _torch_names or _torch()
     rows, d = shape = dY.shape
-    dt = dY.dtype
-    dy, lddy = _matrix(dY, dt, shape)
-    h, ldh = _matrix(H, dt, shape)
-    r, lddr = (None, 0) if dR is None else _matrix(dR, dt, shape)
-    dx, lddx = _matrix(dX, dt, shape)
-    st = lib.gemm_norm_backward(dy, lddy, h, ldh, _dense(W, T.f32, (d,)), _dense(rstd, T.f32, (rows,)), r, lddr,
+    dt, dev = dY.dtype, dY.get_device()
+    dy, lddy = _matrix(dY, dt, shape, dev)
+    h, ldh = _matrix(H, dt, shape, dev)
+    r, lddr = (None, 0) if dR is None else _matrix(dR, dt, shape, dev)
+    dx, lddx = _matrix(dX, dt, shape, dev)
+    st = lib.gemm_norm_backward(dy, lddy, h, ldh, _dense(W, T.f32, (d,), dev), _dense(rstd, T.f32, (rows,), dev), r, lddr,
                                 _type_of(dY, T.real_type), rows, d, dx, lddx,
-                                None if dW is None else _dense(dW, T.f32, (d,)), _stream_of(dY, stream))
+                                None if dW is None else _dense(dW, T.f32, (d,), dev), _stream_of(dev, stream))
     if st:
         _check(st, "gemm_norm_backward")
 
