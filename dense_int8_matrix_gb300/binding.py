@@ -199,8 +199,14 @@ def gemm_plan_for_sms(dtype: int, m: int, k: int, n: int, num_sms: int) -> gemm_
 
 # -------------------------------------------------------------------- run --
 
+def _current_device() -> int:
+    import torch
+    return torch._C._cuda_getDevice()
+
+
 def _addr(x, dtype=None, shape=None, device=True):
-    """Address of a tensor (after checks) or an integer address as is."""
+    """Address of a tensor (after checks) or an integer address as is.  The
+    library works on the current device, so a CUDA tensor has to be there."""
     if x is None:
         return None
     if isinstance(x, int):
@@ -216,6 +222,8 @@ def _addr(x, dtype=None, shape=None, device=True):
         raise ValueError("tensor must be contiguous")
     if device and not x.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
+    if device and x.get_device() != _current_device():
+        raise ValueError("the tensor is on cuda:%d, the current device is cuda:%d" % (x.get_device(), _current_device()))
     if not device and x.is_cuda:
         raise ValueError("tensor must be in host memory")
     return x.data_ptr()

@@ -9,7 +9,7 @@ import torch
 
 from dense_int8_matrix_gb300 import binding as B
 
-F8, BF16, F32, I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
+F8, BF16, F32, I32, I8 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32, torch.int8
 
 
 class Placed(torch.Tensor):
@@ -102,3 +102,41 @@ def test_only_tensors_of_the_current_device_reach_the_library(name, calls):
     with pytest.raises(ValueError, match="CUDA device"):
         call(*tensors([-1] * n))
     assert len(calls) == 1, "a refused call reached the library"
+
+
+def plan(m, k, n):
+    p = B.gemm_plan()
+    p.m, p.k, p.n = m, k, n
+    return p
+
+
+OLDER = {
+    "gemm_i8_run": (lambda a, b, c: B.gemm_i8_run(plan(4, 32, 8), a, b, c, stream=7), [(4, 32, I8), (8, 32, I8), (4, 8, I32)]),
+    "gemm_bf16_run": (lambda a, b, c: B.gemm_bf16_run(plan(4, 32, 8), a, b, c, stream=7),
+                      [(4, 32, BF16), (8, 32, BF16), (4, 8, F32)]),
+    "gemm_i8_run_noalloc": (lambda a, b, c: B.gemm_i8_run_noalloc(plan(4, 32, 8), a, b, c, stream=7),
+                            [(4, 32, I8), (8, 32, I8), (4, 8, I32)]),
+    "gemm_i8_run_requant": (lambda a, b, r, s, d: B.gemm_i8_run_requant(plan(4, 32, 8), a, b, r, s, d, stream=7),
+                            [(4, 32, I8), (8, 32, I8), (4, F32), (8, F32), (4, 8, BF16)]),
+}
+
+
+@pytest.mark.parametrize("name", list(OLDER))
+def test_the_int8_and_bf16_products_take_the_current_device_only(name, calls, monkeypatch):
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    call, operands = OLDER[name]
+    n = len(operands)
+
+    def tensors(devs):
+        return [on(d, *o[:-1], dtype=o[-1]) for d, o in zip(devs, operands)]
+
+    call(*tensors([0] * n))
+    assert calls == [name]
+    for i in range(n):
+        devs = [0] * n
+        devs[i] = 1
+        with pytest.raises(ValueError, match="current device"):
+            call(*tensors(devs))
+    with pytest.raises(ValueError, match="current device"):
+        call(*tensors([1] * n))
+    assert calls == [name]
