@@ -393,6 +393,7 @@ gemm_status gemm_norm_backward(const void* dY, int64_t lddy, const void* H, int6
         a.partial = static_cast<float*>(ws);
     }
     const gemm_status r = staged([&] { return launch_norm_bwd(a, s); }, s);
+    if (r == GEMM_OK && ws) trace_launch(GEMM_KERNEL_STAGE);   // dw's sums are added by a second kernel
     if (ws) cudaFreeAsync(ws, s);
     return r;
 }
