@@ -104,7 +104,10 @@ __device__ __forceinline__ void group_prefix(const int32_t* offsets, int groups,
             group_rows(offsets, g0 + lane, rows, lo, hi);
             c = (hi - lo + per - 1) / per;
         }
-        int sum = c;   // at most 32 * 2^30 / 128
+        // stays in 32 bits: of 32 clamped ranges in a row at most every other one can
+        // start over, so they hold at most 16 times the rows (2^30), 2^30 / 16
+        // pieces of the least size each time, and `before` is at most 2^26 + 1024
+        int sum = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int t = __shfl_up_sync(0xffffffffu, sum, o);
