@@ -23,7 +23,7 @@ struct F8Params {
     int tiles_m, tiles_n; // tiles of one group's D (GEMM_GROUP_ROWS: tiles_n alone)
     int out_f32;
     int d_vec;            // rows of D are 16-byte aligned
-    int halves;           // two-SM kernel: every tile in halves of 128 columns
+    int halves;           // two-SM kernel: every tile in halves of 128 columns (plans edited to bn = 128)
     int pieces;           // row tiles that all groups together can have (GEMM_GROUP_ROWS)
 };
 

@@ -19,11 +19,16 @@
 // shared memory first, and every role walks the same list of tiles.
 //
 // What bounds it (GB300, bf16 output, 128 x 128 scales of Bt): 8192^3 takes
-// 400 us, 2.75 PFLOP/s (446 on quantised data, under the power limit); without the epilogue's TMEM reads and multiply-adds
-// 311 us (the MMAs, under the power limit), without the multiply-adds alone
-// 350 us.  The epilogue needs 256 cycles of multiply-adds and 140 of TMEM
-// reads per block and scheduler beside the MMAs' 512.  With column scales
-// (1 x 128 for both) the multiply-adds double: 8192^3 to fp32 570 us.
+// 395 us, 2.79 PFLOP/s (450 on quantised data, under the power limit); without
+// the epilogue's TMEM reads and multiply-adds 311 us (the MMAs, under the power
+// limit), without the multiply-adds alone 350 us.  Per block and scheduler the
+// epilogue's 256 cycles of multiply-adds and 140 of TMEM reads would fit beside
+// the MMAs' 512, so it is not their number: at 4096^3 the tensor pipe is busy for
+// 49 % of the time, a scheduler issues in 41 % of its cycles, and what warps wait
+// for most is the TMEM read, whose latency each block's chain of reads pays.
+// With column scales (1 x 128 for both) the multiply-adds double to the MMAs'
+// own time: 8192^3 to fp32 580 us, which is longer than either; what the rest
+// is has not been profiled.
 #include <cuda_runtime.h>
 
 #include <cstring>

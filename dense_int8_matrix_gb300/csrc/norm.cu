@@ -6,8 +6,10 @@
 //   dw = sum over rows of dy * xhat
 //
 // Both are bound by DRAM: every element is read and written once.  GB300,
-// 8192 x 8192 bfloat16: forward with residual 81 us (85 % of the measured
-// copy rate), backward with dw 83 us (95 %); odd row lengths 112 and 140 us.
+// 8192 x 8192: bfloat16 forward with residual 81 us (86 % of the measured copy
+// rate; int8 95 us), backward with dw 83 us (97 %); fp32 139 and 223 us (93 and
+// 72 %).  Rows that are not whole 16-byte words: forward 39 to 48 % (8192 x 8191
+// 145 us, 16385 x 1001 37), backward 33 to 58 % (138 and 54 us).
 #include "f8.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -31,7 +33,7 @@ __device__ __forceinline__ float cta_reduce(float v, float* red) {
 
 // One CTA per row, or (WARP, rows of at most 768 elements) a warp per row and
 // kWarpRows rows per CTA, which spares the CTA's barriers and most of its
-// launches (bfloat16 on GB300: 46323 x 622 95 -> 72 us, 19018 x 384 22 -> 15; at
+// launches (bfloat16 on GB300: 46323 x 622 95 -> 76 us, 19018 x 384 22 -> 15; at
 // 1024 elements a CTA per row is faster, 23 against 25).  The row stays in
 // registers (V vectors of eight values per thread, vector v of thread t at
 // column 8 * (v * threads + t), so sixteen neighbouring lanes hold one block of
@@ -126,7 +128,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) norm_fwd_kernel(
 // Persistent CTAs over the rows.  A thread owns the same columns of every row
 // (eight per vector), and dw's running sums of the CTA's rows stay in shared
 // memory, one word per thread and column so that no two lanes share a bank.
-// They go to `partial`, which dw_reduce_kernel adds up in CTA order.
+// They go to `partial`, which dw_reduce_kernel adds up in CTA order.  It takes
+// what the ring kernel below does not: fp32, rows beyond 8192 elements, few
+// rows.  The whole row is held in registers, which 1024 threads do not have for
+// wide rows: bfloat16 with four vectors per thread and fp32 with two spill 160 to
+// 256 bytes, fp32 with four (32 registers) about 2 KB.  GB300, bfloat16 2048 x
+// 16384 79 us (51 % of the measured copy rate), 2048 x 32768 185 (43 %); fp32
+// 8192 x 8192 223 (72 %), 2048 x 16384 140 (57 %), 2048 x 32768 559 (29 %).
 template <typename T, int V, bool VEC>
 __global__ void __launch_bounds__(1024) norm_bwd_kernel(const NormBwd p, bool wvec) {
     extern __shared__ float dw[];   // [V * 8][threads]
@@ -488,7 +496,12 @@ bool ring_vec(const NormBwd& a) { return a.d % 8 == 0 && bwd_vec<__nv_bfloat16>(
 // Threads of a ring CTA, CTAs per SM (two vectors per thread take 128
 // registers) and rows in its ring.  At least six rows per CTA where two CTAs
 // per SM leave that many: each CTA adds d sums to what dw_reduce_kernel reads
-// (8192 x 512 on GB300: 17.7 us with all 16 CTAs per SM, 13.2 with eight).
+// (8192 x 512 on GB300: 17.7 us with all 16 CTAs per SM, 13.2 with eight).  The
+// count takes 1024 threads per SM, which the form for aligned rows has registers
+// for (63 a thread).  That for unaligned ones (95) has them for 640, so of eight
+// CTAs of 128 threads five run at once and the others start as these end; and of
+// 32 CTAs of one warp with full rings about 30 fit in shared memory, of which
+// each holds 1 KiB besides.
 void ring_shape(const NormBwd& a, int* threads, int* per_sm, int* slots) {
     const int64_t nv = (a.d + 7) / 8;
     const int v = nv <= kBwdThreads ? 1 : 2;
@@ -548,7 +561,8 @@ cudaError_t launch_norm_fwd(const NormFwd& a, cudaStream_t stream) {
     return a.x_type == GEMM_DTYPE_BF16 ? fwd_type<__nv_bfloat16>(a, stream) : fwd_type<float>(a, stream);
 }
 
-// As many CTAs as run at once: each keeps its own dw.
+// Persistent CTAs, each with its own dw: as many as run at once (more of some
+// unaligned and short rows, see ring_shape).
 int norm_bwd_grid(const NormBwd& a) {
     if (bwd_ring(a)) {
         int threads, per_sm, slots;
