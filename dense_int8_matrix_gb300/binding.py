@@ -42,6 +42,17 @@ GEMM_SCALE_BLOCKS = 1
 GEMM_GROUP_NONE = 0
 GEMM_GROUP_ROWS = 1
 GEMM_GROUP_K = 2
+GEMM_FORM_NT = 0
+GEMM_FORM_NN = 1
+GEMM_FORM_TN = 2
+GEMM_ACT_NONE = 0
+GEMM_ACT_RELU = 1
+GEMM_ACT_GELU = 2
+GEMM_ACT_GELU_TANH = 3
+GEMM_ACT_SILU = 4
+GEMM_ACT_GRADIENT = 16
+GEMM_PLAN_LINEAR_VERSION = 1
+GEMM_BALANCE_MAX_EXPERTS = 1024
 GEMM_PLAN_F8_VERSION = 1
 GEMM_F8_MAX_GROUPS = 1024
 GEMM_NORM_MAX_D = 32768
@@ -57,7 +68,8 @@ EXPORTED = (
     "gemm_i8_run_noalloc", "gemm_pool_usage", "gemm_i8_run_requant",
     "gemm_f8_plan", "gemm_f8_grouped_plan", "gemm_f8_plan_for_sms", "gemm_f8_run", "gemm_f8_grouped_run",
     "gemm_f8_quantize", "gemm_f8_quantize_cols", "gemm_f8_padded_k", "gemm_norm_f8", "gemm_norm_i8",
-    "gemm_norm_backward",
+    "gemm_norm_backward", "gemm_bf16_linear_plan", "gemm_bf16_linear_plan_for_sms", "gemm_bf16_linear_run",
+    "gemm_activation_backward", "gemm_layer_norm", "gemm_layer_norm_backward", "gemm_balance", "gemm_balance_backward",
 )
 
 
@@ -88,6 +100,20 @@ class gemm_plan_f8(ctypes.Structure):
         ("groups", ctypes.c_int32), ("a_type", ctypes.c_int32), ("b_type", ctypes.c_int32),
         ("b_scale", ctypes.c_int32), ("bm", ctypes.c_int32), ("bn", ctypes.c_int32),
         ("split_k", ctypes.c_int32), ("reserved32", ctypes.c_int32),
+        ("reserved", ctypes.c_int64 * 4),
+    ]
+
+    def as_dict(self):
+        return {name: getattr(self, name) for name, _ in self._fields_
+                if not name.startswith("reserved")}
+
+
+class gemm_plan_linear(ctypes.Structure):
+    _fields_ = [
+        ("version", ctypes.c_int32), ("path", ctypes.c_int32), ("num_sms", ctypes.c_int32),
+        ("form", ctypes.c_int32),
+        ("m", ctypes.c_int64), ("k", ctypes.c_int64), ("n", ctypes.c_int64),
+        ("bm", ctypes.c_int32), ("bn", ctypes.c_int32), ("split_k", ctypes.c_int32), ("reserved32", ctypes.c_int32),
         ("reserved", ctypes.c_int64 * 4),
     ]
 
@@ -128,6 +154,7 @@ def load():
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER(gemm_plan)
     P8 = ctypes.POINTER(gemm_plan_f8)
+    PL = ctypes.POINTER(gemm_plan_linear)
     i64, i32, vp, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
     sig = {
         "gemm_i8_plan": [i64, i64, i64, P],
@@ -155,6 +182,14 @@ def load():
         "gemm_norm_f8": [vp, i64, vp, i64, vp, f32, i32, i64, i64, vp, i64, vp, vp, i64, vp, vp],
         "gemm_norm_i8": [vp, i64, vp, i64, vp, f32, i32, i64, i64, vp, i64, vp, vp, i64, vp, vp],
         "gemm_norm_backward": [vp, i64, vp, i64, vp, vp, vp, i64, i32, i64, i64, vp, i64, vp, vp],
+        "gemm_bf16_linear_plan": [i32, i64, i64, i64, PL],
+        "gemm_bf16_linear_plan_for_sms": [i32, i64, i64, i64, i32, PL],
+        "gemm_bf16_linear_run": [PL, vp, i64, vp, i64, vp, i32, vp, i64, vp, i64, i32, vp, i64, vp],
+        "gemm_activation_backward": [vp, i64, vp, i64, i32, i64, i64, vp, i64, vp, vp],
+        "gemm_layer_norm": [vp, i64, vp, i64, vp, vp, f32, i32, i32, i64, i64, vp, i64, vp, vp, vp, i64, vp],
+        "gemm_layer_norm_backward": [vp, i64, vp, i64, vp, vp, vp, vp, i64, i32, i32, i64, i64, vp, i64, vp, vp, vp],
+        "gemm_balance": [vp, i64, i32, i64, i32, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp],
+        "gemm_balance_backward": [vp, i64, i32, i64, i32, vp, vp, vp, f32, vp, vp, i64, vp, i64, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -583,6 +618,140 @@ def gemm_norm_backward(dY, H, W, rstd, dR, dX, dW, stream=None) -> None:
                                 None if dW is None else _dense(dW, T.f32, (d,), dev), _stream_of(dev, stream))
     if st:
         _check(st, "gemm_norm_backward")
+
+
+# ------------------------------------------------- bfloat16 layer operators --
+
+def gemm_bf16_linear_plan(m: int, k: int, n: int, form: int = GEMM_FORM_NT) -> gemm_plan_linear:
+    p = gemm_plan_linear()
+    _check(load().gemm_bf16_linear_plan(form, m, k, n, ctypes.byref(p)), "gemm_bf16_linear_plan")
+    return p
+
+
+def gemm_bf16_linear_plan_for_sms(m: int, k: int, n: int, num_sms: int, form: int = GEMM_FORM_NT) -> gemm_plan_linear:
+    p = gemm_plan_linear()
+    _check(load().gemm_bf16_linear_plan_for_sms(form, m, k, n, num_sms, ctypes.byref(p)), "gemm_bf16_linear_plan_for_sms")
+    return p
+
+
+def _optional(x, dtype, shape, dev):
+    return None if x is None else _dense(x, dtype, shape, dev)
+
+
+def _optional_matrix(x, dtype, shape, dev):
+    return (None, 0) if x is None else _matrix(x, dtype, shape, dev)
+
+
+def gemm_bf16_linear_run(plan: gemm_plan_linear, A, B, D, bias=None, activation: int = GEMM_ACT_NONE, Z=None,
+                         residual=None, stream=None) -> None:
+    """D (m x n, bfloat16 or fp32) = act(A x B + bias) + residual, or with
+    activation | GEMM_ACT_GRADIENT (A x B + bias) * act'(Z) + residual.  A, B:
+    bfloat16, (m, k) and (n, k) for a plan of GEMM_FORM_NT, (m, k) and (k, n)
+    for GEMM_FORM_NN, (k, m) and (k, n) for GEMM_FORM_TN.  bias: fp32 (n,); Z:
+    bfloat16 (m, n), written without the gradient (A x B + bias) and read with
+    it; residual: like D, may be D.  Rows may have a pitch."""
+    lib, T = _lib or load(), _torch_names or _torch()
+    m, k, n, form = plan.m, plan.k, plan.n, plan.form
+    dev = A.get_device()
+    a, lda = _matrix(A, T.bf16, (k, m) if form == GEMM_FORM_TN else (m, k), dev)
+    b, ldb = _matrix(B, T.bf16, (n, k) if form == GEMM_FORM_NT else (k, n), dev)
+    out = _type_of(D, T.out_type)
+    d, ldd = _matrix(D, D.dtype, (m, n), dev)
+    z, ldz = _optional_matrix(Z, T.bf16, (m, n), dev)
+    r, ldr = _optional_matrix(residual, D.dtype, (m, n), dev)
+    st = lib.gemm_bf16_linear_run(plan, a, lda, b, ldb, _optional(bias, T.f32, (n,), dev), activation, z, ldz, r, ldr, out,
+                                  d, ldd, _stream_of(dev, stream))
+    if st:
+        _check(st, "gemm_bf16_linear_run")
+
+
+def gemm_activation_backward(dY, Z, activation, dZ, dbias, stream=None) -> None:
+    """dZ = dY * act'(Z) (bfloat16, may be dY or Z) and dbias (fp32, (cols,))
+    = its sums over the rows; either may be None, Z for GEMM_ACT_NONE too."""
+    lib, T = _lib or load(), _torch_names or _torch()
+    rows, cols = shape = dY.shape
+    dev = dY.get_device()
+    y, lddy = _matrix(dY, T.bf16, shape, dev)
+    z, ldz = _optional_matrix(Z, T.bf16, shape, dev)
+    o, lddz = _optional_matrix(dZ, T.bf16, shape, dev)
+    st = lib.gemm_activation_backward(y, lddy, z, ldz, activation, rows, cols, o, lddz, _optional(dbias, T.f32, (cols,), dev),
+                                      _stream_of(dev, stream))
+    if st:
+        _check(st, "gemm_activation_backward")
+
+
+def gemm_layer_norm(X, R, W, bias, eps, H, mean, rstd, Y, stream=None) -> None:
+    """h = X + R (kept in H), mean and rstd of its rows, and Y (bfloat16 or
+    fp32) = (h - mean) * rstd * W + bias.  R, bias, H (only without R), mean
+    and rstd may be None."""
+    lib, T = _lib or load(), _torch_names or _torch()
+    rows, d = shape = X.shape
+    dt, dev = X.dtype, X.get_device()
+    x, ldx = _matrix(X, dt, shape, dev)
+    r, ldr = _optional_matrix(R, dt, shape, dev)
+    h, ldh = _optional_matrix(H, dt, shape, dev)
+    y, ldy = _matrix(Y, Y.dtype, shape, dev)
+    st = lib.gemm_layer_norm(x, ldx, r, ldr, _dense(W, T.f32, (d,), dev), _optional(bias, T.f32, (d,), dev), eps,
+                             _type_of(X, T.real_type), _type_of(Y, T.real_type), rows, d, h, ldh,
+                             _optional(mean, T.f32, (rows,), dev), _optional(rstd, T.f32, (rows,), dev), y, ldy,
+                             _stream_of(dev, stream))
+    if st:
+        _check(st, "gemm_layer_norm")
+
+
+def gemm_layer_norm_backward(dY, H, W, mean, rstd, dR, dX, dW, dbias, stream=None) -> None:
+    """dX (the gradient of h, like H), dW and dbias (fp32) from dY, the
+    gradient of Y; dR (may be None) is the gradient that reaches h as the
+    residual; dW and dbias may be None."""
+    lib, T = _lib or load(), _torch_names or _torch()
+    rows, d = shape = H.shape
+    dt, dev = H.dtype, H.get_device()
+    dy, lddy = _matrix(dY, dY.dtype, shape, dev)
+    h, ldh = _matrix(H, dt, shape, dev)
+    r, lddr = _optional_matrix(dR, dt, shape, dev)
+    dx, lddx = _matrix(dX, dt, shape, dev)
+    st = lib.gemm_layer_norm_backward(dy, lddy, h, ldh, _dense(W, T.f32, (d,), dev), _dense(mean, T.f32, (rows,), dev),
+                                      _dense(rstd, T.f32, (rows,), dev), r, lddr, _type_of(H, T.real_type),
+                                      _type_of(dY, T.real_type), rows, d, dx, lddx, _optional(dW, T.f32, (d,), dev),
+                                      _optional(dbias, T.f32, (d,), dev), _stream_of(dev, stream))
+    if st:
+        _check(st, "gemm_layer_norm_backward")
+
+
+def gemm_balance(X, index, coef, counts, offsets, used, lse, probs, loss, stream=None) -> None:
+    """Balance loss (fp32, (1,)) of the logits X (rows x experts, bfloat16 or
+    fp32) and the experts chosen for each row, index (rows x top_k, int32; what
+    lies outside [0, experts) is not taken): counts (experts,), offsets
+    (experts + 1,; may be None) and used (1,) int32, lse (rows,) and probs
+    (experts,) fp32."""
+    lib, T = _lib or load(), _torch_names or _torch()
+    rows, experts = shape = X.shape
+    dev = X.get_device()
+    x, ldx = _matrix(X, X.dtype, shape, dev)
+    top_k = index.shape[-1]
+    st = lib.gemm_balance(x, ldx, _type_of(X, T.real_type), rows, experts, _dense(index, T.i32, (rows, top_k), dev), top_k,
+                          coef, _dense(counts, T.i32, (experts,), dev), _optional(offsets, T.i32, (experts + 1,), dev),
+                          _dense(used, T.i32, (1,), dev), _dense(lse, T.f32, (rows,), dev),
+                          _dense(probs, T.f32, (experts,), dev), _dense(loss, T.f32, (1,), dev), _stream_of(dev, stream))
+    if st:
+        _check(st, "gemm_balance")
+
+
+def gemm_balance_backward(X, lse, counts, used, coef, dloss, dR, dX, stream=None) -> None:
+    """dX (like X) = dR + the gradient of gemm_balance's loss times dloss
+    (fp32, (1,)), from lse, counts and used as that call wrote them; dR may be
+    None, or dX itself."""
+    lib, T = _lib or load(), _torch_names or _torch()
+    rows, experts = shape = X.shape
+    dt, dev = X.dtype, X.get_device()
+    x, ldx = _matrix(X, dt, shape, dev)
+    r, lddr = _optional_matrix(dR, dt, shape, dev)
+    dx, lddx = _matrix(dX, dt, shape, dev)
+    st = lib.gemm_balance_backward(x, ldx, _type_of(X, T.real_type), rows, experts, _dense(lse, T.f32, (rows,), dev),
+                                   _dense(counts, T.i32, (experts,), dev), _dense(used, T.i32, (1,), dev), coef,
+                                   _dense(dloss, T.f32, (1,), dev), r, lddr, dx, lddx, _stream_of(dev, stream))
+    if st:
+        _check(st, "gemm_balance_backward")
 
 
 # ------------------------------------------------------------ convenience --

@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "checks.h"
 #include "context.h"
 #include "f8.h"
 #include "internal.h"
@@ -10,14 +11,6 @@
 using namespace gemm;
 
 namespace {
-
-constexpr int64_t kMaxDim = int64_t(1) << 30;   // coordinates of tiles past the edge stay in 32 bits
-
-bool al(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-bool dim_ok(int64_t v) { return v >= 1 && v <= kMaxDim; }
-// Pitches stay far below where rows * pitch * 4 bytes would pass 63 bits.
-bool pitch_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= (int64_t(1) << 31); }
-int elem_bytes(int type) { return type == GEMM_DTYPE_BF16 ? 2 : 4; }
 
 gemm_status check_f8_shape(int32_t mode, int32_t groups, int64_t m, int64_t k, int64_t n, int32_t a_type,
                            int32_t b_type, int32_t b_scale) {
@@ -31,8 +24,6 @@ gemm_status check_f8_shape(int32_t mode, int32_t groups, int64_t m, int64_t k, i
     if (b_scale != GEMM_SCALE_ROWS && b_scale != GEMM_SCALE_BLOCKS) return GEMM_ERR_INVALID_ARG;
     return GEMM_OK;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Estimated microseconds of a product of `tiles` tiles of bm rows by 128
 // columns and `blocks` K blocks, split_k CTAs to a tile.  The constants were
@@ -193,17 +184,6 @@ gemm_status check_quant(const void* X, int32_t x_type, int64_t rows, int64_t col
     if (f8_type != GEMM_F8_E4M3 && f8_type != GEMM_F8_E5M2) return GEMM_ERR_INVALID_ARG;
     if (!pitch_ok(ldx, cols) || !pitch_ok(ldq, qcols)) return GEMM_ERR_INVALID_ARG;
     if (!al(X, elem_bytes(x_type)) || !al(scale, 4)) return GEMM_ERR_MISALIGNED;
-    return GEMM_OK;
-}
-
-template <typename Launch>
-gemm_status staged(Launch launch, cudaStream_t stream) {
-    const bool sampled = trace_begin_call();
-    void* unit = trace_unit_begin(GEMM_KERNEL_STAGE, stream, sampled);
-    const cudaError_t e = launch();
-    trace_unit_end(unit, stream);
-    if (e != cudaSuccess) return GEMM_ERR_CUDA;
-    trace_launch(GEMM_KERNEL_STAGE);
     return GEMM_OK;
 }
 

@@ -1,0 +1,378 @@
+// C entry points of the bfloat16 layer's operators: argument checks, plans,
+// dispatch.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "checks.h"
+#include "context.h"
+#include "internal.h"
+#include "layer.h"
+
+using namespace gemm;
+
+namespace {
+
+// Scratch from the library's pool for one call, returned on the same stream.
+class Scratch {
+  public:
+    Scratch(cudaMemPool_t pool, cudaStream_t stream) : pool_(pool), stream_(stream) {}
+    ~Scratch() {
+        for (void* p : ptr_)
+            if (p) cudaFreeAsync(p, stream_);
+    }
+    Scratch(const Scratch&) = delete;
+    Scratch& operator=(const Scratch&) = delete;
+    void* take(int64_t bytes) {   // nullptr if there is none (at most two per call)
+        void* p = nullptr;
+        if (cudaMallocFromPoolAsync(&p, static_cast<size_t>(bytes), pool_, stream_) != cudaSuccess) return nullptr;
+        ptr_[ptr_[0] ? 1 : 0] = p;
+        return p;
+    }
+
+  private:
+    cudaMemPool_t pool_;
+    cudaStream_t stream_;
+    void* ptr_[2] = {nullptr, nullptr};
+};
+
+bool act_ok(int32_t act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
+
+// ---- products ------------------------------------------------------------------
+gemm_status check_linear_shape(int32_t form, int64_t m, int64_t k, int64_t n) {
+    if (form < GEMM_FORM_NT || form > GEMM_FORM_TN) return GEMM_ERR_INVALID_ARG;
+    return dim_ok(m) && dim_ok(k) && dim_ok(n) ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+}
+
+void choose_linear(gemm_plan_linear* p) {
+    p->path = GEMM_PATH_TENSOR;
+    p->bm = p->bn = 256;
+    p->split_k = 1;
+}
+
+gemm_status make_linear_plan(int32_t form, int64_t m, int64_t k, int64_t n, int32_t num_sms, gemm_plan_linear* out) {
+    if (!out || num_sms < 1) return GEMM_ERR_INVALID_ARG;
+    const gemm_status st = check_linear_shape(form, m, k, n);
+    if (st != GEMM_OK) return st;
+    std::memset(out, 0, sizeof(*out));
+    out->version = GEMM_PLAN_LINEAR_VERSION;
+    out->num_sms = num_sms;
+    out->form = form;
+    out->m = m;
+    out->k = k;
+    out->n = n;
+    choose_linear(out);
+    return GEMM_OK;
+}
+
+bool linear_config_ok(const gemm_plan_linear* p) {
+    return p->path == GEMM_PATH_TENSOR && p->bm == 256 && (p->bn == 128 || p->bn == 256) && p->split_k == 1;
+}
+
+// A matrix that TMA can read as it lies.
+bool tma_rows(const void* p, int64_t ld) { return al(p, 16) && ld % 8 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+gemm_status gemm_bf16_linear_plan(int32_t form, int64_t m, int64_t k, int64_t n, gemm_plan_linear* out) {
+    if (!out) return GEMM_ERR_INVALID_ARG;
+    gemm_status st = check_linear_shape(form, m, k, n);
+    if (st != GEMM_OK) return st;
+    int sms = 0;
+    st = device_sms(&sms);
+    if (st != GEMM_OK) return st;
+    return make_linear_plan(form, m, k, n, sms, out);
+}
+
+gemm_status gemm_bf16_linear_plan_for_sms(int32_t form, int64_t m, int64_t k, int64_t n, int32_t num_sms,
+                                          gemm_plan_linear* out) {
+    return make_linear_plan(form, m, k, n, num_sms, out);
+}
+
+gemm_status gemm_bf16_linear_run(const gemm_plan_linear* plan, const uint16_t* A, int64_t lda, const uint16_t* B,
+                                 int64_t ldb, const float* bias, int32_t activation, uint16_t* Z, int64_t ldz,
+                                 const void* residual, int64_t ldr, int32_t out_type, void* D, int64_t ldd,
+                                 void* stream) {
+    const gemm_plan_linear* p = plan;
+    if (!p || p->version != GEMM_PLAN_LINEAR_VERSION) return GEMM_ERR_INVALID_ARG;
+    if (check_linear_shape(p->form, p->m, p->k, p->n) != GEMM_OK || !linear_config_ok(p)) return GEMM_ERR_INVALID_ARG;
+    if (!A || !B || !D) return GEMM_ERR_INVALID_ARG;
+    const bool grad = (activation & GEMM_ACT_GRADIENT) != 0;
+    const int32_t act = activation & ~GEMM_ACT_GRADIENT;
+    if (!act_ok(act) || (grad && !Z && act != GEMM_ACT_NONE)) return GEMM_ERR_INVALID_ARG;
+    if (out_type != GEMM_OUT_BF16 && out_type != GEMM_OUT_F32) return GEMM_ERR_INVALID_ARG;
+    const int64_t rows_a = p->form == GEMM_FORM_TN ? p->k : p->m, cols_a = p->form == GEMM_FORM_TN ? p->m : p->k;
+    const int64_t rows_b = p->form == GEMM_FORM_NT ? p->n : p->k, cols_b = p->form == GEMM_FORM_NT ? p->k : p->n;
+    if (!pitch_ok(lda, cols_a) || !pitch_ok(ldb, cols_b) || !pitch_ok(ldd, p->n) || (Z && !pitch_ok(ldz, p->n)) ||
+        (residual && !pitch_ok(ldr, p->n)))
+        return GEMM_ERR_INVALID_ARG;
+    if (residual == D && ldr != ldd) return GEMM_ERR_INVALID_ARG;
+    const uintptr_t es = out_type == GEMM_OUT_F32 ? 4 : 2;
+    if (!al(A, 2) || !al(B, 2) || !al(Z, 2) || !al(D, es) || !al(residual, es) || !al(bias, 4)) return GEMM_ERR_MISALIGNED;
+    DeviceContext ctx;
+    const gemm_status st = device_context(&ctx);
+    if (st != GEMM_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    LinearLaunch L;
+    L.A = A;
+    L.B = B;
+    L.bias = bias;
+    L.R = residual;
+    L.Z = Z;
+    L.D = D;
+    L.err = ctx.err_word;
+    L.m = p->m;
+    L.k = p->k;
+    L.n = p->n;
+    L.lda = lda;
+    L.ldb = ldb;
+    L.ldd = ldd;
+    L.ldr = ldr;
+    L.ldz = ldz;
+    L.form = p->form;
+    L.act = act;
+    L.grad = grad;
+    L.out_f32 = out_type == GEMM_OUT_F32;
+    L.bm = p->bm;
+    L.bn = p->bn;
+    L.split_k = p->split_k;
+    L.num_sms = ctx.num_sms;
+    L.pairs = ctx.pairs;
+    Scratch scratch(ctx.pool, s);
+    const bool sampled = trace_begin_call();
+    auto align = [&](const void** at, int64_t* ld, int64_t rows, int64_t cols) {
+        if (tma_rows(*at, *ld)) return GEMM_OK;
+        const int64_t pitch = (cols + 7) / 8 * 8;
+        void* copy = scratch.take(rows * pitch * 2);
+        if (!copy) return GEMM_ERR_CUDA;
+        void* unit = trace_unit_begin(GEMM_KERNEL_STAGE, s, sampled);
+        const cudaError_t e = launch_repitch(*at, *ld, copy, pitch, rows, cols, ctx.num_sms, s);
+        trace_unit_end(unit, s);
+        if (e != cudaSuccess) return GEMM_ERR_CUDA;
+        trace_launch(GEMM_KERNEL_STAGE);
+        *at = copy;
+        *ld = pitch;
+        return GEMM_OK;
+    };
+    gemm_status r = align(&L.A, &L.lda, rows_a, cols_a);
+    if (r == GEMM_OK) r = align(&L.B, &L.ldb, rows_b, cols_b);
+    if (r != GEMM_OK) return r;
+    const int kind = p->path == GEMM_PATH_SKINNY ? GEMM_KERNEL_SKINNY : GEMM_KERNEL_TC;
+    void* unit = trace_unit_begin(kind, s, sampled);
+    const cudaError_t e = launch_linear_tc2(L, s);
+    trace_unit_end(unit, s);
+    if (e != cudaSuccess) return GEMM_ERR_CUDA;
+    trace_launch(kind);
+    return GEMM_OK;
+}
+
+gemm_status gemm_activation_backward(const uint16_t* dY, int64_t lddy, const uint16_t* Z, int64_t ldz,
+                                     int32_t activation, int64_t rows, int64_t cols, uint16_t* dZ, int64_t lddz,
+                                     float* dbias, void* stream) {
+    if (!dY || (!dZ && !dbias) || !act_ok(activation) || (!Z && activation != GEMM_ACT_NONE)) return GEMM_ERR_INVALID_ARG;
+    if (!dim_ok(rows) || !dim_ok(cols)) return GEMM_ERR_INVALID_ARG;
+    if (activation == GEMM_ACT_NONE) Z = nullptr;   // not read
+    if (!pitch_ok(lddy, cols) || (Z && !pitch_ok(ldz, cols)) || (dZ && !pitch_ok(lddz, cols))) return GEMM_ERR_INVALID_ARG;
+    if ((dZ == dY && lddz != lddy) || (dZ && dZ == Z && lddz != ldz)) return GEMM_ERR_INVALID_ARG;
+    if (!al(dY, 2) || !al(Z, 2) || !al(dZ, 2) || !al(dbias, 4)) return GEMM_ERR_MISALIGNED;
+    DeviceContext ctx;
+    const gemm_status st = device_context(&ctx);
+    if (st != GEMM_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ActBwd a;
+    a.dY = dY;
+    a.Z = Z;
+    a.dZ = dZ;
+    a.dbias = dbias;
+    a.partial = nullptr;
+    a.rows = rows;
+    a.cols = cols;
+    a.lddy = lddy;
+    a.ldz = ldz;
+    a.lddz = lddz;
+    a.act = activation;
+    a.num_sms = ctx.num_sms;
+    a.parts = act_bwd_parts(a);
+    Scratch scratch(ctx.pool, s);
+    const bool joined = dbias && a.parts > 1;
+    if (joined) {
+        a.partial = static_cast<float*>(scratch.take(a.parts * cols * 4));
+        if (!a.partial) return GEMM_ERR_CUDA;
+    }
+    const gemm_status r = staged([&] { return launch_act_bwd(a, s); }, s);
+    if (r == GEMM_OK && joined) trace_launch(GEMM_KERNEL_STAGE);   // the sums are joined by a second kernel
+    return r;
+}
+
+gemm_status gemm_layer_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, const float* W, const float* bias,
+                            float eps, int32_t x_type, int32_t y_type, int64_t rows, int64_t d, void* H, int64_t ldh,
+                            float* mean, float* rstd, void* Y, int64_t ldy, void* stream) {
+    if (!X || !W || !Y || (R && !H)) return GEMM_ERR_INVALID_ARG;
+    if (!real_type(x_type) || !real_type(y_type)) return GEMM_ERR_INVALID_ARG;
+    if (!dim_ok(rows) || d < 1 || d > GEMM_NORM_MAX_D || !(eps >= 0.f)) return GEMM_ERR_INVALID_ARG;
+    if (!pitch_ok(ldx, d) || (R && !pitch_ok(ldr, d)) || (H && !pitch_ok(ldh, d)) || !pitch_ok(ldy, d))
+        return GEMM_ERR_INVALID_ARG;
+    // in place only over the same elements
+    if (H && ((H == X && ldh != ldx) || (H == R && ldh != ldr))) return GEMM_ERR_INVALID_ARG;
+    const int es = elem_bytes(x_type);
+    if (!al(X, es) || !al(R, es) || !al(H, es) || !al(Y, elem_bytes(y_type)) || !al(W, 4) || !al(bias, 4) || !al(mean, 4) ||
+        !al(rstd, 4))
+        return GEMM_ERR_MISALIGNED;
+    DeviceContext ctx;
+    const gemm_status st = device_context(&ctx);
+    if (st != GEMM_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    LayerNormFwd a;
+    a.X = X;
+    a.R = R;
+    a.W = W;
+    a.bias = bias;
+    a.eps = eps;
+    a.x_type = x_type;
+    a.y_type = y_type;
+    a.rows = rows;
+    a.d = d;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.ldh = ldh;
+    a.ldy = ldy;
+    a.H = H;
+    a.Y = Y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.num_sms = ctx.num_sms;
+    return staged([&] { return launch_layer_norm_fwd(a, s); }, s);
+}
+
+gemm_status gemm_layer_norm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh, const float* W,
+                                     const float* mean, const float* rstd, const void* dR, int64_t lddr,
+                                     int32_t x_type, int32_t y_type, int64_t rows, int64_t d, void* dX, int64_t lddx,
+                                     float* dW, float* dbias, void* stream) {
+    if (!dY || !H || !W || !mean || !rstd || !dX) return GEMM_ERR_INVALID_ARG;
+    if (!real_type(x_type) || !real_type(y_type)) return GEMM_ERR_INVALID_ARG;
+    if (!dim_ok(rows) || d < 1 || d > GEMM_NORM_MAX_D) return GEMM_ERR_INVALID_ARG;
+    if (!pitch_ok(lddy, d) || !pitch_ok(ldh, d) || (dR && !pitch_ok(lddr, d)) || !pitch_ok(lddx, d))
+        return GEMM_ERR_INVALID_ARG;
+    if ((dX == dR && lddx != lddr) || (dX == dY && (lddx != lddy || x_type != y_type))) return GEMM_ERR_INVALID_ARG;
+    const int es = elem_bytes(x_type);
+    if (!al(dY, elem_bytes(y_type)) || !al(H, es) || !al(dR, es) || !al(dX, es) || !al(W, 4) || !al(mean, 4) ||
+        !al(rstd, 4) || !al(dW, 4) || !al(dbias, 4))
+        return GEMM_ERR_MISALIGNED;
+    DeviceContext ctx;
+    const gemm_status st = device_context(&ctx);
+    if (st != GEMM_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    LayerNormBwd a;
+    a.dY = dY;
+    a.H = H;
+    a.dR = dR;
+    a.W = W;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.x_type = x_type;
+    a.y_type = y_type;
+    a.rows = rows;
+    a.d = d;
+    a.lddy = lddy;
+    a.ldh = ldh;
+    a.lddr = lddr;
+    a.lddx = lddx;
+    a.dX = dX;
+    a.dW = dW;
+    a.dbias = dbias;
+    a.partial = nullptr;
+    a.num_sms = ctx.num_sms;
+    a.err = ctx.err_word;
+    a.parts = layer_norm_bwd_parts(a);
+    Scratch scratch(ctx.pool, s);
+    if ((dW || dbias) && a.parts > 1) {
+        a.partial = static_cast<float*>(scratch.take(2 * static_cast<int64_t>(a.parts) * d * 4));
+        if (!a.partial) return GEMM_ERR_CUDA;
+    }
+    int launches = 0;
+    const gemm_status r = staged([&] { return launch_layer_norm_bwd(a, s, &launches); }, s);
+    for (int i = 1; r == GEMM_OK && i < launches; ++i) trace_launch(GEMM_KERNEL_STAGE);
+    return r;
+}
+
+gemm_status gemm_balance(const void* X, int64_t ldx, int32_t x_type, int64_t rows, int32_t experts,
+                         const int32_t* index, int32_t top_k, float coef, int32_t* counts, int32_t* offsets,
+                         int32_t* used, float* lse, float* probs, float* loss, void* stream) {
+    if (!X || !index || !counts || !used || !lse || !probs || !loss || !real_type(x_type)) return GEMM_ERR_INVALID_ARG;
+    if (!dim_ok(rows) || experts < 1 || experts > GEMM_BALANCE_MAX_EXPERTS || top_k < 1 || rows * top_k > INT32_MAX)
+        return GEMM_ERR_INVALID_ARG;
+    if (!pitch_ok(ldx, experts)) return GEMM_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(index), static_cast<const void*>(counts), static_cast<const void*>(offsets),
+                          static_cast<const void*>(used), static_cast<const void*>(lse), static_cast<const void*>(probs),
+                          static_cast<const void*>(loss)})
+        if (!al(p, 4)) return GEMM_ERR_MISALIGNED;
+    if (!al(X, elem_bytes(x_type))) return GEMM_ERR_MISALIGNED;
+    DeviceContext ctx;
+    const gemm_status st = device_context(&ctx);
+    if (st != GEMM_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Balance a;
+    a.X = X;
+    a.x_type = x_type;
+    a.rows = rows;
+    a.ldx = ldx;
+    a.experts = experts;
+    a.top_k = top_k;
+    a.index = index;
+    a.coef = coef;
+    a.counts = counts;
+    a.offsets = offsets;
+    a.used = used;
+    a.lse = lse;
+    a.probs = probs;
+    a.loss = loss;
+    a.num_sms = ctx.num_sms;
+    a.parts = balance_parts(a);
+    Scratch scratch(ctx.pool, s);
+    const int64_t sums = static_cast<int64_t>(a.parts) * experts;
+    a.partial_p = static_cast<float*>(scratch.take(4 * (2 * sums + a.parts)));
+    if (!a.partial_p) return GEMM_ERR_CUDA;
+    a.partial_c = reinterpret_cast<int32_t*>(a.partial_p + sums);
+    int launches = 0;
+    const gemm_status r = staged([&] { return launch_balance(a, s, &launches); }, s);
+    for (int i = 1; r == GEMM_OK && i < launches; ++i) trace_launch(GEMM_KERNEL_STAGE);
+    return r;
+}
+
+gemm_status gemm_balance_backward(const void* X, int64_t ldx, int32_t x_type, int64_t rows, int32_t experts,
+                                  const float* lse, const int32_t* counts, const int32_t* used, float coef,
+                                  const float* dloss, const void* dR, int64_t lddr, void* dX, int64_t lddx,
+                                  void* stream) {
+    if (!X || !lse || !counts || !used || !dloss || !dX || !real_type(x_type)) return GEMM_ERR_INVALID_ARG;
+    if (!dim_ok(rows) || experts < 1 || experts > GEMM_BALANCE_MAX_EXPERTS) return GEMM_ERR_INVALID_ARG;
+    if (!pitch_ok(ldx, experts) || (dR && !pitch_ok(lddr, experts)) || !pitch_ok(lddx, experts)) return GEMM_ERR_INVALID_ARG;
+    if (dX == dR && lddx != lddr) return GEMM_ERR_INVALID_ARG;
+    const int es = elem_bytes(x_type);
+    if (!al(X, es) || !al(dR, es) || !al(dX, es) || !al(lse, 4) || !al(counts, 4) || !al(used, 4) || !al(dloss, 4))
+        return GEMM_ERR_MISALIGNED;
+    DeviceContext ctx;
+    const gemm_status st = device_context(&ctx);
+    if (st != GEMM_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    BalanceBwd a;
+    a.X = X;
+    a.dR = dR;
+    a.dX = dX;
+    a.x_type = x_type;
+    a.rows = rows;
+    a.ldx = ldx;
+    a.lddr = lddr;
+    a.lddx = lddx;
+    a.experts = experts;
+    a.lse = lse;
+    a.counts = counts;
+    a.used = used;
+    a.coef = coef;
+    a.dloss = dloss;
+    a.num_sms = ctx.num_sms;
+    return staged([&] { return launch_balance_bwd(a, s); }, s);
+}
+
+}  // extern "C"

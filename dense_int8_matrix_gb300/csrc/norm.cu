@@ -12,6 +12,7 @@
 // 145 us, 16385 x 1001 37), backward 33 to 58 % (138 and 54 us).
 #include "f8.cuh"
 #include "internal.h"
+#include "layer.h"
 #include "ptx.cuh"
 
 namespace gemm {
@@ -579,10 +580,12 @@ int norm_bwd_grid(const NormBwd& a) {
 cudaError_t launch_norm_bwd(const NormBwd& a, cudaStream_t stream) {
     cudaError_t e = bwd_ring(a) ? ring_type(a, stream)
                     : a.x_type == GEMM_DTYPE_BF16 ? rows_type<__nv_bfloat16>(a, stream) : rows_type<float>(a, stream);
-    if (e == cudaSuccess && a.dW && a.grid > 1)
-        e = launch_chained(dw_reduce_kernel, dim3(static_cast<unsigned>((a.d + 7) / 8)), 256, 0, stream, a.partial, a.grid,
-                           a.d, a.dW);
+    if (e == cudaSuccess && a.dW && a.grid > 1) e = launch_column_sums(a.partial, a.grid, a.d, a.dW, stream);
     return e;
+}
+
+cudaError_t launch_column_sums(const float* partial, int parts, int64_t d, float* out, cudaStream_t stream) {
+    return launch_chained(dw_reduce_kernel, dim3(static_cast<unsigned>((d + 7) / 8)), 256, 0, stream, partial, parts, d, out);
 }
 
 }  // namespace gemm

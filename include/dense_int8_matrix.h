@@ -442,6 +442,186 @@ GEMM_API gemm_status gemm_norm_backward(const void *dY, int64_t lddy, const void
                                         const float *rstd, const void *dR, int64_t lddr, int32_t x_type, int64_t rows,
                                         int64_t d, void *dX, int64_t lddx, float *dW, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a bfloat16 layer around the GEMM: the product with bias,
+ * activation and residual in its epilogue and the products of its backward
+ * pass, the activation's gradient with the bias's, the layer norm and its
+ * gradient, and the balance loss of a router, whose offsets the grouped
+ * products take.
+ *
+ * They take device pointers, enqueue on `stream` and return, like
+ * gemm_*_run; scratch comes from the library's pool.  The trace counts
+ * products as GEMM_KERNEL_TC or GEMM_KERNEL_SKINNY, everything else (copies
+ * of unaligned operands among it) as GEMM_KERNEL_STAGE.
+ * ------------------------------------------------------------------------ */
+
+/* How the operands of a product lie in memory.  Rows are contiguous. */
+enum {
+    GEMM_FORM_NT = 0, /* A m x k, B stored n x k (the weights of a forward product) */
+    GEMM_FORM_NN = 1, /* A m x k, B stored k x n (input gradient: A = dZ, B the same weights) */
+    GEMM_FORM_TN = 2  /* A stored k x m, B stored k x n (weight gradient: A = dZ, B = X, k the rows) */
+};
+
+/* Activations, v in fp32, s(v) = 1 / (1 + exp(-v)), Phi the normal distribution:
+ *   RELU v > 0 ? v : 0;  GELU v * Phi(v);  SILU v * s(v);
+ *   GELU_TANH v * s(2 sqrt(2 / pi) (v + 0.044715 v^3)), GELU with the tanh form of Phi.
+ * NaN stays NaN.  GELU, GELU_TANH and SILU of -infinity are NaN (0 times it),
+ * and so may be their derivatives at an infinity. */
+enum {
+    GEMM_ACT_NONE = 0,
+    GEMM_ACT_RELU = 1,
+    GEMM_ACT_GELU = 2,
+    GEMM_ACT_GELU_TANH = 3,
+    GEMM_ACT_SILU = 4,
+    GEMM_ACT_GRADIENT = 16 /* added to one of them: multiply by its derivative at Z */
+};
+
+#define GEMM_PLAN_LINEAR_VERSION 1
+#define GEMM_BALANCE_MAX_EXPERTS 1024
+
+/* The configuration of a bfloat16 product.  Plain data, filled by gemm_bf16_linear_plan*. */
+typedef struct gemm_plan_linear {
+    int32_t version;  /* GEMM_PLAN_LINEAR_VERSION */
+    int32_t path;     /* GEMM_PATH_TENSOR: two-SM tiles; GEMM_PATH_SKINNY: small tiles, split along K */
+    int32_t num_sms;  /* SM count the plan was made for */
+    int32_t form;     /* GEMM_FORM_* */
+    int64_t m, k, n;
+    int32_t bm, bn;   /* rows and columns of D per tile */
+    int32_t split_k;  /* skinny path: CTAs that share a tile along K and join their sums */
+    int32_t reserved32;
+    int64_t reserved[4];
+} gemm_plan_linear;
+
+/*
+ * Plan D (m x n) = A (m x k) x B (k x n).  Host-only apart from one cached
+ * query of the device's SM count; the _for_sms form makes no CUDA call.
+ * Errors: GEMM_ERR_INVALID_ARG (NULL out; m, k or n outside [1, 2^30];
+ * unknown form; num_sms < 1), GEMM_ERR_CUDA (no device).
+ */
+GEMM_API gemm_status gemm_bf16_linear_plan(int32_t form, int64_t m, int64_t k, int64_t n, gemm_plan_linear *out);
+GEMM_API gemm_status gemm_bf16_linear_plan_for_sms(int32_t form, int64_t m, int64_t k, int64_t n, int32_t num_sms,
+                                                   gemm_plan_linear *out);
+
+/*
+ *   v[i][j] = sum_kk A[i][kk] * B[kk][j] + bias[j]      (fp32 accumulation)
+ *   D[i][j] = act(v) + residual[i][j]                   activation = GEMM_ACT_*
+ *   D[i][j] = v * act'(Z[i][j]) + residual[i][j]        activation = GEMM_ACT_* | GEMM_ACT_GRADIENT
+ * rounded once to out_type (GEMM_OUT_BF16 or GEMM_OUT_F32).  bias (n floats)
+ * and residual (out_type, pitch ldr) may be NULL; residual may be D itself
+ * (with its pitch): D += the product.  Z (bfloat16, pitch ldz): without
+ * GEMM_ACT_GRADIENT, if not NULL, it gets v rounded to bfloat16, for the
+ * backward pass (act itself is taken of the fp32 v); with it Z is read, and
+ * may be NULL only for GEMM_ACT_NONE.  With RELU's gradient v is selected,
+ * not multiplied: 0 where Z <= 0, NaN where Z is NaN.
+ * A, B: bfloat16 with row pitches lda, ldb in elements, in the plan's form.
+ * Operands whose address is not 16-byte aligned or whose pitch is not a
+ * multiple of 8 are first copied into scratch with such a pitch.  D, residual
+ * and Z need their element's alignment only; no output may overlap an operand
+ * or another output.
+ * A plan may be edited to force the path, the tile (GEMM_PATH_TENSOR: bm 256,
+ * bn 128 or 256, split_k 1; GEMM_PATH_SKINNY: bm 16, 32, 64 or 128 rows, for
+ * GEMM_FORM_TN 64 or 128, bn 128) or split_k (1, 2, 4 or 8); sums then join
+ * in another order.  One plan always gives the same bits.
+ * Errors: GEMM_ERR_INVALID_ARG (null pointer, bad plan, pitch too small or
+ * above 2^31, unknown type or activation, residual == D with another pitch),
+ * GEMM_ERR_MISALIGNED (A, B, D, residual, Z or bias not element aligned),
+ * GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
+ */
+GEMM_API gemm_status gemm_bf16_linear_run(const gemm_plan_linear *plan, const uint16_t *A, int64_t lda,
+                                          const uint16_t *B, int64_t ldb, const float *bias, int32_t activation,
+                                          uint16_t *Z, int64_t ldz, const void *residual, int64_t ldr,
+                                          int32_t out_type, void *D, int64_t ldd, void *stream);
+
+/*
+ * The gradient of an activation and of the bias before it, rows x cols:
+ *   dZ = dY * act'(Z), rounded to bfloat16;  dbias[j] = sum_i dY[i][j] * act'(Z[i][j]) (fp32, before that rounding)
+ * dY, Z, dZ: bfloat16 with pitches in elements.  Z may be NULL for
+ * GEMM_ACT_NONE.  dZ or dbias may be NULL, not both; dZ may be dY or Z itself
+ * (with its pitch).  Sums are taken in a fixed order.
+ * Errors: GEMM_ERR_INVALID_ARG (null pointer, size outside [1, 2^30], pitch,
+ * unknown activation, dZ in place with another pitch), GEMM_ERR_MISALIGNED
+ * (not element aligned), GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
+ */
+GEMM_API gemm_status gemm_activation_backward(const uint16_t *dY, int64_t lddy, const uint16_t *Z, int64_t ldz,
+                                              int32_t activation, int64_t rows, int64_t cols, uint16_t *dZ,
+                                              int64_t lddz, float *dbias, void *stream);
+
+/*
+ * Residual addition and layer norm in one pass over rows x d elements
+ * (x_type, y_type: GEMM_DTYPE_BF16 or GEMM_DTYPE_F32):
+ *   h    = X + R, rounded to x_type        (R == NULL: h = X)
+ *   mean = mean_j(h_j),  rstd = 1 / sqrt(mean_j((h_j - mean)^2) + eps)   (fp32)
+ *   Y_j  = (h_j - mean) * rstd * W[j] + bias[j], rounded to y_type
+ * W: d floats; bias: d floats or NULL.  H (x_type; may be NULL if R is NULL)
+ * gets h and may be X or R itself (with that one's pitch).  mean and rstd
+ * (rows floats each, may be NULL) are kept for the backward pass.  Pitches in
+ * elements; d <= GEMM_NORM_MAX_D; eps >= 0.  A row that holds an infinity or
+ * a NaN gives NaN; so does a constant row with eps = 0.
+ * Errors: as gemm_norm_f8.
+ */
+GEMM_API gemm_status gemm_layer_norm(const void *X, int64_t ldx, const void *R, int64_t ldr, const float *W,
+                                     const float *bias, float eps, int32_t x_type, int32_t y_type, int64_t rows,
+                                     int64_t d, void *H, int64_t ldh, float *mean, float *rstd, void *Y, int64_t ldy,
+                                     void *stream);
+
+/*
+ * Its gradient, from dY (y_type), h (x_type), mean and rstd as the forward
+ * call wrote them:
+ *   xhat = (h - mean) * rstd,  g = dY * W
+ *   dX = dR + rstd * (g - mean_j(g) - xhat * mean_j(g * xhat))    (dR may be NULL: 0)
+ *   dW_j = sum_i dY_ij * xhat_ij,  dbias_j = sum_i dY_ij          (fp32, overwritten)
+ * dR (x_type) is the gradient that reaches h as the residual; dX (x_type) is
+ * the gradient of X and of R, and may be dR itself, or dY if the types are
+ * the same (with that one's pitch).  dW and dbias may be NULL.  Sums are
+ * taken in a fixed order: the same call gives the same bits.
+ * Errors: as gemm_norm_f8.
+ */
+GEMM_API gemm_status gemm_layer_norm_backward(const void *dY, int64_t lddy, const void *H, int64_t ldh, const float *W,
+                                              const float *mean, const float *rstd, const void *dR, int64_t lddr,
+                                              int32_t x_type, int32_t y_type, int64_t rows, int64_t d, void *dX,
+                                              int64_t lddx, float *dW, float *dbias, void *stream);
+
+/*
+ * Balance loss of a router and the experts' counts.  X: logits, rows x
+ * experts (GEMM_DTYPE_BF16 or GEMM_DTYPE_F32, pitch ldx); index: the experts
+ * chosen for each row, rows x top_k int32 without gaps.  An index outside
+ * [0, experts) is a slot that is not taken (a token that a full expert has
+ * turned away); a row without a taken slot is padding and takes no part.
+ *   counts[e]  = number of slots with index e
+ *   offsets[e] = counts[0] + .. + counts[e-1], experts + 1 values: the row
+ *                offsets that gemm_f8_grouped_run takes (may be NULL)
+ *   used       = number of rows that take part, T
+ *   lse[i]     = log(sum_e exp(X[i][e])); +infinity for padding
+ *   probs[e]   = (1 / T) sum over the used rows of p[i][e], p = softmax of the row
+ *   loss       = coef * experts * sum_e (counts[e] / sum counts) * probs[e]
+ * counts, used: int32; lse (rows), probs (experts), loss (1): fp32.  Without
+ * a used row, probs and loss are 0.  Logits of -infinity have p = 0; a used
+ * row of nothing else has p = 0 throughout and lse = -infinity.  A NaN or
+ * +infinity in a used row makes its lse and the loss NaN.
+ * Sums are taken in a fixed order.
+ * Errors: GEMM_ERR_INVALID_ARG (null pointer; rows outside [1, 2^30];
+ * experts outside [1, GEMM_BALANCE_MAX_EXPERTS]; top_k below 1; rows * top_k
+ * above 2^31 - 1; pitch; unknown type), GEMM_ERR_MISALIGNED (not element
+ * aligned), GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
+ */
+GEMM_API gemm_status gemm_balance(const void *X, int64_t ldx, int32_t x_type, int64_t rows, int32_t experts,
+                                  const int32_t *index, int32_t top_k, float coef, int32_t *counts, int32_t *offsets,
+                                  int32_t *used, float *lse, float *probs, float *loss, void *stream);
+
+/*
+ * Its gradient: with f_e = counts[e] / sum counts (a constant) and p as above
+ *   dX[i][e] = dR[i][e] + dloss * coef * experts / T * p[i][e] * (f_e - sum_j f_j p[i][j])
+ * lse (which rows are padding; p is formed anew), counts and used as
+ * gemm_balance wrote them; dloss: one float on the device.  dR (x_type, may be NULL: 0) is the gradient that reaches the
+ * logits by other ways; dX (x_type) may be dR itself (with its pitch).  Rows
+ * that are padding, or whose lse is -infinity, get dR (or 0), whatever their
+ * logits are.  Errors: as gemm_balance.
+ */
+GEMM_API gemm_status gemm_balance_backward(const void *X, int64_t ldx, int32_t x_type, int64_t rows, int32_t experts,
+                                           const float *lse, const int32_t *counts, const int32_t *used, float coef,
+                                           const float *dloss, const void *dR, int64_t lddr, void *dX, int64_t lddx,
+                                           void *stream);
+
 /*
  * Waits for `stream`, then reads and clears the current device's error word,
  * which the kernels of every run entry point (gemm_i8_run_noalloc included)
