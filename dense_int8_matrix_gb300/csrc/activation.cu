@@ -24,7 +24,7 @@ constexpr int kRowsAtOnce = 4;   // rows in flight per thread
 
 // `lanes` neighbouring threads (a power of two, 32 for unaligned rows, whose
 // stores go by whole warps) hold 8 * lanes columns of a row.
-template <bool VEC>
+template <int ACT, bool VEC>
 __global__ void __launch_bounds__(kThreads) act_bwd_kernel(const ActBwd p, int lanes) {
     __shared__ float red[kThreads * 8];
     pdl_launch_dependents();
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(const ActBwd p, int l
             float g[8], s[8];
             dy[k].get(g);
             z[k].get(s);
-            activate_all<8>(p.act, true, g, [&](int i) { return s[i]; });
+            activate_each<ACT | GEMM_ACT_GRADIENT, 8>(g, [&](int i) { return s[i]; });
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[i] += g[i];
             if (p.dZ && r < hi) {   // (lanes == 32 without VEC: the whole warp)
@@ -116,8 +116,18 @@ int act_bwd_parts(const ActBwd& a) {
 cudaError_t launch_act_bwd(const ActBwd& a, cudaStream_t stream) {
     const int lanes = act_lanes(a);
     const dim3 grid(static_cast<unsigned>((a.cols + 8 * lanes - 1) / (8 * lanes)), static_cast<unsigned>(a.parts));
-    cudaError_t e = act_vec(a) ? launch_chained(act_bwd_kernel<true>, grid, kThreads, 0, stream, a, lanes)
-                               : launch_chained(act_bwd_kernel<false>, grid, kThreads, 0, stream, a, lanes);
+    auto go = [&](auto kern) { return launch_chained(kern, grid, kThreads, 0, stream, a, lanes); };
+    const bool vec = act_vec(a);
+    cudaError_t e;
+    switch (a.act) {
+        case GEMM_ACT_RELU: e = go(vec ? act_bwd_kernel<GEMM_ACT_RELU, true> : act_bwd_kernel<GEMM_ACT_RELU, false>); break;
+        case GEMM_ACT_GELU: e = go(vec ? act_bwd_kernel<GEMM_ACT_GELU, true> : act_bwd_kernel<GEMM_ACT_GELU, false>); break;
+        case GEMM_ACT_GELU_TANH:
+            e = go(vec ? act_bwd_kernel<GEMM_ACT_GELU_TANH, true> : act_bwd_kernel<GEMM_ACT_GELU_TANH, false>);
+            break;
+        case GEMM_ACT_SILU: e = go(vec ? act_bwd_kernel<GEMM_ACT_SILU, true> : act_bwd_kernel<GEMM_ACT_SILU, false>); break;
+        default: e = go(vec ? act_bwd_kernel<GEMM_ACT_NONE, true> : act_bwd_kernel<GEMM_ACT_NONE, false>); break;
+    }
     if (e == cudaSuccess && a.dbias && a.parts > 1) e = launch_column_sums(a.partial, a.parts, a.cols, a.dbias, stream);
     return e;
 }

@@ -15,14 +15,35 @@ __device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + __ex
 
 constexpr float kGeluTanhTwice = 1.5957691216f;    // 2 sqrt(2 / pi)
 constexpr float kGeluTanhCube = 0.044715f;
-constexpr float kRootHalf = 0.70710678119f;
 constexpr float kNormalPeak = 0.39894228040f;      // 1 / sqrt(2 pi)
+
+// Phi(-|v|), the normal distribution's tail, and exp(-v^2 / 2), which its
+// derivative needs too.  With x = |v| / sqrt(2), erfc(x) exp(x^2) is a smooth
+// function of t = 1 / (1 + 0.425 x): t times a polynomial of degree 7, fitted
+// here over x <= 12 for the least relative error, 2.5e-7, so that the tail keeps
+// its digits (1 + erf would cancel there).  erfcf costs six times as much.
+__device__ __forceinline__ float normal_tail(float v, float& e) {
+    const float t = rcp_approx(fmaf(fabsf(v), 0.30052038f, 1.f));   // 0.425 / sqrt(2)
+    e = __expf(-0.5f * v * v);
+    float q = 0.0688852072f;
+    q = fmaf(q, t, -0.3024713099f);
+    q = fmaf(q, t, 0.3894520700f);
+    q = fmaf(q, t, -0.0868048817f);
+    q = fmaf(q, t, 0.2465598583f);
+    q = fmaf(q, t, 0.2032268792f);
+    q = fmaf(q, t, 0.2414486110f);
+    q = fmaf(q, t, 0.2397032976f);
+    return 0.5f * (q * t) * e;
+}
 
 template <int ACT>
 __device__ __forceinline__ float activate(float v) {
     if constexpr (ACT == GEMM_ACT_RELU) return v > 0.f || v != v ? v : 0.f;
-    // erfc of the negative argument: 1 + erf would cancel in the left tail
-    if constexpr (ACT == GEMM_ACT_GELU) return v * (0.5f * erfcf(-v * kRootHalf));
+    if constexpr (ACT == GEMM_ACT_GELU) {
+        float e;
+        const float tail = normal_tail(v, e);
+        return v * (v > 0.f ? 1.f - tail : tail);
+    }
     if constexpr (ACT == GEMM_ACT_GELU_TANH) return v * sigmoid(kGeluTanhTwice * (v + kGeluTanhCube * v * v * v));
     if constexpr (ACT == GEMM_ACT_SILU) return v * sigmoid(v);
     return v;
@@ -32,8 +53,11 @@ __device__ __forceinline__ float activate(float v) {
 template <int ACT>
 __device__ __forceinline__ float activate_gradient(float g, float z) {
     if constexpr (ACT == GEMM_ACT_RELU) return z > 0.f ? g : z != z ? z : 0.f;
-    if constexpr (ACT == GEMM_ACT_GELU)
-        return g * fmaf(z * kNormalPeak, __expf(-0.5f * z * z), 0.5f * erfcf(-z * kRootHalf));
+    if constexpr (ACT == GEMM_ACT_GELU) {
+        float e;
+        const float tail = normal_tail(z, e);
+        return g * fmaf(z * kNormalPeak, e, z > 0.f ? 1.f - tail : tail);
+    }
     if constexpr (ACT == GEMM_ACT_GELU_TANH) {
         // past |z| = 20 the slope is 0 or 1 to the last bit; there z^3 could overflow against s (1 - s) = 0
         const float x = fminf(fmaxf(z, -20.f), 20.f);
@@ -48,26 +72,16 @@ __device__ __forceinline__ float activate_gradient(float g, float z) {
     return g;
 }
 
-// v[i] = act(v[i]), or v[i] times the derivative at z(i): one uniform branch
-// for the N values.
-template <int N, typename Z>
-__device__ __forceinline__ void activate_all(int act, bool grad, float (&v)[N], Z z) {
-#define GEMM_ACT_CASE(ACT)                                        \
-    case ACT:                                                     \
-        if (grad) {                                               \
-            _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = activate_gradient<ACT>(v[i], z(i)); \
-        } else {                                                  \
-            _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = activate<ACT>(v[i]);                \
-        }                                                         \
-        break;
-    switch (act) {
-        GEMM_ACT_CASE(GEMM_ACT_RELU)
-        GEMM_ACT_CASE(GEMM_ACT_GELU)
-        GEMM_ACT_CASE(GEMM_ACT_GELU_TANH)
-        GEMM_ACT_CASE(GEMM_ACT_SILU)
-        default: break;
+// v[i] = act(v[i]), or with GEMM_ACT_GRADIENT v[i] times the derivative at z(i).
+template <int ACT, int N, typename Z>
+__device__ __forceinline__ void activate_each(float (&v)[N], Z z) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if constexpr ((ACT & GEMM_ACT_GRADIENT) != 0)
+            v[i] = activate_gradient<ACT & ~GEMM_ACT_GRADIENT>(v[i], z(i));
+        else
+            v[i] = activate<ACT>(v[i]);
     }
-#undef GEMM_ACT_CASE
 }
 
 }  // namespace gemm

@@ -6,8 +6,11 @@
 // A cluster of two CTAs computes a 256 x 256 tile (or a half, 256 x 128); each
 // CTA loads its 128 rows of A and its half of the columns of B per K step with
 // TMA, and tcgen05.mma (M = 256, N = 256, K = 16, four per step) adds them up in
-// TMEM over all of K, in 32 bits.  The two accumulators of 256 columns alternate,
-// so one tile's epilogue runs beside the next tile's MMAs.
+// TMEM, in 32 bits.  The MMA truncates what it adds to an accumulator, an error
+// that grows with K and always points to zero, so that a chunk of K at a time
+// is added up there and the chunks in registers, rounded to nearest (chunk_of).  The two
+// accumulators of 256 columns alternate: one is read while the next chunk, or
+// the next tile, is multiplied.
 //
 // An operand whose rows lie along K (GEMM_FORM_NT) comes in boxes of 64 K
 // elements by 128 rows.  The backward pass reads the same tensors along their
@@ -83,6 +86,25 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const void* map, bool
     }
 }
 
+// Adds 32 columns of a chunk to the running sums.
+__device__ __forceinline__ void add_block(uint64_t* acc, const uint32_t (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = add2(acc[j], pair_of(v[2 * j], v[2 * j + 1]));
+}
+// 32 columns of running sums into the warp's staging buffer.
+__device__ __forceinline__ void stage_block(uint32_t stg, int lane, const uint64_t* acc) {
+    uint32_t r[32];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float a, b;
+        unpair(acc[j], a, b);
+        r[2 * j] = __float_as_uint(a);
+        r[2 * j + 1] = __float_as_uint(b);
+    }
+    stage_rows32(stg, lane, r);
+}
+
+template <int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_tc2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const LinearParams p, const uint32_t idesc, const uint32_t idesc_half) {
@@ -127,112 +149,145 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const Units list = list_units(p, npairs);
 
-    if (warp == 0) {
-        // ---------------------------------------------------- operand loads --
-        pdl_wait();
-        const uint64_t pol = policy_evict_normal();
-        const uint32_t full_leader = peer_address(full0, 0);
-        Turn<kStages> at;
-        uint32_t issued = 0;
-        bool ok = true;
-        for (int u = pair; ok && u < list.count; u += npairs) {
-            const Unit w = unit_at(u, list, p);
-            const int steps = steps_of(w, p);
-            const int ya = w.row + static_cast<int>(rank) * kHalfRows;
-            // (a half's boxes bring 64 columns more than are multiplied)
-            const int yb = w.col + static_cast<int>(rank) * (w.half ? kTileN / 4 : kTileN / 2);
-            for (int kb = 0; kb < steps; ++kb, ++issued) {
-                // the stage is free once the step that was in it has been multiplied
-                if (!wait_warp(done0 + 8u * at.i, at.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutProducer)) {
-                    ok = false;
-                    break;
+    // the epilogue's running sums need more registers than an even share: of
+    // 384 threads with 168, 128 keep 40 each and 256 take 232
+    if (warp < 4) {
+        fewer_registers<40>();
+        if (warp == 0) {
+            // ------------------------------------------------ operand loads --
+            pdl_wait();
+            const uint64_t pol = policy_evict_normal();
+            const uint32_t full_leader = peer_address(full0, 0);
+            Turn<kStages> at;
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int u = pair; ok && u < list.count; u += npairs) {
+                const Unit w = unit_at(u, list, p);
+                const int steps = steps_of(w, p);
+                const int ya = w.row + static_cast<int>(rank) * kHalfRows;
+                // (a half's boxes bring 64 columns more than are multiplied)
+                const int yb = w.col + static_cast<int>(rank) * (w.half ? kTileN / 4 : kTileN / 2);
+                for (int kb = 0; kb < steps; ++kb, ++issued) {
+                    // the stage is free once the step that was in it has been multiplied
+                    if (!wait_warp(done0 + 8u * at.i, at.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutProducer)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        const uint32_t fb = full_leader + 8u * at.i;
+                        if (leader) mbar_arrive_expect_tx(full0 + 8u * at.i, 2 * kStage);
+                        load_operand(sA + at.i * kHalfBytes, &tmA, p.mn_a, ya, kb, fb, pol);
+                        load_operand(sB + at.i * kHalfBytes, &tmB, p.mn_b, yb, kb, fb, pol);
+                    }
+                    __syncwarp();
+                    at.next();
                 }
-                if (elect_one()) {
-                    const uint32_t fb = full_leader + 8u * at.i;
-                    if (leader) mbar_arrive_expect_tx(full0 + 8u * at.i, 2 * kStage);
-                    load_operand(sA + at.i * kHalfBytes, &tmA, p.mn_a, ya, kb, fb, pol);
-                    load_operand(sB + at.i * kHalfBytes, &tmB, p.mn_b, yb, kb, fb, pol);
-                }
-                __syncwarp();
-                at.next();
             }
-        }
-        // after a time-out the copies still in flight land before the pair ends
-        if (!ok && leader)
-            for (uint32_t j = issued > kStages ? issued - kStages : 0u; j < issued; ++j)
-                wait_bounded(full0 + 8u * (j % kStages), (j / kStages) & 1u, nullptr, p.err, kDevErrTimeoutTeardown);
-    } else if (warp == 1 && leader) {
-        // -------------------------------------------------------------- MMAs --
-        Turn<kStages> st;
-        Turn<2> buf;
-        bool ok = true;
-        const uint32_t step_a = desc_step(p.mn_a), step_b = desc_step(p.mn_b);
-        for (int u = pair; ok && u < list.count; u += npairs) {
-            const Unit w = unit_at(u, list, p);
-            const int steps = steps_of(w, p);
-            if (steps == 0) continue;
-            const uint32_t desc = w.half ? idesc_half : idesc;
-            ok = wait_warp(acce0 + 8u * buf.i, buf.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutMma);
-            for (int kb = 0; ok && kb < steps; ++kb) {
-                if (!wait_warp(full0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutMma)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t ad = smem_desc_linear(sA + st.i * kHalfBytes, p.mn_a);
-                const uint64_t bd = smem_desc_linear(sB + st.i * kHalfBytes, p.mn_b);
-                if (elect_one()) {
+            // after a time-out the copies still in flight land before the pair ends
+            if (!ok && leader)
+                for (uint32_t j = issued > kStages ? issued - kStages : 0u; j < issued; ++j)
+                    wait_bounded(full0 + 8u * (j % kStages), (j / kStages) & 1u, nullptr, p.err, kDevErrTimeoutTeardown);
+        } else if (warp == 1 && leader) {
+            // ---------------------------------------------------------- MMAs --
+            Turn<kStages> st;
+            Turn<2> buf;
+            bool ok = true;
+            const uint32_t step_a = desc_step(p.mn_a), step_b = desc_step(p.mn_b);
+            for (int u = pair; ok && u < list.count; u += npairs) {
+                const Unit w = unit_at(u, list, p);
+                const int steps = steps_of(w, p);
+                const uint32_t desc = w.half ? idesc_half : idesc;
+                int left = 0;   // steps of the running chunk that remain
+                for (int kb = 0; kb < steps; ++kb) {
+                    const bool fresh = left == 0;
+                    if (fresh) {
+                        left = min(p.chunk, steps - kb);
+                        ok = wait_warp(acce0 + 8u * buf.i, buf.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutMma);
+                    }
+                    ok = ok && wait_warp(full0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutMma);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t ad = smem_desc_linear(sA + st.i * kHalfBytes, p.mn_a);
+                    const uint64_t bd = smem_desc_linear(sB + st.i * kHalfBytes, p.mn_b);
+                    --left;
+                    if (elect_one()) {
 #pragma unroll
-                    for (uint32_t kk = 0; kk < kLinBK / kLinMmaK; ++kk)
-                        mma_bf16<2>(tmem + buf.i * kTileN, ad + kk * step_a, bd + kk * step_b, desc, kb > 0 || kk > 0 ? 1u : 0u);
-                    commit_pair(done0 + 8u * st.i);
-                    if (kb + 1 == steps) commit_pair(accf0 + 8u * buf.i);
+                        for (uint32_t kk = 0; kk < kLinBK / kLinMmaK; ++kk)
+                            mma_bf16<2>(tmem + buf.i * kTileN, ad + kk * step_a, bd + kk * step_b, desc, fresh && kk == 0 ? 0u : 1u);
+                        commit_pair(done0 + 8u * st.i);
+                        if (left == 0) commit_pair(accf0 + 8u * buf.i);
+                    }
+                    __syncwarp();
+                    st.next();
+                    if (left == 0) buf.next();
                 }
-                __syncwarp();
-                st.next();
             }
-            buf.next();
+            if (elect_one()) commit_pair(last);
+            __syncwarp();
+            wait_bounded(last, 0u, nullptr, p.err, kDevErrTimeoutTeardown);
         }
-        if (elect_one()) commit_pair(last);
-        __syncwarp();
-        wait_bounded(last, 0u, nullptr, p.err, kDevErrTimeoutTeardown);
-    } else if (warp >= 4) {
+    } else {
         // ---------------------------------------------------------- epilogue --
+        more_registers<232>();
         pdl_wait();
         const int e = warp - 4, q = warp & 3, h = e >> 2;
         const uint32_t stg = sEpi + e * kStageRowsBytes;
         const uint32_t acce = peer_address(acce0, 0);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
         Turn<2> buf;
-        for (int u = pair; u < list.count; u += npairs) {
+        bool ok = true;
+        for (int u = pair; ok && u < list.count; u += npairs) {
             const Unit w = unit_at(u, list, p);
-            if (steps_of(w, p) == 0) continue;
-            if (!wait_warp(accf0 + 8u * buf.i, buf.ph, abort_flag, p.err, kDevErrTimeoutEpilogue)) break;
-            tc_fence_after();
+            const int steps = steps_of(w, p);
+            if (steps == 0) continue;
             const int cols = w.half ? kTileN / 4 : kTileN / 2;   // of this warp
-            const uint32_t t0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf.i * kTileN + h * cols;
             const int row0 = w.row + static_cast<int>(rank) * kHalfRows + q * 32, col0 = w.col + h * cols;
-            for (int c = 0; c < cols; c += 32) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(t0 + c, r);
-                wait_tmem(r);
-                if (c + 32 == cols) {   // all columns have been read: the accumulator is free
-                    tc_fence_before();
-                    if (lane == 0) arrive_in_cluster(acce + 8u * buf.i);
+            uint64_t acc[kTileN / 4];   // pairs of columns; the first half of them for a half
+#pragma unroll
+            for (int j = 0; j < kTileN / 4; ++j) acc[j] = 0;
+            for (int kb = 0; kb < steps; kb += p.chunk) {
+                ok = wait_warp(accf0 + 8u * buf.i, buf.ph, abort_flag, p.err, kDevErrTimeoutEpilogue);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t0 = lanes + buf.i * kTileN + h * cols, free_bar = acce + 8u * buf.i;
+                buf.next();
+                // one block of 32 columns is added while the next is on its way
+                uint32_t v[2][32];
+                tmem_ld_32x32b_x32(t0, v[0]);
+                wait_tmem(v[0]);
+                tmem_ld_32x32b_x32(t0 + 32, v[1]);
+                add_block(acc, v[0]);
+                wait_tmem(v[1]);
+                if (!w.half) {
+                    tmem_ld_32x32b_x32(t0 + 64, v[0]);
+                    add_block(acc + 16, v[1]);
+                    wait_tmem(v[0]);
+                    tmem_ld_32x32b_x32(t0 + 96, v[1]);
+                    add_block(acc + 32, v[0]);
+                    wait_tmem(v[1]);
                 }
-                if (row0 >= p.m || col0 + c >= p.n) continue;   // (the whole warp alike)
-                __syncwarp();   // the block before has been read out
-                stage_rows32(stg, lane, r);
-                __syncwarp();
-                const bool vec = p.vec && col0 + c + 32 <= p.n;
-                if (p.out_f32) {
-                    if (vec) finish_block<true>(p, stg, lane, row0, col0 + c);
-                    else finish_ragged<true>(p, stg, lane, row0, col0 + c);
-                } else {
-                    if (vec) finish_block<false>(p, stg, lane, row0, col0 + c);
-                    else finish_ragged<false>(p, stg, lane, row0, col0 + c);
-                }
+                // all columns are in registers: the accumulator is free
+                tc_fence_before();
+                if (lane == 0) arrive_in_cluster(free_bar);
+                if (w.half)
+                    add_block(acc + 16, v[1]);
+                else
+                    add_block(acc + 48, v[1]);
             }
-            buf.next();
+            if (!ok) break;
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+                if (row0 >= p.m || col0 + c >= p.n) break;   // (the whole warp alike)
+                __syncwarp();   // the block before has been read out
+                switch (c) {
+                    case 0: stage_block(stg, lane, acc); break;
+                    case 32: stage_block(stg, lane, acc + 16); break;
+                    case 64: stage_block(stg, lane, acc + 32); break;
+                    default: stage_block(stg, lane, acc + 48); break;
+                }
+                __syncwarp();
+                finish<ACT>(p, stg, lane, row0, col0 + c);
+            }
         }
     }
     tc_fence_before();
@@ -269,6 +324,13 @@ bool encode_operand(CUtensorMap* map, const LinearLaunch& a, bool is_b, int box_
     return mn ? encode_bf16(map, ptr, rows, a.k, ld, kLinBK) : encode_bf16(map, ptr, a.k, rows, ld, box_rows);
 }
 
+// K steps that are added up in TMEM.  Relative error of sums of products of normal
+// values, fp32 output, against 64 bits: 4096 products in one chunk 4.4e-6 (a
+// plain fp32 matrix product 6e-7), 131072 1.5e-4, and 8e-4 if all are positive;
+// chunks of 512 keep it near 6e-7.  bfloat16 outputs are rounded to 2e-3, so
+// theirs need only stay short of that.
+int chunk_of(const LinearLaunch& a) { return (a.out_f32 ? 512 : 2048) / kLinBK; }
+
 LinearParams linear_params(const LinearLaunch& a, int bm, int bn) {
     LinearParams p;
     p.bias = a.bias;
@@ -284,15 +346,14 @@ LinearParams linear_params(const LinearLaunch& a, int bm, int bn) {
     p.num_kb = static_cast<int>((a.k + kLinBK - 1) / kLinBK);
     p.tiles_m = static_cast<int>((a.m + bm - 1) / bm);
     p.tiles_n = static_cast<int>((a.n + bn - 1) / bn);
-    p.act = a.act;
-    p.grad = a.grad;
     p.out_f32 = a.out_f32;
     p.mn_a = a.form == GEMM_FORM_TN;
     p.mn_b = a.form != GEMM_FORM_NT;
     const int64_t es = a.out_f32 ? 4 : 2;
-    p.vec = aligned_to(a.D, 4 * es) && a.ldd % 4 == 0 && (!a.R || (aligned_to(a.R, 4 * es) && a.ldr % 4 == 0)) &&
-            (!a.Z || (aligned_to(a.Z, 8) && a.ldz % 4 == 0)) && aligned_to(a.bias, 16);
+    p.vec = aligned_to(a.D, 16) && a.ldd * es % 16 == 0 && (!a.R || (aligned_to(a.R, 16) && a.ldr * es % 16 == 0)) &&
+            (!a.Z || (aligned_to(a.Z, 16) && a.ldz % 8 == 0)) && aligned_to(a.bias, 16);
     p.halves = false;
+    p.chunk = chunk_of(a);
     return p;
 }
 
@@ -307,28 +368,30 @@ cudaError_t launch_linear_tc2(const LinearLaunch& a, cudaStream_t stream) {
     if (pairs < 1) pairs = 1;
     const int64_t use = p.halves || 2 * tiles <= pairs ? 2 * tiles : tiles;
     if (pairs > use) pairs = use;
-    const void* kern = reinterpret_cast<const void*>(linear_tc2_kernel);
-    const cudaError_t e = kernel_attrs_once(kern, static_cast<int>(kSmem), true);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    uint32_t idesc = idesc_linear(p.mn_a, p.mn_b, 256, kTileN), idesc_half = idesc_linear(p.mn_a, p.mn_b, 256, kTileN / 2);
-    void* args[] = {&mA, &mB, &p, &idesc, &idesc_half};
-    const cudaError_t r = cudaLaunchKernelExC(&cfg, kern, args);
-    return r != cudaSuccess ? r : cudaGetLastError();
+    return by_activation(a, [&](auto act) -> cudaError_t {
+        const void* kern = reinterpret_cast<const void*>(linear_tc2_kernel<decltype(act)::value>);
+        const cudaError_t e = kernel_attrs_once(kern, static_cast<int>(kSmem), true);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof(cfg));
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = kSmem;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        uint32_t idesc = idesc_linear(p.mn_a, p.mn_b, 256, kTileN), idesc_half = idesc_linear(p.mn_a, p.mn_b, 256, kTileN / 2);
+        void* args[] = {&mA, &mB, &p, &idesc, &idesc_half};
+        const cudaError_t r = cudaLaunchKernelExC(&cfg, kern, args);
+        return r != cudaSuccess ? r : cudaGetLastError();
+    });
 }
 
 }  // namespace gemm

@@ -99,9 +99,10 @@ gemm_status gemm_bf16_linear_run(const gemm_plan_linear* plan, const uint16_t* A
     if (!p || p->version != GEMM_PLAN_LINEAR_VERSION) return GEMM_ERR_INVALID_ARG;
     if (check_linear_shape(p->form, p->m, p->k, p->n) != GEMM_OK || !linear_config_ok(p)) return GEMM_ERR_INVALID_ARG;
     if (!A || !B || !D) return GEMM_ERR_INVALID_ARG;
-    const bool grad = (activation & GEMM_ACT_GRADIENT) != 0;
     const int32_t act = activation & ~GEMM_ACT_GRADIENT;
-    if (!act_ok(act) || (grad && !Z && act != GEMM_ACT_NONE)) return GEMM_ERR_INVALID_ARG;
+    const bool grad = (activation & GEMM_ACT_GRADIENT) != 0 && act != GEMM_ACT_NONE;
+    if (!act_ok(act) || (grad && !Z)) return GEMM_ERR_INVALID_ARG;
+    if (activation == (GEMM_ACT_NONE | GEMM_ACT_GRADIENT)) Z = nullptr;   // its derivative is 1: not read
     if (out_type != GEMM_OUT_BF16 && out_type != GEMM_OUT_F32) return GEMM_ERR_INVALID_ARG;
     const int64_t rows_a = p->form == GEMM_FORM_TN ? p->k : p->m, cols_a = p->form == GEMM_FORM_TN ? p->m : p->k;
     const int64_t rows_b = p->form == GEMM_FORM_NT ? p->n : p->k, cols_b = p->form == GEMM_FORM_NT ? p->k : p->n;

@@ -2,6 +2,8 @@
 // shared memory, the MMA, and the epilogue.
 #pragma once
 
+#include <type_traits>
+
 #include "activation.cuh"
 #include "f8_tc.cuh"
 #include "layer.h"
@@ -20,11 +22,11 @@ struct LinearParams {
     int64_t ldd, ldr, ldz;
     int m, n;
     int num_kb;                // K steps
+    int chunk;                 // K steps added up in TMEM, before they join sums in registers
     int tiles_m, tiles_n;
-    int act;
-    bool grad, out_f32;
+    bool out_f32;
     bool mn_a, mn_b;           // A, B stored with their rows (columns of D) contiguous instead of K
-    bool vec;                  // D, R, Z and bias take vectors of four elements
+    bool vec;                  // rows of D, R, Z and bias take vectors of eight elements
     bool halves;               // two-SM kernel: every tile in halves of 128 columns
 };
 
@@ -61,6 +63,12 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
         mma_f16_ss(d_tmem, a_desc, b_desc, idesc, accumulate);
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // Elements of D's type as fp32, and back.
 template <bool F32>
 __device__ __forceinline__ float load_out(const void* p, int64_t i) {
@@ -77,108 +85,133 @@ __device__ __forceinline__ void store_out(void* p, int64_t i, float v) {
         static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// Four values of a row as loaded (bfloat16: two words, fp32: four).
+// Eight values of a row as loaded (bfloat16: four words, fp32: eight).
 template <bool F32>
-struct Four {
-    uint32_t w[F32 ? 4 : 2];
-    __device__ __forceinline__ void load(const void* p, int64_t i) {
-        if constexpr (F32) {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-            w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-        } else {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
-            w[0] = u.x; w[1] = u.y;
-        }
+struct Eight {
+    uint4 u[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const uint8_t* p) {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (uint32_t& x : w) x = 0u;
+        for (uint4& x : u) x = make_uint4(0u, 0u, 0u, 0u);
     }
     __device__ __forceinline__ float at(int t) const {
-        if constexpr (F32) return __uint_as_float(w[t]);
-        return __uint_as_float(t & 1 ? w[t >> 1] & 0xffff0000u : w[t >> 1] << 16);
+        const uint4& x = u[F32 ? t >> 2 : 0];
+        const int w = F32 ? t & 3 : t >> 1;
+        const uint32_t y = w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w;
+        if constexpr (F32) return __uint_as_float(y);
+        return __uint_as_float(t & 1 ? y & 0xffff0000u : y << 16);
     }
 };
 template <bool F32>
-__device__ __forceinline__ void store_four(void* p, int64_t i, float a, float b, float c, float d) {
-    if constexpr (F32)
-        *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a, b, c, d);
-    else
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) = make_uint2(bf16x2(a, b), bf16x2(c, d));
+__device__ __forceinline__ void store_eight(uint8_t* p, const float* v) {
+    if constexpr (F32) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+    }
 }
 
 // The epilogue of a warp's 32 x 32 block of sums in its staging buffer
-// (stage_rows32): rows row0.., columns col0...  Whole aligned blocks: a lane
-// takes four columns of every fourth row, so that eight lanes move one row's
-// piece.  What is read (residual, Z) is asked for before the sums are used.
-template <bool F32>
+// (stage_rows32): rows row0.., columns col0...  Aligned rows: a lane takes eight
+// columns of every eighth row, two rows at a time, so that four lanes move one
+// row's piece (both ways through shared memory without bank conflicts).  What
+// is read (residual, Z) is asked for before the sums are used.  ACT: GEMM_ACT_*,
+// with GEMM_ACT_GRADIENT or without.
+template <bool F32, int ACT>
 __device__ __forceinline__ void finish_block(const LinearParams& p, uint32_t stg, int lane, int row0, int col0) {
-    const int col = col0 + (lane & 7) * 4, r0 = lane >> 3;
-    auto at = [&](int j, int64_t ld) { return static_cast<int64_t>(row0 + r0 + 4 * j) * ld + col; };
-    auto in = [&](int j) { return row0 + r0 + 4 * j < p.m; };
-    float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.bias) bias = __ldg(reinterpret_cast<const float4*>(p.bias + col));
-    Four<false> z[8];
-    Four<F32> r[8];
-    const bool read_z = p.grad && p.Z;
+    constexpr bool kReadZ = (ACT & GEMM_ACT_GRADIENT) != 0;
+    constexpr int ES = F32 ? 4 : 2;
+    const int part = lane & 3, r0 = lane >> 2;
+    const int col = col0 + part * 8;
+    if (col >= p.n) return;   // (n is a multiple of eight, or the block is whole)
+    const int rows = p.m - row0 - r0;   // of the lane's rows r0 + 8 j, those with 8 j < rows exist
+    float bias[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        z[j].zero();
-        if (read_z && in(j)) z[j].load(p.Z, at(j, p.ldz));
+    for (int t = 0; t < 8; ++t) bias[t] = 0.f;
+    if (p.bias) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p.bias + col)), b = __ldg(reinterpret_cast<const float4*>(p.bias + col) + 1);
+        bias[0] = a.x; bias[1] = a.y; bias[2] = a.z; bias[3] = a.w;
+        bias[4] = b.x; bias[5] = b.y; bias[6] = b.z; bias[7] = b.w;
     }
-    if (p.R)
+    const int64_t row = row0 + r0;
+    uint8_t* d = static_cast<uint8_t*>(p.D) + (row * p.ldd + col) * ES;
+    uint8_t* zp = reinterpret_cast<uint8_t*>(p.Z) + (row * p.ldz + col) * 2;
+    const uint8_t* rp = static_cast<const uint8_t*>(p.R) + (row * p.ldr + col) * ES;
+    const int64_t sd = 8 * ES * p.ldd, sz = 16 * p.ldz, sr = 8 * ES * p.ldr;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (in(j)) r[j].load(p.R, at(j, p.ldr)); else r[j].zero();
-    float v[32];
+    for (int half = 0; half < 2; ++half) {
+        Eight<false> z[2];
+        Eight<F32> r[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int row = r0 + 4 * j;
-        const uint4 u = ld_shared_v4(stg + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
-        v[4 * j] = __uint_as_float(u.x) + bias.x;
-        v[4 * j + 1] = __uint_as_float(u.y) + bias.y;
-        v[4 * j + 2] = __uint_as_float(u.z) + bias.z;
-        v[4 * j + 3] = __uint_as_float(u.w) + bias.w;
+        for (int i = 0; i < 2; ++i) {
+            const int j = 2 * half + i;
+            if constexpr (kReadZ) {
+                z[i].zero();
+                if (8 * j < rows) z[i].load(zp + j * sz);
+            }
+            r[i].zero();
+            if (p.R && 8 * j < rows) r[i].load(rp + j * sr);
+        }
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int rr = r0 + 8 * (2 * half + i);
+                const uint4 u = ld_shared_v4(stg + rr * 128 + (((2 * part + k) ^ (rr & 7)) << 4));
+                float* x = v + 8 * i + 4 * k;
+                x[0] = __uint_as_float(u.x) + bias[4 * k];
+                x[1] = __uint_as_float(u.y) + bias[4 * k + 1];
+                x[2] = __uint_as_float(u.z) + bias[4 * k + 2];
+                x[3] = __uint_as_float(u.w) + bias[4 * k + 3];
+            }
+        if constexpr (!kReadZ)
+            if (p.Z)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (8 * (2 * half + i) < rows) store_eight<false>(zp + (2 * half + i) * sz, v + 8 * i);
+        activate_each<ACT, 16>(v, [&](int i) { return kReadZ ? z[i >> 3].at(i & 7) : 0.f; });
+        if (p.R)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += r[i >> 3].at(i & 7);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (8 * (2 * half + i) < rows) store_eight<F32>(d + (2 * half + i) * sd, v + 8 * i);
     }
-    if (p.Z && !p.grad)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (in(j)) store_four<false>(p.Z, at(j, p.ldz), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    activate_all<32>(p.act, p.grad, v, [&](int i) { return z[i >> 2].at(i & 3); });
-    if (p.R)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += r[i >> 2].at(i & 3);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (in(j)) store_four<F32>(p.D, at(j, p.ldd), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
 // N rows of one column (row0.. by steps of one; `rows` of them exist), for
-// blocks at a ragged edge and unaligned rows: the lanes of a warp hold
-// neighbouring columns, so that every access is contiguous along a row
-// whatever its alignment.  v: the sums.
-template <bool F32, int N>
+// ragged edges and unaligned rows: the lanes of a warp hold neighbouring
+// columns, so that every access is contiguous along a row whatever its
+// alignment.  v: the sums.
+template <bool F32, int ACT, int N>
 __device__ __forceinline__ void finish_column(const LinearParams& p, int row0, int rows, int col, float (&v)[N]) {
-    if (col >= p.n) rows = 0;
-    const float bias = p.bias && rows > 0 ? __ldg(p.bias + col) : 0.f;
+    constexpr bool kReadZ = (ACT & GEMM_ACT_GRADIENT) != 0;
+    if (col >= p.n) return;
+    const float bias = p.bias ? __ldg(p.bias + col) : 0.f;
     auto at = [&](int i, int64_t ld) { return static_cast<int64_t>(row0 + i) * ld + col; };
     float z[N], r[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = p.grad && p.Z && i < rows ? __bfloat162float(p.Z[at(i, p.ldz)]) : 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = p.R && i < rows ? load_out<F32>(p.R, at(i, p.ldr)) : 0.f;
+    for (int i = 0; i < N; ++i) {
+        z[i] = kReadZ && i < rows ? __bfloat162float(p.Z[at(i, p.ldz)]) : 0.f;
+        r[i] = p.R && i < rows ? load_out<F32>(p.R, at(i, p.ldr)) : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += bias;
-    if (p.Z && !p.grad)
+    if (!kReadZ && p.Z)
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (i < rows) p.Z[at(i, p.ldz)] = __float2bfloat16_rn(v[i]);
-    activate_all<N>(p.act, p.grad, v, [&](int i) { return z[i]; });
+    activate_each<ACT, N>(v, [&](int i) { return z[i]; });
 #pragma unroll
     for (int i = 0; i < N; ++i)
         if (i < rows) store_out<F32>(p.D, at(i, p.ldd), p.R ? v[i] + r[i] : v[i]);
 }
-template <bool F32>
+template <bool F32, int ACT>
 __device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t stg, int lane, int row0, int col0) {
     constexpr int N = 8;   // rows in flight
 #pragma unroll 1
@@ -186,8 +219,38 @@ __device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t st
         float v[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = __uint_as_float(staged_at(stg, j + i, lane));
-        finish_column<F32, N>(p, row0 + j, min(N, p.m - row0 - j), col0 + lane, v);
+        finish_column<F32, ACT, N>(p, row0 + j, min(N, p.m - row0 - j), col0 + lane, v);
     }
+}
+// Either of them for the block at (row0, col0).
+template <int ACT>
+__device__ __forceinline__ void finish(const LinearParams& p, uint32_t stg, int lane, int row0, int col0) {
+    const bool vec = p.vec && (p.n % 8 == 0 || col0 + 32 <= p.n);
+    if (p.out_f32) {
+        if (vec) finish_block<true, ACT>(p, stg, lane, row0, col0);
+        else finish_ragged<true, ACT>(p, stg, lane, row0, col0);
+    } else {
+        if (vec) finish_block<false, ACT>(p, stg, lane, row0, col0);
+        else finish_ragged<false, ACT>(p, stg, lane, row0, col0);
+    }
+}
+
+// Host: calls f(integral constant of the launch's ACT).
+template <typename F>
+cudaError_t by_activation(const LinearLaunch& a, F f) {
+#define GEMM_ACT_CASE(ACT) case ACT: return f(std::integral_constant<int, ACT>{});
+    switch (a.act | (a.grad ? GEMM_ACT_GRADIENT : 0)) {
+        GEMM_ACT_CASE(GEMM_ACT_RELU)
+        GEMM_ACT_CASE(GEMM_ACT_GELU)
+        GEMM_ACT_CASE(GEMM_ACT_GELU_TANH)
+        GEMM_ACT_CASE(GEMM_ACT_SILU)
+        GEMM_ACT_CASE(GEMM_ACT_RELU | GEMM_ACT_GRADIENT)
+        GEMM_ACT_CASE(GEMM_ACT_GELU | GEMM_ACT_GRADIENT)
+        GEMM_ACT_CASE(GEMM_ACT_GELU_TANH | GEMM_ACT_GRADIENT)
+        GEMM_ACT_CASE(GEMM_ACT_SILU | GEMM_ACT_GRADIENT)
+        default: return f(std::integral_constant<int, GEMM_ACT_NONE>{});   // (the gradient of none is none: Z is not given)
+    }
+#undef GEMM_ACT_CASE
 }
 
 // Host: the kernels' parameters for tiles of bm x bn of D.
