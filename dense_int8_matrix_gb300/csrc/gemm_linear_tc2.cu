@@ -236,6 +236,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
         Turn<2> buf;
         bool ok = true;
+        auto prefetch = [&](int u) {
+            if (u >= list.count || !((ACT & GEMM_ACT_GRADIENT) != 0 || p.R)) return;
+            const Unit w = unit_at(u, list, p);
+            const int cols = w.half ? kTileN / 4 : kTileN / 2;
+            prefetch_rows<(ACT & GEMM_ACT_GRADIENT) != 0>(p, lane, w.row + static_cast<int>(rank) * kHalfRows + q * 32,
+                                                          w.col + h * cols, cols);
+        };
+        prefetch(pair);
         for (int u = pair; ok && u < list.count; u += npairs) {
             const Unit w = unit_at(u, list, p);
             const int steps = steps_of(w, p);
@@ -275,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     add_block(acc + 48, v[1]);
             }
             if (!ok) break;
+            prefetch(u + npairs);
 #pragma unroll 1
             for (int c = 0; c < cols; c += 32) {
                 if (row0 >= p.m || col0 + c >= p.n) break;   // (the whole warp alike)
@@ -286,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     default: stage_block(stg, lane, acc + 48); break;
                 }
                 __syncwarp();
-                finish<ACT>(p, stg, lane, row0, col0 + c);
+                finish<ACT>(p, stg, lane, row0, p.m, col0 + c);
             }
         }
     }
@@ -352,6 +361,8 @@ LinearParams linear_params(const LinearLaunch& a, int bm, int bn) {
     const int64_t es = a.out_f32 ? 4 : 2;
     p.vec = aligned_to(a.D, 16) && a.ldd * es % 16 == 0 && (!a.R || (aligned_to(a.R, 16) && a.ldr * es % 16 == 0)) &&
             (!a.Z || (aligned_to(a.Z, 16) && a.ldz % 8 == 0)) && aligned_to(a.bias, 16);
+    p.pairs = aligned_to(a.D, 4) && a.ldd % 2 == 0 && (!a.R || (aligned_to(a.R, 4) && a.ldr % 2 == 0)) &&
+              (!a.Z || (aligned_to(a.Z, 4) && a.ldz % 2 == 0));
     p.halves = false;
     p.chunk = chunk_of(a);
     return p;

@@ -30,6 +30,8 @@ struct LinearLaunch {
 };
 // Two-SM tiles of 256 x bn (gemm_linear_tc2.cu).
 cudaError_t launch_linear_tc2(const LinearLaunch& a, cudaStream_t stream);
+// Tiles of bm (16, 32, 64, 128; GEMM_FORM_TN 64, 128) rows x 128 columns, split_k CTAs each (gemm_linear_skinny.cu).
+cudaError_t launch_linear_skinny(const LinearLaunch& a, cudaStream_t stream);
 
 // Copies a bfloat16 matrix of any address and pitch to rows that are 16-byte
 // aligned (dst, pitch a multiple of 8).

@@ -66,7 +66,10 @@ gemm_status make_linear_plan(int32_t form, int64_t m, int64_t k, int64_t n, int3
 }
 
 bool linear_config_ok(const gemm_plan_linear* p) {
-    return p->path == GEMM_PATH_TENSOR && p->bm == 256 && (p->bn == 128 || p->bn == 256) && p->split_k == 1;
+    if (p->path == GEMM_PATH_TENSOR) return p->bm == 256 && (p->bn == 128 || p->bn == 256) && p->split_k == 1;
+    const int bm = p->bm, s = p->split_k;
+    return p->path == GEMM_PATH_SKINNY && (bm == 64 || bm == 128 || (p->form != GEMM_FORM_TN && (bm == 16 || bm == 32))) &&
+           p->bn == 128 && (s == 1 || s == 2 || s == 4 || s == 8);
 }
 
 // A matrix that TMA can read as it lies.
@@ -162,7 +165,7 @@ gemm_status gemm_bf16_linear_run(const gemm_plan_linear* plan, const uint16_t* A
     if (r != GEMM_OK) return r;
     const int kind = p->path == GEMM_PATH_SKINNY ? GEMM_KERNEL_SKINNY : GEMM_KERNEL_TC;
     void* unit = trace_unit_begin(kind, s, sampled);
-    const cudaError_t e = launch_linear_tc2(L, s);
+    const cudaError_t e = p->path == GEMM_PATH_SKINNY ? launch_linear_skinny(L, s) : launch_linear_tc2(L, s);
     trace_unit_end(unit, s);
     if (e != cudaSuccess) return GEMM_ERR_CUDA;
     trace_launch(kind);

@@ -27,6 +27,7 @@ struct LinearParams {
     bool out_f32;
     bool mn_a, mn_b;           // A, B stored with their rows (columns of D) contiguous instead of K
     bool vec;                  // rows of D, R, Z and bias take vectors of eight elements
+    bool pairs;                // rows of bfloat16 D, R and Z start at even elements
     bool halves;               // two-SM kernel: every tile in halves of 128 columns
 };
 
@@ -122,13 +123,13 @@ __device__ __forceinline__ void store_eight(uint8_t* p, const float* v) {
 // is read (residual, Z) is asked for before the sums are used.  ACT: GEMM_ACT_*,
 // with GEMM_ACT_GRADIENT or without.
 template <bool F32, int ACT>
-__device__ __forceinline__ void finish_block(const LinearParams& p, uint32_t stg, int lane, int row0, int col0) {
+__device__ __forceinline__ void finish_block(const LinearParams& p, uint32_t stg, int lane, int row0, int row_end, int col0) {
     constexpr bool kReadZ = (ACT & GEMM_ACT_GRADIENT) != 0;
     constexpr int ES = F32 ? 4 : 2;
     const int part = lane & 3, r0 = lane >> 2;
     const int col = col0 + part * 8;
     if (col >= p.n) return;   // (n is a multiple of eight, or the block is whole)
-    const int rows = p.m - row0 - r0;   // of the lane's rows r0 + 8 j, those with 8 j < rows exist
+    const int rows = row_end - row0 - r0;   // of the lane's rows r0 + 8 j, those with 8 j < rows exist
     float bias[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t) bias[t] = 0.f;
@@ -184,8 +185,39 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, uint32_t stg
     }
 }
 
+// One or two neighbouring bfloat16 values (two only at even elements); of two
+// columns the second may be past the row.
+template <int W>
+__device__ __forceinline__ uint32_t load_some(const __nv_bfloat16* p, int64_t cols) {
+    if (W == 2 && cols >= 2) return *reinterpret_cast<const uint32_t*>(p);
+    return *reinterpret_cast<const uint16_t*>(p);
+}
+template <int W>
+__device__ __forceinline__ void store_some(__nv_bfloat16* p, int64_t cols, const float* v) {
+    if (W == 2 && cols >= 2)
+        *reinterpret_cast<uint32_t*>(p) = bf16x2(v[0], v[W - 1]);
+    else
+        *p = __float2bfloat16_rn(v[0]);
+}
+
+// Asks the L2 for the rows that the epilogue of rows row0 .. row0 + 31 and
+// `cols` columns from col0 will read, a row per lane, while the products run.
+template <bool READ_Z>
+__device__ __forceinline__ void prefetch_rows(const LinearParams& p, int lane, int row0, int col0, int cols) {
+    const int64_t row = row0 + lane;
+    const int64_t n = min(cols, p.n - col0);
+    if (row >= p.m || n <= 0) return;
+    auto ask = [](const uint8_t* at, int64_t bytes) {
+        for (int64_t i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + bytes - 1));
+    };
+    if constexpr (READ_Z) ask(reinterpret_cast<const uint8_t*>(p.Z + row * p.ldz + col0), 2 * n);
+    const int64_t es = p.out_f32 ? 4 : 2;
+    if (p.R) ask(static_cast<const uint8_t*>(p.R) + (row * p.ldr + col0) * es, es * n);
+}
+
 // N rows of one column (row0.. by steps of one; `rows` of them exist), for
-// ragged edges and unaligned rows: the lanes of a warp hold neighbouring
+// tiles of few rows, whose sums need no staging: the lanes of a warp hold neighbouring
 // columns, so that every access is contiguous along a row whatever its
 // alignment.  v: the sums.
 template <bool F32, int ACT, int N>
@@ -211,27 +243,88 @@ __device__ __forceinline__ void finish_column(const LinearParams& p, int row0, i
     for (int i = 0; i < N; ++i)
         if (i < rows) store_out<F32>(p.D, at(i, p.ldd), p.R ? v[i] + r[i] : v[i]);
 }
-template <bool F32, int ACT>
-__device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t stg, int lane, int row0, int col0) {
-    constexpr int N = 8;   // rows in flight
-#pragma unroll 1
-    for (int j = 0; j < 32 && row0 + j < p.m; j += N) {
-        float v[N];
+// The same 32 x 32 block of a ragged edge, or of rows that are not aligned
+// for vectors: a lane takes one column of every row, or (PAIRS, rows at even
+// elements) two columns of every other row, so that every access is contiguous
+// along a row.  What is read is asked for sixteen rows ahead.
+template <bool F32, int ACT, bool PAIRS>
+__device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t stg, int lane, int row0, int row_end, int col0) {
+    constexpr bool kReadZ = (ACT & GEMM_ACT_GRADIENT) != 0;
+    constexpr int W = PAIRS ? 2 : 1;          // columns of a lane, and rows of an access
+    constexpr int N = 16 / W;                 // accesses in flight
+    const int c = PAIRS ? (lane & 15) * 2 : lane, r0 = PAIRS ? lane >> 4 : 0;
+    const int col = col0 + c, cols = p.n - col;   // the lane's columns: all W, or the first, or none
+    if (cols <= 0) return;
+    float bias[W];
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __uint_as_float(staged_at(stg, j + i, lane));
-        finish_column<F32, ACT, N>(p, row0 + j, min(N, p.m - row0 - j), col0 + lane, v);
+    for (int t = 0; t < W; ++t) bias[t] = p.bias && t < cols ? __ldg(p.bias + col + t) : 0.f;
+    const int64_t row = row0 + r0;
+    const __nv_bfloat16* zp = p.Z + row * p.ldz + col;
+    const uint8_t* rp = static_cast<const uint8_t*>(p.R) + (row * p.ldr + col) * (F32 ? 4 : 2);
+    uint8_t* dp = static_cast<uint8_t*>(p.D) + (row * p.ldd + col) * (F32 ? 4 : 2);
+    const int rows = row_end - row0 - r0;
+#pragma unroll 1
+    for (int j = 0; j < 32 / W; j += N) {
+        if (W * j >= rows) break;
+        uint32_t z[N], r[N * (F32 ? W : 1)];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const bool in = W * (j + i) < rows;
+            if constexpr (kReadZ) z[i] = in ? load_some<W>(zp + W * (j + i) * p.ldz, cols) : 0u;
+            if constexpr (F32) {
+#pragma unroll
+                for (int t = 0; t < W; ++t)
+                    r[i * W + t] = p.R && in && t < cols ? reinterpret_cast<const uint32_t*>(rp)[W * (j + i) * p.ldr + t] : 0u;
+            } else {
+                r[i] = p.R && in ? load_some<W>(reinterpret_cast<const __nv_bfloat16*>(rp) + W * (j + i) * p.ldr, cols) : 0u;
+            }
+        }
+        float v[N * W];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int rr = r0 + W * (j + i);
+            const uint32_t at = stg + rr * 128 + (((c >> 2) ^ (rr & 7)) << 4) + (c & 3) * 4;
+#pragma unroll
+            for (int t = 0; t < W; ++t) v[i * W + t] = __uint_as_float(ld_shared_u32(at + 4 * t)) + bias[t];
+        }
+        if constexpr (!kReadZ)
+            if (p.Z)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (W * (j + i) < rows) store_some<W>(const_cast<__nv_bfloat16*>(zp) + W * (j + i) * p.ldz, cols, v + i * W);
+        activate_each<ACT, N * W>(v, [&](int i) {
+            return kReadZ ? __uint_as_float(i % W ? z[i / W] & 0xffff0000u : z[i / W] << 16) : 0.f;
+        });
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (p.R)
+#pragma unroll
+                for (int t = 0; t < W; ++t)
+                    v[i * W + t] += F32 ? __uint_as_float(r[F32 ? i * W + t : 0]) : __uint_as_float(t ? r[i] & 0xffff0000u : r[i] << 16);
+            if (W * (j + i) < rows) {
+                if constexpr (F32) {
+#pragma unroll
+                    for (int t = 0; t < W; ++t)
+                        if (t < cols) reinterpret_cast<float*>(dp)[W * (j + i) * p.ldd + t] = v[i * W + t];
+                } else {
+                    store_some<W>(reinterpret_cast<__nv_bfloat16*>(dp) + W * (j + i) * p.ldd, cols, v + i * W);
+                }
+            }
+        }
     }
 }
-// Either of them for the block at (row0, col0).
+// Either of them for the block at (row0, col0); rows at or past row_end are
+// not its own.
 template <int ACT>
-__device__ __forceinline__ void finish(const LinearParams& p, uint32_t stg, int lane, int row0, int col0) {
+__device__ __forceinline__ void finish(const LinearParams& p, uint32_t stg, int lane, int row0, int row_end, int col0) {
     const bool vec = p.vec && (p.n % 8 == 0 || col0 + 32 <= p.n);
     if (p.out_f32) {
-        if (vec) finish_block<true, ACT>(p, stg, lane, row0, col0);
-        else finish_ragged<true, ACT>(p, stg, lane, row0, col0);
+        if (vec) finish_block<true, ACT>(p, stg, lane, row0, row_end, col0);
+        else finish_ragged<true, ACT, false>(p, stg, lane, row0, row_end, col0);
     } else {
-        if (vec) finish_block<false, ACT>(p, stg, lane, row0, col0);
-        else finish_ragged<false, ACT>(p, stg, lane, row0, col0);
+        if (vec) finish_block<false, ACT>(p, stg, lane, row0, row_end, col0);
+        else if (p.pairs) finish_ragged<false, ACT, true>(p, stg, lane, row0, row_end, col0);
+        else finish_ragged<false, ACT, false>(p, stg, lane, row0, row_end, col0);
     }
 }
 

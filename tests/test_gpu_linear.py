@@ -47,6 +47,9 @@ def plans(form, m, k, n):
     yield edit()
     for bn in (128, 256):
         yield edit(path=B.GEMM_PATH_TENSOR, bm=256, bn=bn, split_k=1)
+    for bm in (64, 128) if form == TN else (16, 32, 64, 128):
+        for split in (1, 2, 4, 8):
+            yield edit(path=B.GEMM_PATH_SKINNY, bm=bm, bn=128, split_k=split)
 
 
 def filled(*shape, dtype=torch.bfloat16, fill=float("nan")):
