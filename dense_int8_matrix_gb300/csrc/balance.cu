@@ -4,14 +4,20 @@
 //   loss = coef * E * sum(f * P)
 //   dx = dr + dloss * coef * E / T * p * (f - sum(f * p))
 //
-// Bound by DRAM: the logits are read once by each pass.  A warp takes a row at
-// a time, its lanes the columns lane + 32 v, so that each lane keeps the sums of
-// p over its own columns in registers.  A CTA writes its sums of p and its
-// counts; a second kernel adds them in CTA order and forms the loss.
-#include "f8.cuh"
+// Bound by DRAM: the logits are read once by each pass.  L lanes (as many as
+// have four columns each, 32 at most) hold a row, so that a warp takes 32 / L
+// rows at once, whatever the number of experts, and a lane has the same columns
+// of every row: its sums of p stay in registers.  The next row is on its way
+// while one is worked on.  Sums are joined in a fixed order: rows of a lane, row
+// groups of a warp, warps of a CTA, the eight CTAs of a cluster (through
+// distributed shared memory), and clusters by a second kernel.  Batches that
+// one cluster (or one CTA) takes in a few turns need no second kernel.
+#include <type_traits>
+
+#include "activation.cuh"
+#include "f8_tc.cuh"
 #include "internal.h"
 #include "layer.h"
-#include "ptx.cuh"
 
 namespace gemm {
 
@@ -19,243 +25,499 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kLossThreads = 1024;
 constexpr int kRowsPerSum = 32;   // rows added in a row before they join the running sum
+constexpr int kFewTurns = 4;      // of rows, up to which one cluster takes a whole batch
+constexpr float kInf = __builtin_huge_valf();
+constexpr int kExpertsPerThread = GEMM_BALANCE_MAX_EXPERTS / kThreads;
+static_assert(kLossThreads >= GEMM_BALANCE_MAX_EXPERTS, "a thread per expert");
 
-// exp(a - largest) of a warp's row in place, and 1 / their sum (0 for a row of
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ int32_t ld_cluster_i32(uint32_t addr) {
+    int32_t v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// A lane's columns of a row: four at 4 * (l + L * u) for each u < U; -infinity
+// past the row.  VEC: rows take vectors of four.
+template <int L, int U>
+__device__ __forceinline__ int column(int l, int i) { return 4 * (l + L * (i >> 2)) + (i & 3); }
+template <typename T, int L, int U, bool VEC>
+__device__ __forceinline__ void load_row(const T* x, int l, int e, float fill, float (&a)[4 * U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = 4 * (l + L * u);
+        if constexpr (VEC) {
+            if (c < e) {
+                if constexpr (sizeof(T) == 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(x + c);
+                    a[4 * u] = v.x; a[4 * u + 1] = v.y; a[4 * u + 2] = v.z; a[4 * u + 3] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(x + c);
+                    a[4 * u] = __uint_as_float(v.x << 16); a[4 * u + 1] = __uint_as_float(v.x & 0xffff0000u);
+                    a[4 * u + 2] = __uint_as_float(v.y << 16); a[4 * u + 3] = __uint_as_float(v.y & 0xffff0000u);
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[4 * u + t] = fill;
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) a[4 * u + t] = c + t < e ? to_f32(x[c + t]) : fill;
+        }
+    }
+}
+template <int L>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+template <int L, typename V>
+__device__ __forceinline__ V group_sum(V v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// exp(a - largest) of a row in place, and 1 / their sum (0 for a row of
 // -infinity alone, whose p are 0); a NaN or +infinity makes the sum NaN.
-// Columns past the row hold -infinity.
-template <int V>
-__device__ __forceinline__ float exponentials(float (&a)[V], float& base, float& sum) {
+template <int L, int N>
+__device__ __forceinline__ float exponentials(float (&a)[N], float& base, float& sum) {
     float top = a[0];
 #pragma unroll
-    for (int v = 1; v < V; ++v) top = fmaxf(top, a[v]);
-    top = warp_max(top);
-    base = top == -__int_as_float(0x7f800000) ? 0.f : top;
+    for (int i = 1; i < N; ++i) top = fmaxf(top, a[i]);
+    top = group_max<L>(top);
+    base = top == -kInf ? 0.f : top;
     sum = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        a[v] = expf(a[v] - base);
-        sum += a[v];
+    for (int i = 0; i < N; ++i) {
+        a[i] = __expf(a[i] - base);   // within (2 + 1.16 |a - base|) 2^-23 of itself: p a few units of fp32 off
+        sum += a[i];
     }
-    sum = warp_sum(sum);
-    return sum == 0.f ? 0.f : 1.f / sum;
+    sum = group_sum<L>(sum);
+    return sum == 0.f ? 0.f : rcp_approx(sum);
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) balance_rows_kernel(const Balance p) {
-    extern __shared__ int32_t shared[];   // counts[experts + 1] (the last one: used rows), then sums[warps][experts]
-    int32_t* hist = shared;
-    float* sums = reinterpret_cast<float*>(shared + p.experts + 1);
-    pdl_launch_dependents();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = p.experts;
-    for (int i = threadIdx.x; i <= e; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    float total[V], part[V];
+// Counts, offsets, means and the loss from the counts and sums of p of experts
+// N t .. N t + N - 1 in thread t, and the used rows.  One CTA of WARPS warps.
+template <int N, int WARPS>
+__device__ __forceinline__ void write_loss(const Balance& p, const int32_t (&count)[N], const float (&sum)[N], int32_t rows) {
+    __shared__ int32_t scan[WARPS];
+    __shared__ float red[WARPS];
+    const int e = p.experts, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    int32_t mine = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) total[v] = part[v] = 0.f;
-    int pending = 0, mine = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp; row < p.rows; row += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int32_t* index = p.index + row * p.top_k;
-        bool taken = false;
-        for (int k = lane; k < p.top_k; k += 32) {
-            const int32_t i = __ldg(index + k);
-            if (i >= 0 && i < e) {
-                taken = true;
-                atomicAdd(hist + i, 1);
-            }
-        }
-        if (!__any_sync(0xffffffffu, taken)) {   // padding: not read
-            if (lane == 0) p.lse[row] = __int_as_float(0x7f800000);
-            continue;
-        }
-        ++mine;
-        const T* x = static_cast<const T*>(p.X) + row * p.ldx;
-        float a[V], base, sum;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = lane + 32 * v;
-            a[v] = c < e ? to_f32(x[c]) : -__int_as_float(0x7f800000);
-        }
-        const float inv = exponentials<V>(a, base, sum);
-        if (lane == 0) p.lse[row] = base + logf(sum);
-#pragma unroll
-        for (int v = 0; v < V; ++v) part[v] = fmaf(a[v], inv, part[v]);
-        if (++pending == kRowsPerSum) {
-            pending = 0;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                total[v] += part[v];
-                part[v] = 0.f;
-            }
-        }
-    }
-    if (lane == 0 && mine) atomicAdd(hist + e, mine);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (lane + 32 * v < e) sums[warp * e + lane + 32 * v] = total[v] + part[v];
-    __syncthreads();
-    for (int i = threadIdx.x; i <= e; i += kThreads) {
-        p.partial_c[static_cast<int64_t>(blockIdx.x) * (e + 1) + i] = hist[i];
-        if (i == e) break;
-        float s = sums[i];
-        for (int w = 1; w < kWarps; ++w) s += sums[w * e + i];
-        p.partial_p[static_cast<int64_t>(blockIdx.x) * e + i] = s;
-    }
-}
-
-// One CTA: a thread per expert adds the CTAs' sums, then counts, offsets and
-// the loss.
-__global__ void __launch_bounds__(1024) balance_loss_kernel(const Balance p) {
-    __shared__ int32_t scan[32];
-    __shared__ float red[32];
-    pdl_launch_dependents();
-    pdl_wait();
-    const int e = p.experts, t = threadIdx.x, lane = t & 31, warp = t >> 5, warps = blockDim.x >> 5;
-    int32_t count = 0, rows = 0;
-    float sum = 0.f;
-    if (t < e)
-        for (int i = 0; i < p.parts; ++i) {
-            count += p.partial_c[static_cast<int64_t>(i) * (e + 1) + t];
-            sum += p.partial_p[static_cast<int64_t>(i) * e + t];
-        }
-    for (int i = lane; i < p.parts; i += 32) rows += p.partial_c[static_cast<int64_t>(i) * (e + 1) + e];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
-    int32_t before = count;
+    for (int i = 0; i < N; ++i) mine += count[i];
+    int32_t before = mine;   // of the warp's threads up to this one
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int32_t up = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += up;
     }
     if (lane == 31) scan[warp] = before;
+    before -= mine;
     __syncthreads();
     int32_t slots = 0;
-    for (int w = 0; w < warps; ++w) {
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += scan[w];
         slots += scan[w];
     }
-    const float prob = rows > 0 ? sum / static_cast<float>(rows) : 0.f;
-    const float share = slots > 0 ? static_cast<float>(count) / static_cast<float>(slots) : 0.f;
-    float l = warp_sum(t < e ? share * prob : 0.f);
+    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = N * t + i;
+        before += count[i];
+        if (c >= e) continue;
+        const float prob = rows > 0 ? sum[i] / static_cast<float>(rows) : 0.f;
+        const float share = slots > 0 ? static_cast<float>(count[i]) / static_cast<float>(slots) : 0.f;
+        l += share * prob;
+        p.counts[c] = count[i];
+        p.probs[c] = prob;
+        if (p.offsets) p.offsets[c + 1] = before;
+    }
+    l = warp_sum(l);
     if (lane == 0) red[warp] = l;
     __syncthreads();
-    if (warp == 0) l = warp_sum(lane < warps ? red[lane] : 0.f);
-    if (t < e) {
-        p.counts[t] = count;
-        p.probs[t] = prob;
-        if (p.offsets) p.offsets[t + 1] = before;
-    }
-    if (t == 0) {
-        if (p.offsets) p.offsets[0] = 0;
-        *p.used = rows;
-        *p.loss = p.coef * static_cast<float>(e) * l;
+    if (warp == 0) {
+        l = warp_sum(lane < WARPS ? red[lane] : 0.f);
+        if (lane == 0) {
+            if (p.offsets) p.offsets[0] = 0;
+            *p.used = rows;
+            *p.loss = p.coef * static_cast<float>(e) * l;
+        }
     }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalanceBwd p) {
+template <typename T, int L, int U, bool VEC>
+__global__ void __launch_bounds__(kThreads) balance_rows_kernel(const Balance p, int cluster) {
+    constexpr int N = 4 * U, kGroups = 32 / L;
+    constexpr bool kCountInRegisters = L <= 4;   // (few experts: shared counters would be fought over)
+    extern __shared__ int32_t shared[];          // counts[experts + 1] (the last one: used rows), sums[warps][experts]
+    int32_t* hist = shared;
+    float* sums = reinterpret_cast<float*>(shared + p.experts + 1);
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = p.experts;
-    int32_t slots = 0;
-    float f[V];
+    const int l = lane % L, group = lane / L;
+    for (int i = threadIdx.x; i <= e; i += kThreads) hist[i] = 0;
+    __syncthreads();
+    float total[N], part[N], x[2][N];
+    int32_t slot[2], counted[kCountInRegisters ? N : 1], used_rows = 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int32_t c = lane + 32 * v < e ? __ldg(p.counts + lane + 32 * v) : 0;
-        slots += c;
-        f[v] = static_cast<float>(c);
+    for (int i = 0; i < N; ++i) total[i] = part[i] = 0.f;
+#pragma unroll
+    for (int32_t& c : counted) c = 0;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kGroups;
+    int64_t row = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kGroups + group;
+    const T* at = static_cast<const T*>(p.X) + row * p.ldx;
+    const int32_t* index = p.index + row * p.top_k + l;
+    const int64_t at_step = step * p.ldx, index_step = step * p.top_k;
+    int64_t ahead = row;   // the row that `at` and `index` point to
+    auto fetch = [&](float (&a)[N], int32_t& s) {
+        s = -1;
+        if (ahead < p.rows) {
+            load_row<T, L, U, VEC>(at, l, e, -kInf, a);
+            if (l < p.top_k) s = __ldg(index);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) a[i] = -kInf;
+        }
+        at += at_step;
+        index += index_step;
+        ahead += step;
+    };
+    auto work = [&](float (&a)[N], int32_t s) {
+        const bool mine = row < p.rows;
+        bool taken = false;
+        for (int k = 0;;) {
+            const bool in = static_cast<uint32_t>(s) < static_cast<uint32_t>(e);
+            taken = taken || in;
+            if constexpr (kCountInRegisters) {
+#pragma unroll
+                for (int j = 0; j < L; ++j) {
+                    const int32_t y = L == 1 ? s : __shfl_sync(0xffffffffu, s, (lane & ~(L - 1)) + j);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) counted[i] += y == column<L, U>(l, i) ? 1 : 0;
+                }
+            } else if (in) {
+                atomicAdd(hist + s, 1);
+            }
+            k += L;
+            if (k >= p.top_k) break;
+            s = mine && k + l < p.top_k ? __ldg(p.index + row * p.top_k + k + l) : -1;
+        }
+        const uint32_t votes = __ballot_sync(0xffffffffu, taken);
+        const bool used = ((votes >> (lane & ~(L - 1))) & (L == 32 ? 0xffffffffu : (1u << (L % 32)) - 1u)) != 0;
+        float base, sum;
+        const float inv = exponentials<L, N>(a, base, sum);
+        if (l == 0 && mine) p.lse[row] = used ? base + __logf(sum) : kInf;   // (sum is 1 to 1024, or 0, or NaN)
+        if (used) {   // (padding takes no part, whatever it holds)
+            if (l == 0) ++used_rows;
+#pragma unroll
+            for (int i = 0; i < N; ++i) part[i] = fmaf(a[i], inv, part[i]);
+        }
+        row += step;
+    };
+    // a warp's rows: while any of its groups has one, and the second of each
+    // two may be past the end
+    int64_t first = row - group;
+    fetch(x[0], slot[0]);
+    for (int pending = 0; first < p.rows; first += 2 * step) {
+        fetch(x[1], slot[1]);
+        work(x[0], slot[0]);
+        fetch(x[0], slot[0]);
+        work(x[1], slot[1]);
+        if ((pending += 2) == kRowsPerSum) {
+            pending = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                total[i] += part[i];
+                part[i] = 0.f;
+            }
+        }
     }
+    // the warp's row groups, then the CTA's warps
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) slots += __shfl_xor_sync(0xffffffffu, slots, o);
+    for (int i = 0; i < N; ++i) {
+        total[i] += part[i];
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) total[i] += __shfl_xor_sync(0xffffffffu, total[i], o);
+        const int c = column<L, U>(l, i);
+        if (group == 0 && c < e) sums[warp * e + c] = total[i];
+        if constexpr (kCountInRegisters) {
+#pragma unroll
+            for (int o = L; o < 32; o <<= 1) counted[i] += __shfl_xor_sync(0xffffffffu, counted[i], o);
+            if (group == 0 && c < e && counted[i]) atomicAdd(hist + c, counted[i]);
+        }
+    }
+    used_rows = group_sum<32>(used_rows);
+    if (lane == 0 && used_rows) atomicAdd(hist + e, used_rows);
+    __syncthreads();
+    for (int c = threadIdx.x; c < e; c += kThreads) {
+        float s = sums[c];
+        for (int w = 1; w < kWarps; ++w) s += sums[w * e + c];
+        sums[c] = s;   // (its only reader)
+    }
+    // the cluster's CTAs
+    const uint32_t hist0 = smem_u32(hist), sums0 = smem_u32(sums);
+    auto joined_count = [&](int c) {
+        int32_t v = 0;
+        for (int r = 0; r < cluster; ++r) v += ld_cluster_i32(peer_address(hist0 + 4 * c, r));
+        return v;
+    };
+    auto joined_sum = [&](int c) {
+        float v = 0.f;
+        for (int r = 0; r < cluster; ++r) v += ld_cluster_f32(peer_address(sums0 + 4 * c, r));
+        return v;
+    };
+    if (cluster > 1)
+        cluster_barrier();
+    else
+        __syncthreads();
+    const int rank = static_cast<int>(blockIdx.x) % cluster, id = static_cast<int>(blockIdx.x) / cluster;
+    if (p.parts == 1) {
+        if (rank == 0) {
+            auto join = [&](auto n) {   // experts per thread
+                constexpr int kPer = decltype(n)::value;
+                int32_t count[kPer];
+                float sum[kPer];
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const int c = kPer * static_cast<int>(threadIdx.x) + i;
+                    count[i] = c < e ? joined_count(c) : 0;
+                    sum[i] = c < e ? joined_sum(c) : 0.f;
+                }
+                write_loss<kPer, kWarps>(p, count, sum, joined_count(e));
+            };
+            if (e <= kThreads)
+                join(std::integral_constant<int, 1>{});
+            else
+                join(std::integral_constant<int, kExpertsPerThread>{});
+        }
+    } else {
+        for (int c = rank + cluster * static_cast<int>(threadIdx.x); c <= e; c += cluster * kThreads) {
+            p.partial_c[static_cast<int64_t>(id) * (e + 1) + c] = joined_count(c);
+            if (c < e) p.partial_p[static_cast<int64_t>(id) * e + c] = joined_sum(c);
+        }
+    }
+    if (cluster > 1) cluster_barrier();   // the others' shared memory has been read
+}
+
+// The clusters' sums: as many threads per expert as there are, each with every
+// groups-th cluster, joined in order.
+__global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const Balance p) {
+    __shared__ int32_t counts[kLossThreads];
+    __shared__ float sums[kLossThreads];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int e = p.experts, t = threadIdx.x;
+    const int per = (e + 31) / 32 * 32, groups = kLossThreads / per;   // (whole warps read neighbouring experts)
+    const int c = t % per, g = t / per;
+    int32_t count[1] = {0}, rows = 0;
+    float sum[1] = {0.f};
+    if (c < e && g < groups) {
+#pragma unroll 8
+        for (int j = g; j < p.parts; j += groups) {
+            count[0] += p.partial_c[static_cast<int64_t>(j) * (e + 1) + c];
+            sum[0] += p.partial_p[static_cast<int64_t>(j) * e + c];
+        }
+    }
+    for (int j = t & 31; j < p.parts; j += 32) rows += p.partial_c[static_cast<int64_t>(j) * (e + 1) + e];
+    rows = group_sum<32>(rows);
+    counts[t] = count[0];
+    sums[t] = sum[0];
+    __syncthreads();
+    count[0] = 0;
+    sum[0] = 0.f;
+    if (t < e)
+        for (int i = 0; i < groups; ++i) {
+            count[0] += counts[i * per + t];
+            sum[0] += sums[i * per + t];
+        }
+    write_loss<1, kLossThreads / 32>(p, count, sum, rows);
+}
+
+template <typename T, int L, int U, bool VEC>
+__global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalanceBwd p) {
+    constexpr int N = 4 * U, kGroups = 32 / L;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = p.experts;
+    const int l = lane % L, group = lane / L;
+    int32_t slots = 0;
+    float f[N], a[N], d[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int c = column<L, U>(l, i);
+        const int32_t n = c < e ? __ldg(p.counts + c) : 0;
+        slots += n;
+        f[i] = static_cast<float>(n);
+    }
+    slots = group_sum<L>(slots);
     const int32_t used = __ldg(p.used);
     const float per_slot = slots > 0 ? 1.f / static_cast<float>(slots) : 0.f;
     const float scale = used > 0 ? __ldg(p.dloss) * p.coef * static_cast<float>(e) / static_cast<float>(used) : 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) f[v] *= per_slot;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp; row < p.rows; row += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const float lse = __ldg(p.lse + row);
-        const bool part = !isinf(lse);
-        const T* x = static_cast<const T*>(p.X) + row * p.ldx;
-        const T* dr = p.dR ? static_cast<const T*>(p.dR) + row * p.lddr : nullptr;
-        T* dx = static_cast<T*>(p.dX) + row * p.lddx;
-        float a[V], d[V];
+    for (int i = 0; i < N; ++i) f[i] *= per_slot;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kGroups;
+    for (int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kGroups; first < p.rows; first += step) {
+        const int64_t row = first + group;
+        const bool mine = row < p.rows;
+        const float lse = mine ? __ldg(p.lse + row) : kInf;
+        const bool part = !isinf(lse);   // not padding, nor a row without any p
+        if (mine) {
+            load_row<T, L, U, VEC>(static_cast<const T*>(p.X) + row * p.ldx, l, e, -kInf, a);
+            if (p.dR) load_row<T, L, U, VEC>(static_cast<const T*>(p.dR) + row * p.lddr, l, e, 0.f, d);
+        }
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = lane + 32 * v;
-            a[v] = part && c < e ? to_f32(x[c]) : -__int_as_float(0x7f800000);
-            d[v] = dr && c < e ? to_f32(dr[c]) : 0.f;
+        for (int i = 0; i < N; ++i) {
+            if (!mine) a[i] = -kInf;
+            if (!mine || !p.dR) d[i] = 0.f;
         }
         // p is formed from the row again: exp(x - lse) would carry lse's rounding
         float base, sum, mix = 0.f;
-        const float inv = exponentials<V>(a, base, sum);
+        const float inv = exponentials<L, N>(a, base, sum);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            a[v] *= inv;
-            if (lane + 32 * v < e) mix = fmaf(a[v], f[v], mix);
+        for (int i = 0; i < N; ++i) {
+            a[i] *= inv;
+            mix = fmaf(a[i], f[i], mix);   // (past the row both are zero)
         }
-        mix = warp_sum(mix);
+        mix = group_sum<L>(mix);
+        if (!mine) continue;
+        if (part)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (lane + 32 * v < e) from_f32(part ? fmaf(scale * a[v], f[v] - mix, d[v]) : d[v], dx + lane + 32 * v);
+            for (int i = 0; i < N; ++i) d[i] = fmaf(scale * a[i], f[i] - mix, d[i]);
+        T* dx = static_cast<T*>(p.dX) + row * p.lddx;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = 4 * (l + L * u);
+            if constexpr (VEC) {
+                if (c < e) {
+                    if constexpr (sizeof(T) == 4)
+                        *reinterpret_cast<float4*>(dx + c) = make_float4(d[4 * u], d[4 * u + 1], d[4 * u + 2], d[4 * u + 3]);
+                    else
+                        *reinterpret_cast<uint2*>(dx + c) = make_uint2(bf16x2(d[4 * u], d[4 * u + 1]), bf16x2(d[4 * u + 2], d[4 * u + 3]));
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    if (c + t < e) from_f32(d[4 * u + t], dx + c + t);
+            }
+        }
     }
 }
 
-int columns_per_lane(int experts) {
-    int v = 1;
-    while (32 * v < experts) v *= 2;
-    return v;
+int lanes_of(int experts) {
+    int l = 1;
+    while (l < 32 && 4 * l < experts) l *= 2;
+    return l;
+}
+int rows_per_turn(int experts) { return kWarps * 32 / lanes_of(experts); }   // of a CTA
+
+bool takes_fours(const void* p, int64_t ld, int es, int experts) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(4 * es) == 0 && ld % 4 == 0 && experts % 4 == 0);
 }
 
-template <typename T>
+// f(L, U as integral constants)
+template <typename F>
+cudaError_t by_experts(int experts, F f) {
+#define GEMM_LANES(L, U) return f(std::integral_constant<int, L>{}, std::integral_constant<int, U>{});
+    switch (lanes_of(experts)) {
+        case 1: GEMM_LANES(1, 1)
+        case 2: GEMM_LANES(2, 1)
+        case 4: GEMM_LANES(4, 1)
+        case 8: GEMM_LANES(8, 1)
+        case 16: GEMM_LANES(16, 1)
+        default: break;
+    }
+    if (experts <= 128) GEMM_LANES(32, 1)
+    if (experts <= 256) GEMM_LANES(32, 2)
+    if (experts <= 512) GEMM_LANES(32, 4)
+    GEMM_LANES(32, 8)
+#undef GEMM_LANES
+}
+
+int cluster_of(const Balance& a) { return a.rows <= 2 * static_cast<int64_t>(rows_per_turn(a.experts)) ? 1 : kCluster; }
+
+template <typename T, bool VEC>
 cudaError_t rows_launch(const Balance& a, cudaStream_t stream) {
-    const size_t smem = static_cast<size_t>(a.experts + 1 + kWarps * a.experts) * 4;   // at most 37 KB
-    auto go = [&](auto kern) { return launch_chained(kern, dim3(static_cast<unsigned>(a.parts)), kThreads, smem, stream, a); };
-    switch (columns_per_lane(a.experts)) {
-        case 1: return go(balance_rows_kernel<T, 1>);
-        case 2: return go(balance_rows_kernel<T, 2>);
-        case 4: return go(balance_rows_kernel<T, 4>);
-        case 8: return go(balance_rows_kernel<T, 8>);
-        case 16: return go(balance_rows_kernel<T, 16>);
-        default: return go(balance_rows_kernel<T, 32>);
-    }
+    return by_experts(a.experts, [&](auto L, auto U) -> cudaError_t {
+        const auto kern = balance_rows_kernel<T, decltype(L)::value, decltype(U)::value, VEC>;
+        const size_t smem = static_cast<size_t>(a.experts + 1 + kWarps * a.experts) * 4;   // at most 68 KB
+        const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), (GEMM_BALANCE_MAX_EXPERTS * (kWarps + 1) + 1) * 4, false);
+        if (e != cudaSuccess) return e;
+        int cluster = cluster_of(a);
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof(cfg));
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(a.parts * cluster), 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        const cudaError_t r = cudaLaunchKernelEx(&cfg, kern, a, cluster);
+        return r != cudaSuccess ? r : cudaGetLastError();
+    });
 }
 
-template <typename T>
+template <typename T, bool VEC>
 cudaError_t bwd_launch(const BalanceBwd& a, cudaStream_t stream) {
-    const int64_t blocks = (a.rows + kWarps - 1) / kWarps, most = 8 * static_cast<int64_t>(a.num_sms);
-    auto go = [&](auto kern) {
-        return launch_chained(kern, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), kThreads, 0, stream, a);
-    };
-    switch (columns_per_lane(a.experts)) {
-        case 1: return go(balance_bwd_kernel<T, 1>);
-        case 2: return go(balance_bwd_kernel<T, 2>);
-        case 4: return go(balance_bwd_kernel<T, 4>);
-        case 8: return go(balance_bwd_kernel<T, 8>);
-        case 16: return go(balance_bwd_kernel<T, 16>);
-        default: return go(balance_bwd_kernel<T, 32>);
-    }
+    const int64_t turn = rows_per_turn(a.experts);
+    const int64_t blocks = (a.rows + turn - 1) / turn, most = 8 * static_cast<int64_t>(a.num_sms);
+    return by_experts(a.experts, [&](auto L, auto U) {
+        return launch_chained(balance_bwd_kernel<T, decltype(L)::value, decltype(U)::value, VEC>,
+                              dim3(static_cast<unsigned>(blocks < most ? blocks : most)), kThreads, 0, stream, a);
+    });
 }
 
 }  // namespace
 
+// Clusters of the first kernel: one for batches of a few turns, else as many
+// as run at once.  A cluster's CTAs lie in one GPC, so that not every SM is
+// full: of two CTAs of 512 threads per SM 32 such clusters run at once and not
+// 38, and the rest started only as those ended (65536 x 256: 48 us).
 int balance_parts(const Balance& a) {
-    const int64_t blocks = (a.rows + kWarps - 1) / kWarps, most = a.num_sms;
-    return static_cast<int>(blocks < most ? blocks : most);
+    const int64_t turn = static_cast<int64_t>(kCluster) * rows_per_turn(a.experts);
+    if (a.rows <= kFewTurns * turn) return 1;
+    const int64_t most = 7 * static_cast<int64_t>(a.num_sms) / (2 * kCluster), parts = (a.rows + turn - 1) / turn;
+    return static_cast<int>(parts < most ? parts : most);
 }
 
 cudaError_t launch_balance(const Balance& a, cudaStream_t stream, int* launches) {
     *launches = 0;
-    cudaError_t e = a.x_type == GEMM_DTYPE_BF16 ? rows_launch<__nv_bfloat16>(a, stream) : rows_launch<float>(a, stream);
+    const bool bf = a.x_type == GEMM_DTYPE_BF16, vec = takes_fours(a.X, a.ldx, bf ? 2 : 4, a.experts);
+    cudaError_t e = bf ? (vec ? rows_launch<__nv_bfloat16, true>(a, stream) : rows_launch<__nv_bfloat16, false>(a, stream))
+                       : (vec ? rows_launch<float, true>(a, stream) : rows_launch<float, false>(a, stream));
     if (e != cudaSuccess) return e;
     ++*launches;
-    e = launch_chained(balance_loss_kernel, dim3(1), static_cast<unsigned>((a.experts + 31) / 32 * 32), 0, stream, a);
+    if (a.parts == 1) return cudaSuccess;
+    e = launch_chained(balance_loss_kernel, dim3(1), kLossThreads, 0, stream, a);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
 
 cudaError_t launch_balance_bwd(const BalanceBwd& a, cudaStream_t stream) {
-    return a.x_type == GEMM_DTYPE_BF16 ? bwd_launch<__nv_bfloat16>(a, stream) : bwd_launch<float>(a, stream);
+    const bool bf = a.x_type == GEMM_DTYPE_BF16;
+    const int es = bf ? 2 : 4;
+    const bool vec = takes_fours(a.X, a.ldx, es, a.experts) && takes_fours(a.dR, a.lddr, es, a.experts) &&
+                     takes_fours(a.dX, a.lddx, es, a.experts);
+    return bf ? (vec ? bwd_launch<__nv_bfloat16, true>(a, stream) : bwd_launch<__nv_bfloat16, false>(a, stream))
+              : (vec ? bwd_launch<float, true>(a, stream) : bwd_launch<float, false>(a, stream));
 }
 
 }  // namespace gemm

@@ -96,8 +96,8 @@ struct Balance {
     int32_t *counts, *offsets, *used;
     float *lse, *probs, *loss;
     float* partial_p;     // parts x experts
-    int32_t* partial_c;   // parts x (experts + 1): counts, then the used rows
-    int parts;
+    int32_t* partial_c;   // parts x (experts + 1): counts, and behind them the used rows
+    int parts;            // clusters of CTAs; with more than one, scratch for their sums
     int num_sms;
 };
 int balance_parts(const Balance& a);

@@ -335,10 +335,14 @@ gemm_status gemm_balance(const void* X, int64_t ldx, int32_t x_type, int64_t row
     a.num_sms = ctx.num_sms;
     a.parts = balance_parts(a);
     Scratch scratch(ctx.pool, s);
-    const int64_t sums = static_cast<int64_t>(a.parts) * experts;
-    a.partial_p = static_cast<float*>(scratch.take(4 * (2 * sums + a.parts)));
-    if (!a.partial_p) return GEMM_ERR_CUDA;
-    a.partial_c = reinterpret_cast<int32_t*>(a.partial_p + sums);
+    a.partial_p = nullptr;
+    a.partial_c = nullptr;
+    if (a.parts > 1) {
+        const int64_t sums = static_cast<int64_t>(a.parts) * experts;
+        a.partial_p = static_cast<float*>(scratch.take(4 * (2 * sums + a.parts)));
+        if (!a.partial_p) return GEMM_ERR_CUDA;
+        a.partial_c = reinterpret_cast<int32_t*>(a.partial_p + sums);
+    }
     int launches = 0;
     const gemm_status r = staged([&] { return launch_balance(a, s, &launches); }, s);
     for (int i = 1; r == GEMM_OK && i < launches; ++i) trace_launch(GEMM_KERNEL_STAGE);
