@@ -10,8 +10,22 @@ __device__ __forceinline__ float rcp_approx(float x) {   // within one unit in t
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// exp(x) within (2 + 1.16 |x|) 2^-23 of itself (the product's rounding, and two
+// units of ex2); below 2^-126 it is 0.  Without ftz each call carries the
+// scaling of denormal results, four instructions more.
+__device__ __forceinline__ float exp_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950409f));
+    return r;
+}
+// log(x) of a normal x.
+__device__ __forceinline__ float log_approx(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r * 0.69314718056f;
+}
 // 1 / (1 + exp(-x)): no cancellation on either side, 0 and 1 at the infinities.
-__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + __expf(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + exp_approx(-x)); }
 
 constexpr float kGeluTanhTwice = 1.5957691216f;    // 2 sqrt(2 / pi)
 constexpr float kGeluTanhCube = 0.044715f;
@@ -24,7 +38,7 @@ constexpr float kNormalPeak = 0.39894228040f;      // 1 / sqrt(2 pi)
 // its digits (1 + erf would cancel there).  erfcf costs six times as much.
 __device__ __forceinline__ float normal_tail(float v, float& e) {
     const float t = rcp_approx(fmaf(fabsf(v), 0.30052038f, 1.f));   // 0.425 / sqrt(2)
-    e = __expf(-0.5f * v * v);
+    e = exp_approx(-0.5f * v * v);
     float q = 0.0688852072f;
     q = fmaf(q, t, -0.3024713099f);
     q = fmaf(q, t, 0.3894520700f);

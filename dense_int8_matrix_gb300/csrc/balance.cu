@@ -5,13 +5,15 @@
 //   dx = dr + dloss * coef * E / T * p * (f - sum(f * p))
 //
 // Bound by DRAM: the logits are read once by each pass.  L lanes (as many as
-// have four columns each, 32 at most) hold a row, so that a warp takes 32 / L
+// have sixteen columns each, 32 at most) hold a row, so that a warp takes 32 / L
 // rows at once, whatever the number of experts, and a lane has the same columns
-// of every row: its sums of p stay in registers.  The next row is on its way
-// while one is worked on.  Sums are joined in a fixed order: rows of a lane, row
+// of every row: its sums of p stay with it.  (Four columns per lane leave the
+// same work per row to be done for fewer rows at once.)  The next row is on its
+// way while one is worked on.  Sums are joined in a fixed order: rows of a lane, row
 // groups of a warp, warps of a CTA, the eight CTAs of a cluster (through
 // distributed shared memory), and clusters by a second kernel.  Batches that
 // one cluster (or one CTA) takes in a few turns need no second kernel.
+#include <algorithm>
 #include <type_traits>
 
 #include "activation.cuh"
@@ -31,16 +33,17 @@ constexpr int kRowsPerSum = 32;   // rows added in a row before they join the ru
 constexpr int kFewTurns = 4;      // of rows, up to which one cluster takes a whole batch
 constexpr float kInf = __builtin_huge_valf();
 constexpr int kExpertsPerThread = GEMM_BALANCE_MAX_EXPERTS / kThreads;
-static_assert(kLossThreads >= GEMM_BALANCE_MAX_EXPERTS, "a thread per expert");
+constexpr int kMaxParts = 256;
+static_assert(kLossThreads >= GEMM_BALANCE_MAX_EXPERTS && kMaxParts <= kLossThreads && kLossThreads == 1024, "a thread per expert and per part");
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));   // (volatile: stays behind the barrier)
     return v;
 }
 __device__ __forceinline__ int32_t ld_cluster_i32(uint32_t addr) {
     int32_t v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
 
@@ -98,7 +101,7 @@ __device__ __forceinline__ float exponentials(float (&a)[N], float& base, float&
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        a[i] = __expf(a[i] - base);   // within (2 + 1.16 |a - base|) 2^-23 of itself: p a few units of fp32 off
+        a[i] = exp_approx(a[i] - base);
         sum += a[i];
     }
     sum = group_sum<L>(sum);
@@ -157,22 +160,24 @@ __device__ __forceinline__ void write_loss(const Balance& p, const int32_t (&cou
 }
 
 template <typename T, int L, int U, bool VEC>
-__global__ void __launch_bounds__(kThreads) balance_rows_kernel(const Balance p, int cluster) {
+__global__ void __launch_bounds__(kThreads, U == 8 ? 2 : 3) balance_rows_kernel(const Balance p, int cluster) {
     constexpr int N = 4 * U, kGroups = 32 / L;
-    constexpr bool kCountInRegisters = L <= 4;   // (few experts: shared counters would be fought over)
-    extern __shared__ int32_t shared[];          // counts[experts + 1] (the last one: used rows), sums[warps][experts]
+    constexpr bool kCountInRegisters = L == 1;   // (at most 16 experts: shared counters would be fought over)
+    // counts[experts + 1] (the last one: used rows), sums[warps][experts], running sums[N][threads]
+    extern __shared__ int32_t shared[];
     int32_t* hist = shared;
     float* sums = reinterpret_cast<float*>(shared + p.experts + 1);
+    float* total = sums + kWarps * p.experts + threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = p.experts;
     const int l = lane % L, group = lane / L;
     for (int i = threadIdx.x; i <= e; i += kThreads) hist[i] = 0;
     __syncthreads();
-    float total[N], part[N], x[2][N];
+    float part[N], x[2][N];
     int32_t slot[2], counted[kCountInRegisters ? N : 1], used_rows = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) total[i] = part[i] = 0.f;
+    for (int i = 0; i < N; ++i) total[i * kThreads] = part[i] = 0.f;
 #pragma unroll
     for (int32_t& c : counted) c = 0;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kGroups;
@@ -202,11 +207,7 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const Balance p,
             taken = taken || in;
             if constexpr (kCountInRegisters) {
 #pragma unroll
-                for (int j = 0; j < L; ++j) {
-                    const int32_t y = L == 1 ? s : __shfl_sync(0xffffffffu, s, (lane & ~(L - 1)) + j);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) counted[i] += y == column<L, U>(l, i) ? 1 : 0;
-                }
+                for (int i = 0; i < N; ++i) counted[i] += s == column<L, U>(l, i) ? 1 : 0;
             } else if (in) {
                 atomicAdd(hist + s, 1);
             }
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const Balance p,
         const bool used = ((votes >> (lane & ~(L - 1))) & (L == 32 ? 0xffffffffu : (1u << (L % 32)) - 1u)) != 0;
         float base, sum;
         const float inv = exponentials<L, N>(a, base, sum);
-        if (l == 0 && mine) p.lse[row] = used ? base + __logf(sum) : kInf;   // (sum is 1 to 1024, or 0, or NaN)
+        if (l == 0 && mine) p.lse[row] = used ? base + log_approx(sum) : kInf;   // (sum is 1 to 1024, or 0, or NaN)
         if (used) {   // (padding takes no part, whatever it holds)
             if (l == 0) ++used_rows;
 #pragma unroll
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const Balance p,
             pending = 0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                total[i] += part[i];
+                total[i * kThreads] += part[i];
                 part[i] = 0.f;
             }
         }
@@ -247,11 +248,11 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const Balance p,
     // the warp's row groups, then the CTA's warps
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        total[i] += part[i];
+        float v = total[i * kThreads] + part[i];
 #pragma unroll
-        for (int o = L; o < 32; o <<= 1) total[i] += __shfl_xor_sync(0xffffffffu, total[i], o);
+        for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         const int c = column<L, U>(l, i);
-        if (group == 0 && c < e) sums[warp * e + c] = total[i];
+        if (group == 0 && c < e) sums[warp * e + c] = v;
         if constexpr (kCountInRegisters) {
 #pragma unroll
             for (int o = L; o < 32; o <<= 1) counted[i] += __shfl_xor_sync(0xffffffffu, counted[i], o);
@@ -269,14 +270,22 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const Balance p,
     // the cluster's CTAs
     const uint32_t hist0 = smem_u32(hist), sums0 = smem_u32(sums);
     auto joined_count = [&](int c) {
-        int32_t v = 0;
-        for (int r = 0; r < cluster; ++r) v += ld_cluster_i32(peer_address(hist0 + 4 * c, r));
-        return v;
+        if (cluster == 1) return hist[c];
+        int32_t v[kCluster], all = 0;   // (asked for together: a remote read takes its time)
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) v[r] = ld_cluster_i32(peer_address(hist0 + 4 * c, r));
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) all += v[r];
+        return all;
     };
     auto joined_sum = [&](int c) {
-        float v = 0.f;
-        for (int r = 0; r < cluster; ++r) v += ld_cluster_f32(peer_address(sums0 + 4 * c, r));
-        return v;
+        if (cluster == 1) return sums[c];
+        float v[kCluster], all = 0.f;
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) v[r] = ld_cluster_f32(peer_address(sums0 + 4 * c, r));
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) all += v[r];
+        return all;
     };
     if (cluster > 1)
         cluster_barrier();
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) balance_rows_kernel(const Balance p,
 // The clusters' sums: as many threads per expert as there are, each with every
 // groups-th cluster, joined in order.
 __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const Balance p) {
-    __shared__ int32_t counts[kLossThreads];
+    __shared__ int32_t counts[kLossThreads], used[kLossThreads / 32];
     __shared__ float sums[kLossThreads];
     pdl_launch_dependents();
     pdl_wait();
@@ -323,18 +332,31 @@ __global__ void __launch_bounds__(kLossThreads) balance_loss_kernel(const Balanc
     const int c = t % per, g = t / per;
     int32_t count[1] = {0}, rows = 0;
     float sum[1] = {0.f};
+    if (t < p.parts) rows = p.partial_c[static_cast<int64_t>(t) * (e + 1) + e];   // (parts are at most kMaxParts)
     if (c < e && g < groups) {
-#pragma unroll 8
-        for (int j = g; j < p.parts; j += groups) {
-            count[0] += p.partial_c[static_cast<int64_t>(j) * (e + 1) + c];
-            sum[0] += p.partial_p[static_cast<int64_t>(j) * e + c];
+        constexpr int kLoads = 12;   // at a time: the latency of the L2 is what this kernel takes
+        for (int j = g; j < p.parts; j += kLoads * groups) {
+            int32_t n[kLoads];
+            float f[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int64_t part = j + i * groups;
+                n[i] = part < p.parts ? p.partial_c[part * (e + 1) + c] : 0;
+                f[i] = part < p.parts ? p.partial_p[part * e + c] : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                count[0] += n[i];
+                sum[0] += f[i];
+            }
         }
     }
-    for (int j = t & 31; j < p.parts; j += 32) rows += p.partial_c[static_cast<int64_t>(j) * (e + 1) + e];
-    rows = group_sum<32>(rows);
     counts[t] = count[0];
     sums[t] = sum[0];
+    rows = group_sum<32>(rows);
+    if ((t & 31) == 0) used[t >> 5] = rows;
     __syncthreads();
+    rows = group_sum<32>(used[t & 31]);
     count[0] = 0;
     sum[0] = 0.f;
     if (t < e)
@@ -415,12 +437,15 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalanceBwd 
     }
 }
 
-int lanes_of(int experts) {
+// Lanes of a row: sixteen columns each, or, for a batch of few rows, four (64
+// rows of 32 experts: 4.0 us with sixteen, 2.8 with four).
+int lanes_of(int experts, bool few) {
     int l = 1;
-    while (l < 32 && 4 * l < experts) l *= 2;
+    while (l < 32 && (few ? 4 : 16) * l < experts) l *= 2;
     return l;
 }
-int rows_per_turn(int experts) { return kWarps * 32 / lanes_of(experts); }   // of a CTA
+int rows_per_turn(int experts, bool few) { return kWarps * 32 / lanes_of(experts, few); }   // of a CTA
+bool few_rows(int64_t rows, int experts) { return rows <= static_cast<int64_t>(kFewTurns) * kCluster * rows_per_turn(experts, true); }
 
 bool takes_fours(const void* p, int64_t ld, int es, int experts) {
     return !p || (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(4 * es) == 0 && ld % 4 == 0 && experts % 4 == 0);
@@ -428,31 +453,44 @@ bool takes_fours(const void* p, int64_t ld, int es, int experts) {
 
 // f(L, U as integral constants)
 template <typename F>
-cudaError_t by_experts(int experts, F f) {
+cudaError_t by_experts(int experts, bool few, F f) {
 #define GEMM_LANES(L, U) return f(std::integral_constant<int, L>{}, std::integral_constant<int, U>{});
-    switch (lanes_of(experts)) {
-        case 1: GEMM_LANES(1, 1)
+    if (experts <= 4) GEMM_LANES(1, 1)
+    if (few && experts <= 256) switch (lanes_of(experts, true)) {
         case 2: GEMM_LANES(2, 1)
         case 4: GEMM_LANES(4, 1)
         case 8: GEMM_LANES(8, 1)
         case 16: GEMM_LANES(16, 1)
         default: break;
     }
-    if (experts <= 128) GEMM_LANES(32, 1)
-    if (experts <= 256) GEMM_LANES(32, 2)
+    if (few && experts <= 128) GEMM_LANES(32, 1)
+    if (few && experts <= 256) GEMM_LANES(32, 2)
+    if (experts <= 8) GEMM_LANES(1, 2)
+    switch (lanes_of(experts, false)) {
+        case 1: GEMM_LANES(1, 4)
+        case 2: GEMM_LANES(2, 4)
+        case 4: GEMM_LANES(4, 4)
+        case 8: GEMM_LANES(8, 4)
+        case 16: GEMM_LANES(16, 4)
+        default: break;
+    }
     if (experts <= 512) GEMM_LANES(32, 4)
     GEMM_LANES(32, 8)
 #undef GEMM_LANES
 }
 
-int cluster_of(const Balance& a) { return a.rows <= 2 * static_cast<int64_t>(rows_per_turn(a.experts)) ? 1 : kCluster; }
+int cluster_of(const Balance& a) {
+    return a.rows <= 2 * static_cast<int64_t>(rows_per_turn(a.experts, few_rows(a.rows, a.experts))) ? 1 : kCluster;
+}
 
 template <typename T, bool VEC>
 cudaError_t rows_launch(const Balance& a, cudaStream_t stream) {
-    return by_experts(a.experts, [&](auto L, auto U) -> cudaError_t {
+    return by_experts(a.experts, few_rows(a.rows, a.experts), [&](auto L, auto U) -> cudaError_t {
         const auto kern = balance_rows_kernel<T, decltype(L)::value, decltype(U)::value, VEC>;
-        const size_t smem = static_cast<size_t>(a.experts + 1 + kWarps * a.experts) * 4;   // at most 68 KB
-        const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), (GEMM_BALANCE_MAX_EXPERTS * (kWarps + 1) + 1) * 4, false);
+        constexpr int kRunning = 4 * decltype(U)::value * kThreads * 4;
+        const size_t smem = static_cast<size_t>(a.experts + 1 + kWarps * a.experts) * 4 + kRunning;   // at most 69 KB
+        const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern),
+                                                (GEMM_BALANCE_MAX_EXPERTS * (kWarps + 1) + 1) * 4 + kRunning, false);
         if (e != cudaSuccess) return e;
         int cluster = cluster_of(a);
         cudaLaunchConfig_t cfg;
@@ -477,9 +515,10 @@ cudaError_t rows_launch(const Balance& a, cudaStream_t stream) {
 
 template <typename T, bool VEC>
 cudaError_t bwd_launch(const BalanceBwd& a, cudaStream_t stream) {
-    const int64_t turn = rows_per_turn(a.experts);
+    const bool few = few_rows(a.rows, a.experts);
+    const int64_t turn = rows_per_turn(a.experts, few);
     const int64_t blocks = (a.rows + turn - 1) / turn, most = 8 * static_cast<int64_t>(a.num_sms);
-    return by_experts(a.experts, [&](auto L, auto U) {
+    return by_experts(a.experts, few, [&](auto L, auto U) {
         return launch_chained(balance_bwd_kernel<T, decltype(L)::value, decltype(U)::value, VEC>,
                               dim3(static_cast<unsigned>(blocks < most ? blocks : most)), kThreads, 0, stream, a);
     });
@@ -489,13 +528,15 @@ cudaError_t bwd_launch(const BalanceBwd& a, cudaStream_t stream) {
 
 // Clusters of the first kernel: one for batches of a few turns, else as many
 // as run at once.  A cluster's CTAs lie in one GPC, so that not every SM is
-// full: of two CTAs of 512 threads per SM 32 such clusters run at once and not
-// 38, and the rest started only as those ended (65536 x 256: 48 us).
+// full: at three CTAs per SM (two beyond 512 experts) 48 (32) run at once, and
+// further ones would start only as those end (65536 x 256: 25.5 us with 48, 37 with
+// 54; 16384 x 1024 30.6 with 32, 41.5 with 40).
 int balance_parts(const Balance& a) {
-    const int64_t turn = static_cast<int64_t>(kCluster) * rows_per_turn(a.experts);
+    const bool few = few_rows(a.rows, a.experts);
+    const int64_t turn = static_cast<int64_t>(kCluster) * rows_per_turn(a.experts, few);
     if (a.rows <= kFewTurns * turn) return 1;
-    const int64_t most = 7 * static_cast<int64_t>(a.num_sms) / (2 * kCluster), parts = (a.rows + turn - 1) / turn;
-    return static_cast<int>(parts < most ? parts : most);
+    const int64_t most = static_cast<int64_t>(a.experts <= 512 ? 48 : 32) * a.num_sms / 152, parts = (a.rows + turn - 1) / turn;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(parts, most), kMaxParts)));
 }
 
 cudaError_t launch_balance(const Balance& a, cudaStream_t stream, int* launches) {
