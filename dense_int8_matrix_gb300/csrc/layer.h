@@ -56,7 +56,7 @@ struct ActBwd {
 int act_bwd_parts(const ActBwd& a);
 cudaError_t launch_act_bwd(const ActBwd& a, cudaStream_t stream);
 
-// ---- layer norm (layer_norm.cu) ------------------------------------------------
+// ---- layer norm (layer_norm.cu, layer_norm_bwd.cu) ------------------------------------------------
 struct LayerNormFwd {
     const void *X, *R;
     const float *W, *bias;
@@ -66,6 +66,7 @@ struct LayerNormFwd {
     void *H, *Y;
     float *mean, *rstd;
     int num_sms;
+    int* err;            // device error word
 };
 cudaError_t launch_layer_norm_fwd(const LayerNormFwd& a, cudaStream_t stream);
 

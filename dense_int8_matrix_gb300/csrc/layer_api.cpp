@@ -247,6 +247,7 @@ gemm_status gemm_layer_norm(const void* X, int64_t ldx, const void* R, int64_t l
     a.mean = mean;
     a.rstd = rstd;
     a.num_sms = ctx.num_sms;
+    a.err = ctx.err_word;
     return staged([&] { return launch_layer_norm_fwd(a, s); }, s);
 }
 

@@ -1,22 +1,24 @@
-// Layer norm with the residual's addition, and its gradient.
+// Layer norm with the residual's addition.
 //
 //   h = x + r,  mean = mean(h),  rstd = 1 / sqrt(mean((h - mean)^2) + eps),  y = (h - mean) * rstd * w + b
-//   dx = dr + rstd * (g - mean(g) - xhat * mean(g * xhat)),  g = dy * w, xhat = (h - mean) * rstd
-//   dw = sum over rows of dy * xhat,  db = sum over rows of dy
 //
-// Both are bound by DRAM.  The variance is taken of h - mean, not of h^2: the
-// row is in registers, so the second pass costs no memory traffic, and a mean
-// far from zero cancels nothing.
-#include "f8.cuh"
+// Bound by DRAM.  The variance is taken of h - mean, not of h^2: the row is in
+// registers, so the second pass costs no memory traffic, and a mean far from
+// zero cancels nothing.  Rows come through a ring of bulk copies where there are
+// many and they are longer, or not aligned; short aligned rows take a warp, or part
+// of one, each; few rows a CTA each.
+#include <algorithm>
+
 #include "internal.h"
 #include "layer.h"
-#include "ptx.cuh"
+#include "row_ring.cuh"
 
 namespace gemm {
 
 namespace {
 
-// Sum over the CTA; `red` is used by this call alone.
+// Sum over the CTA; `red` is used by this call alone until the CTA's next
+// barrier.
 __device__ __forceinline__ float cta_sum(float v, float* red) {
     v = warp_sum(v);
     const int warps = blockDim.x >> 5;
@@ -25,57 +27,88 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
     __syncthreads();
     return warp_sum((threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f);
 }
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
 
-// One CTA per row, or (WARP, rows of at most 768 elements) a warp per row and
-// kWarpRows rows per CTA.  The row stays in registers: V vectors of eight values
-// per thread, vector v of thread t at column 8 * (v * threads + t).  Mean and
-// variance are taken of h as it is stored.
-constexpr int kWarpRows = 8;
+// h = x + r as stored, in place of x; the sum of its eight values.
+template <typename T>
+__device__ __forceinline__ void add_to(Vec8<T>& x, const Vec8<T>& r) {
+    float a[8], b[8];
+    x.get(a);
+    r.get(b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] += b[i];
+    x.set(a);
+}
+template <typename T>
+__device__ __forceinline__ float sum8(const Vec8<T>& x) {
+    float a[8], s = 0.f;
+    x.get(a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += a[i];
+    return s;
+}
+// Sum of (h - mean)^2 over the eight values that lie in the row.
+template <typename T>
+__device__ __forceinline__ float squares8(const Vec8<T>& x, float mean, int64_t c, int64_t d) {
+    float a[8], s = 0.f;
+    x.get(a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float e = c + i < d ? a[i] - mean : 0.f;
+        s += e * e;
+    }
+    return s;
+}
+template <typename T, typename TY>
+__device__ __forceinline__ Vec8<TY> normed(const Vec8<T>& x, float mean, float rstd, const float (&w)[8], const float (&b)[8]) {
+    float a[8];
+    x.get(a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = fmaf((a[i] - mean) * rstd, w[i], b[i]);
+    Vec8<TY> y;
+    y.set(a);
+    return y;
+}
+__device__ __forceinline__ void load_wb(const LayerNormFwd& p, int64_t c, bool wvec, bool bvec, float (&w)[8], float (&b)[8]) {
+    load8_f32(p.W, c, p.d, wvec, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = 0.f;
+    if (p.bias) load8_f32(p.bias, c, p.d, bvec, b);
+}
+
+// One CTA per row, or (WARP) a warp per row: V vectors of eight values per
+// thread, vector v of thread t at column 8 * (v * threads + t).
+constexpr int kWarpThreads = 256;
 template <typename T, typename TY, int V, bool VEC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) layer_norm_fwd_kernel(const LayerNormFwd p, bool wvec, bool bvec) {
+__global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) layer_norm_fwd_kernel(const LayerNormFwd p, bool wvec, bool bvec) {
     __shared__ float red[2][32];
     pdl_launch_dependents();
     pdl_wait();
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
-    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (kWarpThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     if (WARP && row >= p.rows) return;   // whole warps, and no barrier of the CTA
-    const T* x = static_cast<const T*>(p.X) + row * p.ldx;
-    const T* r = p.R ? static_cast<const T*>(p.R) + row * p.ldr : nullptr;
     auto column = [&](int v) { return 8 * (static_cast<int64_t>(v) * nt + t); };
     Vec8<T> h[V];
     float sum = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        h[v] = load8<VEC>(x, column(v), p.d);
-        if (r) {
-            float a[8], b[8];
-            h[v].get(a);
-            load8<VEC>(r, column(v), p.d).get(b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] += b[i];
-            h[v].set(a);
-        }
+        h[v] = load8<VEC>(static_cast<const T*>(p.X) + row * p.ldx, column(v), p.d);
+        if (p.R) add_to(h[v], load8<VEC>(static_cast<const T*>(p.R) + row * p.ldr, column(v), p.d));
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         if (p.H) store8<VEC>(static_cast<T*>(p.H) + row * p.ldh, column(v), p.d, h[v]);
-        float a[8];
-        h[v].get(a);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += a[i];   // (columns past the row are zero)
+        sum += sum8(h[v]);   // (columns past the row are zero)
     }
     const float mean = (WARP ? warp_sum(sum) : cta_sum(sum, red[0])) / static_cast<float>(p.d);
     float ss = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float a[8];
-        h[v].get(a);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float c = column(v) + i < p.d ? a[i] - mean : 0.f;
-            ss += c * c;
-        }
-    }
+    for (int v = 0; v < V; ++v) ss += squares8(h[v], mean, column(v), p.d);
     ss = WARP ? warp_sum(ss) : cta_sum(ss, red[1]);
     const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
     if (t == 0) {
@@ -84,173 +117,427 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) layer_norm_fwd_k
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float a[8], w[8], b[8];
-        h[v].get(a);
-        load8_f32(p.W, column(v), p.d, wvec, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = 0.f;
-        if (p.bias) load8_f32(p.bias, column(v), p.d, bvec, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = fmaf((a[i] - mean) * rstd, w[i], b[i]);
-        Vec8<TY> y;
-        y.set(a);
-        store8<VEC>(static_cast<TY*>(p.Y) + row * p.ldy, column(v), p.d, y);
+        float w[8], b[8];
+        load_wb(p, column(v), wvec, bvec, w, b);
+        store8<VEC>(static_cast<TY*>(p.Y) + row * p.ldy, column(v), p.d, normed<T, TY>(h[v], mean, rstd, w, b));
     }
 }
 
-// dx: one CTA per row, the row in registers.
-template <typename T, typename TY, int V, bool VEC>
-__global__ void __launch_bounds__(1024) layer_norm_dx_kernel(const LayerNormBwd p, bool wvec) {
-    __shared__ float red[2][32];
+// Short aligned rows: L lanes hold a row (eight values each), 32 / L rows per
+// warp, w and b in registers, and the next rows on their way while these are
+// worked on.
+template <typename T, typename TY, int L>
+__global__ void __launch_bounds__(kWarpThreads) layer_norm_fwd_warp_kernel(const LayerNormFwd p, bool wvec, bool bvec) {
+    constexpr int kRows = 32 / L, V = 1;
+    constexpr bool VEC = true;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t row = blockIdx.x;
-    auto column = [&](int v) { return 8 * (static_cast<int64_t>(v) * blockDim.x + threadIdx.x); };
-    const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
-    Vec8<TY> dy[V];
-    Vec8<T> h[V], dr[V];
-    float sum = 0.f, dot = 0.f;
+    const int lane = threadIdx.x & 31, l = lane % L, group = lane / L;
+    auto column = [&](int v) { return 8 * (v * L + l); };
+    float w[V][8], b[V][8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        dy[v] = load8<VEC>(static_cast<const TY*>(p.dY) + row * p.lddy, column(v), p.d);
-        h[v] = load8<VEC>(static_cast<const T*>(p.H) + row * p.ldh, column(v), p.d);
-        if (p.dR)
-            dr[v] = load8<VEC>(static_cast<const T*>(p.dR) + row * p.lddr, column(v), p.d);
-        else
-            dr[v].zero();
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float w[8], a[8], b[8];
-        load8_f32(p.W, column(v), p.d, wvec, w);
-        dy[v].get(a);
-        h[v].get(b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {   // (past the row dy and w are zero)
-            const float g = a[i] * w[i];
-            sum += g;
-            dot += column(v) + i < p.d ? g * ((b[i] - mean) * rstd) : 0.f;
-        }
-    }
+    for (int v = 0; v < V; ++v) load_wb(p, column(v), wvec, bvec, w[v], b[v]);
     const float inv_d = 1.f / static_cast<float>(p.d);
-    const float mg = cta_sum(sum, red[0]) * inv_d, mx = cta_sum(dot, red[1]) * inv_d;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kWarpThreads / 32) * kRows;
+    int64_t first = (static_cast<int64_t>(blockIdx.x) * (kWarpThreads / 32) + (threadIdx.x >> 5)) * kRows;
+    Vec8<T> x[V], r[V];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float w[8], a[8], b[8], o[8];
-        load8_f32(p.W, column(v), p.d, wvec, w);
-        dy[v].get(a);
-        h[v].get(b);
-        dr[v].get(o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float xhat = (b[i] - mean) * rstd;
-            o[i] = fmaf(rstd, fmaf(-xhat, mx, fmaf(a[i], w[i], -mg)), o[i]);
+        for (int v = 0; v < V; ++v) {
+            x[v].zero();
+            r[v].zero();
+            if (row < p.rows) {
+                x[v] = load8<VEC>(static_cast<const T*>(p.X) + row * p.ldx, column(v), p.d);
+                if (p.R) r[v] = load8<VEC>(static_cast<const T*>(p.R) + row * p.ldr, column(v), p.d);
+            }
         }
-        Vec8<T> out;
-        out.set(o);
-        store8<VEC>(static_cast<T*>(p.dX) + row * p.lddx, column(v), p.d, out);
+    };
+    fetch(first + group);
+    for (; first < p.rows; first += step) {   // (the whole warp alike)
+        const int64_t row = first + group;
+        const bool mine = row < p.rows;
+        Vec8<T> h[V];
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            h[v] = x[v];
+            if (p.R) add_to(h[v], r[v]);
+            sum += sum8(h[v]);
+        }
+        fetch(row + step);
+        const float mean = lanes_sum<L>(sum) * inv_d;
+        float ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) ss += squares8(h[v], mean, column(v), p.d);
+        const float rstd = 1.f / sqrtf(lanes_sum<L>(ss) * inv_d + p.eps);
+        if (!mine) continue;
+        if (l == 0) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (p.H) store8<VEC>(static_cast<T*>(p.H) + row * p.ldh, column(v), p.d, h[v]);
+            store8<VEC>(static_cast<TY*>(p.Y) + row * p.ldy, column(v), p.d, normed<T, TY>(h[v], mean, rstd, w[v], b[v]));
+        }
     }
 }
 
-// dw and db: a thread takes eight columns of a range of rows, `lanes`
-// neighbouring threads the columns of a row; a CTA's sums are joined in shared
-// memory in a fixed order.
-constexpr int kColThreads = 256;
-constexpr int kColRows = 4;   // rows in flight per thread
-template <typename T, typename TY, bool VEC>
-__global__ void __launch_bounds__(kColThreads) layer_norm_dw_kernel(const LayerNormBwd p, int lanes) {
-    __shared__ float red[2][kColThreads * 8];
+// What the ring kernels begin with: the team's ring, its first chunks on their
+// way.
+template <typename T>
+__device__ __forceinline__ void start_ring(ChunkRing& ring, const LayerNormFwd& p, const RingShape& shape, const Team& team,
+                                           uint32_t ring_at, uint64_t* bars, int64_t first) {
+    ring.set(0, p.X, p.ldx, sizeof(T), p.d);
+    ring.set(1, p.R, p.ldr, sizeof(T), p.d);
+    ring.set(2, nullptr, 0, 0, 0);
+    ring.ring = ring_at;
+    if (team.thread == 0) {
+        for (int s = 0; s < shape.slots; ++s) mbar_init(smem_u32(bars + s), 1);
+        fence_barrier_init();
+        pdl_wait();
+        for (int s = 0; s < shape.slots; ++s) ring.fill(first + s * ring.by, s);
+    }
+}
+
+// Longer aligned rows, many of them: two rows per team from its ring, V vectors
+// of eight values per thread and row.
+constexpr int kPair = 2;
+template <typename T, typename TY, int V>
+__global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_ring_kernel(const LayerNormFwd p, const RingShape shape, bool wvec, bool bvec) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float2 red[2][kRingThreads / 32];
+    __shared__ __align__(8) uint64_t bars[kRingThreads / 32][ChunkRing::kSlots];
+    __shared__ uint32_t abort_flag;
+    const int d = static_cast<int>(p.d), lane = threadIdx.x & 31;
+    const Team team(shape.team);
+    const int64_t first = blockIdx.x + static_cast<int64_t>(team.id) * gridDim.x;
+    ChunkRing ring;
+    ring.init(p.rows, kPair, false, shape.slots, static_cast<int64_t>(gridDim.x) * shape.teams, smem_u32(bars[team.id]));
     pdl_launch_dependents();
+    if (threadIdx.x == 0) abort_flag = 0u;
+    const int64_t room = shape.smem / shape.teams;
+    start_ring<T>(ring, p, shape, team, smem_u32(smem) + team.id * static_cast<uint32_t>(room), bars[team.id], first);
     pdl_wait();
-    const int groups = kColThreads / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    const int64_t c = (static_cast<int64_t>(blockIdx.x) * lanes + lane) * 8;
-    const int64_t per = (p.rows + p.parts - 1) / p.parts;
-    const int64_t lo = per * blockIdx.y, hi = lo + per < p.rows ? lo + per : p.rows;
-    float dw[8], db[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.f;
-    for (int64_t r0 = lo + group; r0 < hi; r0 += static_cast<int64_t>(kColRows) * groups) {
-        Vec8<TY> dy[kColRows];
-        Vec8<T> h[kColRows];
-        float mean[kColRows], rstd[kColRows];
-#pragma unroll
-        for (int k = 0; k < kColRows; ++k) {
-            const int64_t r = r0 + static_cast<int64_t>(k) * groups;
-            dy[k].zero();
-            h[k].zero();
-            mean[k] = rstd[k] = 0.f;
-            if (r < hi && c < p.d) {
-                dy[k] = load8<VEC>(static_cast<const TY*>(p.dY) + r * p.lddy, c, p.d);
-                h[k] = load8<VEC>(static_cast<const T*>(p.H) + r * p.ldh, c, p.d);
-                mean[k] = __ldg(p.mean + r);
-                rstd[k] = __ldg(p.rstd + r);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kColRows; ++k) {
-            float a[8], b[8];
-            dy[k].get(a);
-            h[k].get(b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dw[i] = fmaf(a[i], (b[i] - mean[k]) * rstd[k], dw[i]);
-                db[i] += a[i];
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        red[0][(group * lanes + lane) * 8 + i] = dw[i];
-        red[1][(group * lanes + lane) * 8 + i] = db[i];
-    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * lanes; i += kColThreads) {
-        const int which = i / (8 * lanes), j = i % (8 * lanes);
-        float* out = which == 0 ? p.dW : p.dbias;
-        if (!out) continue;
-        float v = red[which][j];
-        for (int g = 1; g < groups; ++g) v += red[which][g * lanes * 8 + j];
-        const int64_t col = static_cast<int64_t>(blockIdx.x) * lanes * 8 + j;
-        if (p.parts > 1) out = p.partial + (static_cast<int64_t>(which) * p.parts + blockIdx.y) * p.d;
-        if (col < p.d) out[col] = v;
+    const uint8_t* slots = smem + team.id * room;
+    auto column = [&](int v) { return 8 * (v * team.threads + team.thread); };
+    Pairs w[V], b[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float f[8], g[8];
+        load_wb(p, column(v), wvec, bvec, f, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[v].p[i] = pair_of(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]));
+            b[v].p[i] = pair_of(__float_as_uint(g[2 * i]), __float_as_uint(g[2 * i + 1]));
+        }
     }
+    // the sums of both rows over the team
+    auto sums = [&](uint64_t x, uint64_t y, float2* at) {
+        float2 v = make_float2(warp_sum(sum_of(x)), warp_sum(sum_of(y)));
+        if (team.warps == 1) {
+            __syncwarp();
+            return v;
+        }
+        if (lane == 0) at[threadIdx.x >> 5] = v;
+        team.sync();
+        v = lane < team.warps ? at[team.id * team.warps + lane] : make_float2(0.f, 0.f);
+        return make_float2(warp_sum(v.x), warp_sum(v.y));
+    };
+    const float inv_d = 1.f / static_cast<float>(d);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int64_t c = first; c < ring.chunks; c += ring.by) {
+        // a wait that gives up is recorded; the rows are then wrong
+        wait_bounded(ring.full0 + 8u * s, ph, &abort_flag, p.err, kDevErrTimeoutEpilogue);
+        const int n = ring.rows_of(c);
+        const int64_t row = c * kPair;
+        Vec8<T> h[kPair][V];
+        uint64_t part[kPair] = {0, 0};
+#pragma unroll
+        for (int r = 0; r < kPair; ++r) {
+            if (r >= n) break;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (column(v) >= d) continue;
+                h[r][v].load(reinterpret_cast<const T*>(slots + ring.aligned_row(0, s, r)) + column(v));
+                Pairs x = pairs(h[r][v]);
+                if (p.R) {
+                    Vec8<T> res;
+                    res.load(reinterpret_cast<const T*>(slots + ring.aligned_row(1, s, r)) + column(v));
+                    const Pairs y = pairs(res);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x.p[i] = add2(x.p[i], y.p[i]);
+                    h[r][v] = vec<T>(x);
+                    x = pairs(h[r][v]);
+                }
+                if (p.H) h[r][v].store(static_cast<T*>(p.H) + (row + r) * p.ldh + column(v));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[r] = add2(part[r], x.p[i]);
+            }
+        }
+        const float2 total = sums(part[0], part[1], red[0]);
+        if (team.thread == 0) ring.fill(c + shape.slots * ring.by, s);   // the whole team has read the slot
+        const float mean[kPair] = {total.x * inv_d, total.y * inv_d};
+        part[0] = part[1] = 0;
+#pragma unroll
+        for (int r = 0; r < kPair; ++r) {
+            if (r >= n) break;
+            const uint64_t minus = both(-mean[r]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (column(v) >= d) continue;
+                const Pairs x = pairs(h[r][v]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t e = add2(x.p[i], minus);
+                    part[r] = fma2(e, e, part[r]);
+                }
+            }
+        }
+        const float2 ss = sums(part[0], part[1], red[1]);
+        const float rstd[kPair] = {1.f / sqrtf(ss.x * inv_d + p.eps), 1.f / sqrtf(ss.y * inv_d + p.eps)};
+#pragma unroll
+        for (int r = 0; r < kPair; ++r) {
+            if (r >= n) break;
+            if (team.thread == 0) {
+                if (p.mean) p.mean[row + r] = mean[r];
+                if (p.rstd) p.rstd[row + r] = rstd[r];
+            }
+            const uint64_t minus = both(-mean[r]), scale = both(rstd[r]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (column(v) >= d) continue;
+                Pairs x = pairs(h[r][v]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x.p[i] = fma2(mul2(add2(x.p[i], minus), scale), w[v].p[i], b[v].p[i]);
+                vec<TY>(x).store(static_cast<TY*>(p.Y) + (row + r) * p.ldy + column(v));
+            }
+        }
+        if (++s == shape.slots) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+}
+
+// Rows that are not aligned (or not of whole vectors): they come through the
+// ring as runs of bytes and leave through staging buffers the same way, and in
+// between each value is taken by itself, neighbouring lanes neighbouring values,
+// J values per thread and row.  Dense short rows: a warp per team, which takes
+// several rows at a time.
+template <typename T, typename TY, int J>
+__global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_odd_kernel(const LayerNormFwd p, const RingShape shape) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int kRows = rows_together(J);
+    __shared__ float red[2][kRingThreads / 32 * kRows];
+    __shared__ __align__(8) uint64_t bars[kRingThreads / 32][ChunkRing::kSlots];
+    __shared__ uint32_t abort_flag;
+    const int d = static_cast<int>(p.d), lane = threadIdx.x & 31;
+    const bool dense = shape.dense != 0;
+    const Team team(shape.team);
+    const int64_t begin = blockIdx.x + static_cast<int64_t>(team.id) * gridDim.x;
+    ChunkRing ring;
+    ring.init(p.rows, shape.per, dense, shape.slots, static_cast<int64_t>(gridDim.x) * shape.teams, smem_u32(bars[team.id]));
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) abort_flag = 0u;
+    const int64_t room = shape.smem / shape.teams;
+    uint8_t* slots = smem + team.id * room;
+    start_ring<T>(ring, p, shape, team, smem_u32(slots), bars[team.id], begin);
+    pdl_wait();
+    __syncthreads();
+    uint8_t* out = slots + shape.slots * ring.slot_bytes;
+    const uint32_t h_run = static_cast<uint32_t>(ChunkRing::run_place(p.d * sizeof(T))), y_run = static_cast<uint32_t>(ChunkRing::run_place(p.d * sizeof(TY)));
+    const uint32_t h_place = p.H ? static_cast<uint32_t>(ChunkRing::place(p.d * sizeof(T), shape.per, dense)) : 0u;
+    const uint32_t out_bytes = h_place + static_cast<uint32_t>(ChunkRing::place(p.d * sizeof(TY), shape.per, dense));
+    const int first = team.thread, stride = team.threads;
+    constexpr int P = J / 2;   // pairs of values, at 2 i and 2 i + 1 strides
+    auto in = [&](int j) { return first + j * stride < d; };
+    uint64_t w[P], b[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        w[i] = pair_at(p.W + first + 2 * i * stride, stride, in(2 * i), in(2 * i + 1));
+        b[i] = p.bias ? pair_at(p.bias + first + 2 * i * stride, stride, in(2 * i), in(2 * i + 1)) : 0ull;
+    }
+    const float inv_d = 1.f / static_cast<float>(d);
+    int s = 0, buf = 0;
+    uint32_t ph = 0;
+    for (int64_t c = begin; c < ring.chunks; c += ring.by, buf ^= 1) {
+        // a wait that gives up is recorded; the rows are then wrong
+        wait_bounded(ring.full0 + 8u * s, ph, &abort_flag, p.err, kDevErrTimeoutEpilogue);
+        if (!ring.copied(c)) load_chunk(ring, slots, s, c, team);
+        const int n = ring.rows_of(c);
+        const int64_t row0 = c * shape.per;
+        // where row r goes, and where it is staged
+        auto h_to = [&](int r) { return reinterpret_cast<uintptr_t>(p.H) + (row0 + r) * p.ldh * sizeof(T); };
+        auto y_to = [&](int r) { return reinterpret_cast<uintptr_t>(p.Y) + (row0 + r) * p.ldy * sizeof(TY); };
+        auto h_at = [&](int r) { return out + buf * out_bytes + (dense ? (h_to(0) & 15) + r * d * sizeof(T) : r * h_run + (h_to(r) & 15)); };
+        auto y_at = [&](int r) {
+            return out + buf * out_bytes + h_place + (dense ? (y_to(0) & 15) + r * d * sizeof(TY) : r * y_run + (y_to(r) & 15));
+        };
+        for (int r0 = 0; r0 < n; r0 += kRows) {
+            uint64_t a[kRows][P];
+            float mean[kRows], rstd[kRows];
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) {
+                mean[q] = 0.f;
+                if (r0 + q >= n) continue;
+                const T* x = reinterpret_cast<const T*>(slots + ring.row(0, s, c, r0 + q)) + first;
+                const T* res = reinterpret_cast<const T*>(slots + ring.row(1, s, c, r0 + q)) + first;
+                T* h = reinterpret_cast<T*>(h_at(r0 + q)) + first;
+                uint64_t sum2 = 0;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const int e = 2 * i * stride;
+                    a[q][i] = pair_at(x + e, stride, in(2 * i), in(2 * i + 1));
+                    if (p.R) a[q][i] = rounded_pair<T>(add2(a[q][i], pair_at(res + e, stride, in(2 * i), in(2 * i + 1))));
+                    if (p.H) put_pair(a[q][i], h + e, stride, in(2 * i), in(2 * i + 1));
+                    sum2 = add2(sum2, a[q][i]);
+                }
+                mean[q] = sum_of(sum2);
+            }
+            team.sum(mean, red[0]);
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) {
+                rstd[q] = 0.f;
+                if (r0 + q >= n) continue;
+                mean[q] *= inv_d;
+                const uint64_t minus = both(-mean[q]);
+                uint64_t ss2 = 0;
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    // (a value past the row stays zero)
+                    a[q][i] = add2(a[q][i], pair_of(in(2 * i) ? static_cast<uint32_t>(minus) : 0u, in(2 * i + 1) ? static_cast<uint32_t>(minus) : 0u));
+                    ss2 = fma2(a[q][i], a[q][i], ss2);
+                }
+                rstd[q] = sum_of(ss2);
+            }
+            team.sum(rstd, red[1]);
+#pragma unroll
+            for (int q = 0; q < kRows; ++q) {
+                if (r0 + q >= n) continue;
+                rstd[q] = 1.f / sqrtf(rstd[q] * inv_d + p.eps);
+                if (first == 0) {
+                    if (p.mean) p.mean[row0 + r0 + q] = mean[q];
+                    if (p.rstd) p.rstd[row0 + r0 + q] = rstd[q];
+                }
+                TY* y = reinterpret_cast<TY*>(y_at(r0 + q)) + first;
+                const uint64_t scale = both(rstd[q]);
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    put_pair(fma2(mul2(a[q][i], scale), w[i], b[i]), y + 2 * i * stride, stride, in(2 * i), in(2 * i + 1));
+            }
+        }
+        // What was staged leaves; the buffer before it has been read by then.
+        fence_proxy_async_smem();
+        if (team.thread == 0) bulk_wait_read_all();
+        team.sync();
+        const int runs = dense ? 1 : n;
+        const uint32_t values = static_cast<uint32_t>(dense ? n * d : d);
+        if (team.thread == 0) {
+            ring.fill(c + shape.slots * ring.by, s);
+            for (int r = 0; r < runs; ++r) {
+                if (p.H) store_run(h_to(r), smem_u32(h_at(r)), values * sizeof(T));
+                store_run(y_to(r), smem_u32(y_at(r)), values * sizeof(TY));
+            }
+            bulk_commit();
+        }
+        if (team.warp == team.warps - 1)
+            for (int r = 0; r < runs; ++r) {
+                if (p.H) store_ends<T>(h_to(r), h_at(r), values * sizeof(T), lane);
+                store_ends<TY>(y_to(r), y_at(r), values * sizeof(TY), lane);
+            }
+        if (++s == shape.slots) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+    if (team.thread == 0) bulk_wait_all();
 }
 
 bool al16(const void* p, int64_t pitch_bytes) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && pitch_bytes % 16 == 0;
 }
 
-// Threads and vectors per thread of a row of d elements; many rows at once
-// run best with two vectors per thread, a few rows sooner with one.
-void row_shape(int64_t rows, int64_t d, int num_sms, int* threads, int* vecs) {
-    const int64_t nv = (d + 7) / 8;
-    int v = rows <= 2 * static_cast<int64_t>(num_sms) ? 1 : 2;
-    while (v < 4 && (nv + v - 1) / v > 1024) v *= 2;
-    *threads = static_cast<int>(((nv + v - 1) / v + 31) / 32 * 32);
-    *vecs = v;
-}
-
-template <typename T, typename TY, int V, bool VEC, bool WARP>
-cudaError_t fwd_launch(const LayerNormFwd& a, int threads, cudaStream_t stream) {
-    const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0, bvec = reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-    const int64_t grid = WARP ? (a.rows + kWarpRows - 1) / kWarpRows : a.rows;
-    return launch_chained(layer_norm_fwd_kernel<T, TY, V, VEC, WARP>, dim3(static_cast<unsigned>(grid)), threads, 0, stream, a,
-                          wvec, bvec);
+template <typename K, typename... A>
+cudaError_t ring_launch(K kern, const LayerNormFwd& a, const RingShape& r, cudaStream_t stream, A... more) {
+    const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), static_cast<int>(kRingSmem), true);
+    if (e != cudaSuccess) return e;
+    return launch_chained(kern, dim3(static_cast<unsigned>(r.grid)), r.team * r.teams, static_cast<size_t>(r.smem), stream, a, r, more...);
 }
 
 template <typename T, typename TY, bool VEC>
 cudaError_t fwd_aligned(const LayerNormFwd& a, cudaStream_t stream) {
-    // a warp per row, once there is a CTA of such for every SM
-    if (a.d <= 768 && a.rows >= static_cast<int64_t>(kWarpRows) * a.num_sms) {
-        constexpr int kThreads = 32 * kWarpRows;
-        return a.d <= 256 ? fwd_launch<T, TY, 1, VEC, true>(a, kThreads, stream)
-               : a.d <= 512 ? fwd_launch<T, TY, 2, VEC, true>(a, kThreads, stream)
-                            : fwd_launch<T, TY, 3, VEC, true>(a, kThreads, stream);
+    const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0, bvec = reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+    const int64_t nv = (a.d + 7) / 8, sms = a.num_sms;
+    const int64_t es = sizeof(T), ey = sizeof(TY);
+    const bool whole = VEC && a.d % 8 == 0;
+    const bool many = a.rows > 4 * sms;
+    if (whole && many && a.d > 768 && a.d <= 8192) {
+        RingShape r;
+        r.per = kPair;
+        r.dense = 0;
+        team_of(&r, nv, {2, 1});
+        if (fit_ring(&r, a.rows, (a.R ? 2 : 1) * ChunkRing::place(a.d * es, kPair, false), 0, a.num_sms))
+            return r.each == 2 ? ring_launch(layer_norm_fwd_ring_kernel<T, TY, 2>, a, r, stream, wvec, bvec)
+                               : ring_launch(layer_norm_fwd_ring_kernel<T, TY, 1>, a, r, stream, wvec, bvec);
     }
-    int t, v;
-    row_shape(a.rows, a.d, a.num_sms, &t, &v);
-    return v == 1 ? fwd_launch<T, TY, 1, VEC, false>(a, t, stream)
-           : v == 2 ? fwd_launch<T, TY, 2, VEC, false>(a, t, stream) : fwd_launch<T, TY, 4, VEC, false>(a, t, stream);
+    if (!whole && many && a.d <= 8192 && a.d > 16) {
+        RingShape r;
+        r.dense = a.ldx == a.d && (!a.R || a.ldr == a.d) && (!a.H || a.ldh == a.d) && a.ldy == a.d;
+        if (r.dense && a.d <= 512) {   // a warp's rows: about 2 KiB
+            r.per = static_cast<int>(std::max<int64_t>(4, std::min<int64_t>(32, 2048 / (std::max(es, ey) * a.d) / 4 * 4)));
+            r.team = 32;
+            const int j = static_cast<int>((a.d + 31) / 32);
+            r.each = j + j % 2;
+        } else {
+            r.per = 2;
+            team_of(&r, a.d, {16, 14, 12, 10, 8});
+        }
+        auto fits = [&] {
+            const int64_t out = ChunkRing::place(a.d * ey, r.per, r.dense) + (a.H ? ChunkRing::place(a.d * es, r.per, r.dense) : 0);
+            return fit_ring(&r, a.rows, (a.R ? 2 : 1) * ChunkRing::place(a.d * es, r.per, r.dense), 2 * out, a.num_sms);
+        };
+        bool fit = fits();
+        if (!fit && r.per == 2) {   // longer rows one by one
+            r.per = 1;
+            fit = fits();
+        }
+        if (fit)
+            switch (r.each) {
+                case 2: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 2>, a, r, stream);
+                case 4: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 4>, a, r, stream);
+                case 6: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 6>, a, r, stream);
+                case 8: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 8>, a, r, stream);
+                case 10: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 10>, a, r, stream);
+                case 14: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 14>, a, r, stream);
+                case 12: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 12>, a, r, stream);
+                default: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 16>, a, r, stream);
+            }
+    }
+    if (a.d <= 768 && a.rows >= 8 * sms) {   // a warp per row, once there are eight for every SM
+        if constexpr (VEC) {
+            auto go = [&](auto kern, int lanes) {
+                const int64_t rows = kWarpThreads / lanes, blocks = (a.rows + rows - 1) / rows, most = 8 * sms;
+                return launch_chained(kern, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), kWarpThreads, 0, stream,
+                                      a, wvec, bvec);
+            };
+            if (a.d <= 64) return go(layer_norm_fwd_warp_kernel<T, TY, 8>, 8);
+            if (a.d <= 128) return go(layer_norm_fwd_warp_kernel<T, TY, 16>, 16);
+            if (a.d <= 256) return go(layer_norm_fwd_warp_kernel<T, TY, 32>, 32);
+        }
+        const dim3 grid(static_cast<unsigned>((a.rows + kWarpThreads / 32 - 1) / (kWarpThreads / 32)));
+        auto go = [&](auto kern) { return launch_chained(kern, grid, kWarpThreads, 0, stream, a, wvec, bvec); };
+        return a.d <= 256 ? go(layer_norm_fwd_kernel<T, TY, 1, VEC, true>)
+               : a.d <= 512 ? go(layer_norm_fwd_kernel<T, TY, 2, VEC, true>) : go(layer_norm_fwd_kernel<T, TY, 3, VEC, true>);
+    }
+    int v = many ? 2 : 1;   // a few rows are done sooner with one
+    while (v < 4 && (nv + v - 1) / v > 1024) v *= 2;
+    const unsigned threads = static_cast<unsigned>(((nv + v - 1) / v + 31) / 32 * 32);
+    const auto kern = v == 1 ? layer_norm_fwd_kernel<T, TY, 1, VEC, false>
+                      : v == 2 ? layer_norm_fwd_kernel<T, TY, 2, VEC, false> : layer_norm_fwd_kernel<T, TY, 4, VEC, false>;
+    return launch_chained(kern, dim3(static_cast<unsigned>(a.rows)), threads, 0, stream, a, wvec, bvec);
 }
 
 template <typename T, typename TY>
@@ -261,80 +548,12 @@ cudaError_t fwd_type(const LayerNormFwd& a, cudaStream_t stream) {
     return vec ? fwd_aligned<T, TY, true>(a, stream) : fwd_aligned<T, TY, false>(a, stream);
 }
 
-template <typename T, typename TY>
-bool bwd_vec(const LayerNormBwd& a) {
-    const int64_t es = sizeof(T);
-    return al16(a.dY, a.lddy * static_cast<int64_t>(sizeof(TY))) && al16(a.H, a.ldh * es) && (!a.dR || al16(a.dR, a.lddr * es)) &&
-           al16(a.dX, a.lddx * es);
-}
-
-// Lanes of a row in the column sums: whole warps unless the row is shorter.
-int col_lanes(int64_t d) {
-    int lanes = 32;
-    while (lanes > 1 && 4 * lanes >= d) lanes /= 2;
-    return lanes;
-}
-
-template <typename T, typename TY, bool VEC>
-cudaError_t dx_launch(const LayerNormBwd& a, cudaStream_t stream) {
-    int t, v;
-    row_shape(a.rows, a.d, a.num_sms, &t, &v);
-    const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0;
-    const auto kern = v == 1 ? layer_norm_dx_kernel<T, TY, 1, VEC>
-                      : v == 2 ? layer_norm_dx_kernel<T, TY, 2, VEC> : layer_norm_dx_kernel<T, TY, 4, VEC>;
-    return launch_chained(kern, dim3(static_cast<unsigned>(a.rows)), t, 0, stream, a, wvec);
-}
-
-template <typename T, typename TY>
-cudaError_t bwd_type(const LayerNormBwd& a, cudaStream_t stream, int* launches) {
-    const bool vec = bwd_vec<T, TY>(a);
-    *launches = 0;
-    if (a.dW || a.dbias) {   // first: dX may be dR, or dY
-        const int lanes = col_lanes(a.d);
-        const dim3 grid(static_cast<unsigned>((a.d + 8 * lanes - 1) / (8 * lanes)), static_cast<unsigned>(a.parts));
-        cudaError_t e = vec ? launch_chained(layer_norm_dw_kernel<T, TY, true>, grid, kColThreads, 0, stream, a, lanes)
-                            : launch_chained(layer_norm_dw_kernel<T, TY, false>, grid, kColThreads, 0, stream, a, lanes);
-        if (e != cudaSuccess) return e;
-        ++*launches;
-        if (a.parts > 1) {
-            if (a.dW) {
-                e = launch_column_sums(a.partial, a.parts, a.d, a.dW, stream);
-                if (e != cudaSuccess) return e;
-                ++*launches;
-            }
-            if (a.dbias) {
-                e = launch_column_sums(a.partial + static_cast<int64_t>(a.parts) * a.d, a.parts, a.d, a.dbias, stream);
-                if (e != cudaSuccess) return e;
-                ++*launches;
-            }
-        }
-    }
-    ++*launches;
-    return vec ? dx_launch<T, TY, true>(a, stream) : dx_launch<T, TY, false>(a, stream);
-}
-
 }  // namespace
 
 cudaError_t launch_layer_norm_fwd(const LayerNormFwd& a, cudaStream_t stream) {
     const bool xb = a.x_type == GEMM_DTYPE_BF16, yb = a.y_type == GEMM_DTYPE_BF16;
     return xb ? (yb ? fwd_type<__nv_bfloat16, __nv_bfloat16>(a, stream) : fwd_type<__nv_bfloat16, float>(a, stream))
               : (yb ? fwd_type<float, __nv_bfloat16>(a, stream) : fwd_type<float, float>(a, stream));
-}
-
-int layer_norm_bwd_parts(const LayerNormBwd& a) {
-    const int lanes = col_lanes(a.d);
-    const int64_t blocks = (a.d + 8 * lanes - 1) / (8 * lanes);
-    const int64_t turn = static_cast<int64_t>(kColRows) * (kColThreads / lanes);
-    int64_t parts = (8 * static_cast<int64_t>(a.num_sms) + blocks - 1) / blocks;
-    const int64_t most = (a.rows + 2 * turn - 1) / (2 * turn);
-    if (parts > most) parts = most;
-    return static_cast<int>(parts < 1 ? 1 : parts);
-}
-
-cudaError_t launch_layer_norm_bwd(const LayerNormBwd& a, cudaStream_t stream, int* launches) {
-    const bool xb = a.x_type == GEMM_DTYPE_BF16, yb = a.y_type == GEMM_DTYPE_BF16;
-    return xb ? (yb ? bwd_type<__nv_bfloat16, __nv_bfloat16>(a, stream, launches) : bwd_type<__nv_bfloat16, float>(a, stream, launches))
-              : (yb ? bwd_type<float, __nv_bfloat16>(a, stream, launches) : bwd_type<float, float>(a, stream, launches));
 }
 
 }  // namespace gemm

@@ -64,12 +64,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
         mma_f16_ss(d_tmem, a_desc, b_desc, idesc, accumulate);
 }
 
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // Elements of D's type as fp32, and back.
 template <bool F32>
 __device__ __forceinline__ float load_out(const void* p, int64_t i) {
