@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_odd_kernel(con
     for (int64_t c = begin; c < ring.chunks; c += ring.by, buf ^= 1) {
         // a wait that gives up is recorded; the rows are then wrong
         wait_bounded(ring.full0 + 8u * s, ph, &abort_flag, p.err, kDevErrTimeoutEpilogue);
-        if (!ring.copied(c)) load_chunk(ring, slots, s, c, team);
+        if (!ring.whole(c)) load_ends(ring, slots, s, c, team);
         const int n = ring.rows_of(c);
         const int64_t row0 = c * shape.per;
         // where row r goes, and where it is staged

@@ -17,9 +17,9 @@ namespace gemm {
 
 // A chunk is `per` neighbouring rows.  Dense rows (without gaps) are one run of
 // bytes, others a run each.  A run is copied with the 16-byte words that hold its
-// ends, to the same place modulo 16; a chunk whose words could reach past the
-// matrix (the first or the last, unless its ends are aligned) is not copied:
-// its team loads it.
+// ends, to the same place modulo 16; of a chunk whose words could reach past the
+// matrix (the first or the last, unless its ends are aligned) the words inside
+// its runs are copied, and its team loads what is left.
 struct ChunkRing {
     static constexpr int kSlots = 8;
     struct Array {
@@ -32,7 +32,7 @@ struct ChunkRing {
     int64_t rows, chunks, by;  // by: chunks from one of this ring to its next
     int per, slots;
     bool dense;
-    bool head, tail;           // whether the first and the last chunk are copied
+    bool head, tail;           // whether the first and the last chunk are copied whole
     uint32_t ring, full0, slot_bytes;
 
     // Bytes of a run's place in a slot.
@@ -70,15 +70,12 @@ struct ChunkRing {
     __device__ __forceinline__ int rows_of(int64_t c) const {
         return c + 1 < chunks ? per : static_cast<int>(rows - (chunks - 1) * per);
     }
-    __device__ __forceinline__ bool copied(int64_t c) const { return (c > 0 || head) && (c + 1 < chunks || tail); }
+    __device__ __forceinline__ bool whole(int64_t c) const { return (c > 0 || head) && (c + 1 < chunks || tail); }
     // One thread: chunk c (nothing past the last) into slot s.
     __device__ __forceinline__ void fill(int64_t c, int s) const {
         if (c >= chunks) return;
         const uint32_t bar = full0 + 8u * s, dst = ring + s * slot_bytes;
-        if (!copied(c)) {
-            mbar_arrive(bar);
-            return;
-        }
+        const bool out = whole(c);   // words that hold an end, or words inside
         const int n = rows_of(c), runs = dense ? 1 : n;
         uint32_t all = 0;
         for (int r = 0; r < runs; ++r)
@@ -86,9 +83,11 @@ struct ChunkRing {
             for (int i = 0; i < 3; ++i) {
                 if (!a[i].base) continue;
                 const uintptr_t from = reinterpret_cast<uintptr_t>(a[i].base) + (c * per + r) * a[i].pitch;
-                const uint32_t bytes = ((static_cast<uint32_t>(from) & 15u) + (dense ? n * a[i].bytes : a[i].bytes) + 15u) & ~15u;
-                all += bytes;
-                bulk_load(dst + a[i].at + r * a[i].place, reinterpret_cast<const void*>(from & ~uintptr_t(15)), bytes, bar);
+                const uint32_t low = static_cast<uint32_t>(from) & 15u, end = low + (dense ? n * a[i].bytes : a[i].bytes);
+                const uint32_t lo = out ? 0u : (low + 15u) & ~15u, hi = out ? (end + 15u) & ~15u : end & ~15u;   // from the first word's start
+                if (hi <= lo) continue;
+                all += hi - lo;
+                bulk_load(dst + a[i].at + r * a[i].place + lo, reinterpret_cast<const void*>((from & ~uintptr_t(15)) + lo), hi - lo, bar);
             }
         mbar_arrive_expect_tx(bar, all);
     }
@@ -154,17 +153,20 @@ struct Team {
     }
 };
 
-// Loads a chunk that was not copied into its place in slot s.  The whole team.
-__device__ __forceinline__ void load_chunk(const ChunkRing& ring, uint8_t* slots, int s, int64_t c, const Team& team) {
-    const int n = ring.rows_of(c);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
+// Loads the ends of a chunk that was not copied whole (at most seven elements of
+// two bytes at either end of a run).  The whole team.
+__device__ __forceinline__ void load_ends(const ChunkRing& ring, uint8_t* slots, int s, int64_t c, const Team& team) {
+    const int n = ring.rows_of(c), runs = ring.dense ? 1 : n;
+    for (int k = team.thread; k < runs * 3 * 16; k += team.threads) {
+        const int r = k / 48, i = k / 16 % 3, j = k % 16;
         if (!ring.a[i].base) continue;
-        for (int r = 0; r < n; ++r) {
-            const uint16_t* from = reinterpret_cast<const uint16_t*>(ring.a[i].base + (c * ring.per + r) * ring.a[i].pitch);
-            uint16_t* to = reinterpret_cast<uint16_t*>(slots + ring.row(i, s, c, r));
-            for (uint32_t k = team.thread; k < ring.a[i].bytes / 2; k += team.threads) to[k] = from[k];
-        }
+        const uintptr_t from = reinterpret_cast<uintptr_t>(ring.a[i].base) + (c * ring.per + r) * ring.a[i].pitch;
+        const uint32_t low = static_cast<uint32_t>(from) & 15u, end = low + (ring.dense ? n : 1) * ring.a[i].bytes;
+        const uint32_t lo = (low + 15u) & ~15u, hi = max(end & ~15u, lo);   // (rows are longer than a word)
+        const uint32_t at = j < 8 ? low + 2 * j : hi + 2 * (j - 8);
+        if (j < 8 ? at < lo : at < end)
+            *reinterpret_cast<uint16_t*>(slots + s * ring.slot_bytes + ring.a[i].at + r * ring.a[i].place + at) =
+                *reinterpret_cast<const uint16_t*>((from & ~uintptr_t(15)) + at);
     }
     team.sync();
 }
