@@ -3,15 +3,21 @@
 //
 //   dz = dy * act'(z),  dbias[j] = sum_i dy[i][j] * act'(z[i][j])
 //
-// Bound by DRAM: every element is read and written once.  A thread takes eight
-// columns of a range of rows and keeps their sums; the sums of a CTA are joined
-// in shared memory and those of the row ranges by launch_column_sums, both in a
-// fixed order.
+// Bound by DRAM: every element is read and written once (4096 x 16384, GELU_TANH:
+// 81 us, 5.0 TB/s; RELU 72 us, 5.6 TB/s; more rows in flight per thread spill or
+// cost CTAs).  A thread takes eight columns of a range of rows and keeps their
+// sums; the sums of a CTA are joined in shared memory, those of the row ranges
+// of a cluster through distributed shared memory, and those of clusters by
+// launch_column_sums, all in a fixed order.  Small problems are one cluster
+// deep: one launch and no scratch (2050 x 777, the sums alone: 7.3 us, 12.4
+// through scratch).
+#include <algorithm>
+#include <type_traits>
+
 #include "activation.cuh"
-#include "f8.cuh"
+#include "f8_tc.cuh"
 #include "internal.h"
 #include "layer.h"
-#include "ptx.cuh"
 
 namespace gemm {
 
@@ -20,123 +26,186 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 256;
-constexpr int kRowsAtOnce = 4;   // rows in flight per thread
+constexpr int kPerSm = 4;        // CTAs (of 64 registers per thread)
 
-// `lanes` neighbouring threads (a power of two, 32 for unaligned rows, whose
-// stores go by whole warps) hold 8 * lanes columns of a row.
-template <int ACT, bool VEC>
-__global__ void __launch_bounds__(kThreads) act_bwd_kernel(const ActBwd p, int lanes) {
-    __shared__ float red[kThreads * 8];
+// How a row is read.  kVectors: eight columns per thread, sixteen-byte aligned.
+// kShifted: the matrices are not aligned so, but lie alike (equal address and
+// pitch modulo sixteen bytes): the rows of a thread are a multiple of eight
+// apart and all start equally far past a boundary, so that the thread takes the
+// eight elements from a boundary to the next, and the ends of a row are what
+// the first and last lane hold of it.  kSingles: one column per thread
+// (measured, 55369 x 453, GELU_TANH: 45 us shifted, 128 as singles).
+enum { kVectors, kShifted, kSingles };
+
+// Rows in flight per thread: as many as the registers of kPerSm CTAs hold.
+template <int ACT, int MODE>
+constexpr int kRows = MODE == kSingles ? 8 : ACT <= GEMM_ACT_RELU ? 4 : 2;
+
+// W elements of row r from column c (that may start before the row or end
+// behind it).  What is before the matrix's first element or behind its last is
+// not read; other elements outside [first, last) are read and not used.
+template <int MODE, int W>
+__device__ __forceinline__ void load_piece(uint32_t (&w)[(W + 1) / 2], const void* m, int64_t ld, int64_t r, int64_t c, int first,
+                                           int last, const ActBwd& p) {
+    const int64_t off = r * ld + c;
+    const bf16* at = static_cast<const bf16*>(m) + off;
+    if (MODE == kSingles) {
+        w[0] = *reinterpret_cast<const uint16_t*>(at);
+    } else if (MODE == kVectors ? last == W : off >= 0 && off + W <= (p.rows - 1) * ld + p.cols) {
+        const uint4 u = *reinterpret_cast<const uint4*>(at);
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (i >= first && i < last) w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[i]) << 16 * (i & 1);
+    }
+}
+
+// `lanes` neighbouring threads (a power of two) hold p's `span` columns of a row.
+template <int ACT, int MODE>
+__global__ void __launch_bounds__(kThreads, kPerSm) act_bwd_kernel(const ActBwd p, int lanes, int span, int cluster) {
+    constexpr int R = kRows<ACT, MODE>, W = MODE == kSingles ? 1 : 8;
+    __shared__ float red[kThreads * W];
     pdl_launch_dependents();
     pdl_wait();
     const int groups = kThreads / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    const int64_t c = (static_cast<int64_t>(blockIdx.x) * lanes + lane) * 8;
     const int64_t per = (p.rows + p.parts - 1) / p.parts;
     const int64_t lo = per * blockIdx.y, hi = lo + per < p.rows ? lo + per : p.rows;
-    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int64_t r0 = lo + group; r0 < hi; r0 += static_cast<int64_t>(kRowsAtOnce) * groups) {
-        Vec8<bf16> dy[kRowsAtOnce], z[kRowsAtOnce];
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * span;
+    const int limit = p.cols - c0 < span ? static_cast<int>(p.cols - c0) : span;
+    // This thread's elements: [first, last) of the W from column c0 + rel.
+    const int before = MODE == kShifted
+        ? static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const bf16*>(p.dY) + (lo + group) * p.lddy + c0) / 2 % 8) : 0;
+    const int rel = lane * W - before, first = rel < 0 ? -rel : 0, last = limit - rel < W ? limit - rel : W;
+    float sum[W];
 #pragma unroll
-        for (int k = 0; k < kRowsAtOnce; ++k) {
+    for (int i = 0; i < W; ++i) sum[i] = 0.f;
+    for (int64_t r0 = lo + group; r0 < hi && first < last; r0 += static_cast<int64_t>(R) * groups) {
+        uint32_t dy[R][(W + 1) / 2], z[R][(W + 1) / 2];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
             const int64_t r = r0 + static_cast<int64_t>(k) * groups;
-            dy[k].zero();
-            z[k].zero();
-            if (r < hi && c < p.cols) {
-                dy[k] = load8<VEC>(static_cast<const bf16*>(p.dY) + r * p.lddy, c, p.cols);
-                if (p.Z) z[k] = load8<VEC>(static_cast<const bf16*>(p.Z) + r * p.ldz, c, p.cols);
+#pragma unroll
+            for (int i = 0; i < (W + 1) / 2; ++i) dy[k][i] = z[k][i] = 0u;
+            if (r < hi) {
+                load_piece<MODE, W>(dy[k], p.dY, p.lddy, r, c0 + rel, first, last, p);
+                if (ACT != GEMM_ACT_NONE) load_piece<MODE, W>(z[k], p.Z, p.ldz, r, c0 + rel, first, last, p);
             }
         }
+        auto value = [](const uint32_t(&w)[(W + 1) / 2], int i) { return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16); };
 #pragma unroll
-        for (int k = 0; k < kRowsAtOnce; ++k) {
+        for (int k = 0; k < R; ++k) {
             const int64_t r = r0 + static_cast<int64_t>(k) * groups;
-            float g[8], s[8];
-            dy[k].get(g);
-            z[k].get(s);
-            activate_each<ACT | GEMM_ACT_GRADIENT, 8>(g, [&](int i) { return s[i]; });
+            float g[W];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += g[i];
-            if (p.dZ && r < hi) {   // (lanes == 32 without VEC: the whole warp)
-                Vec8<bf16> o;
-                o.set(g);
-                store8<VEC>(static_cast<bf16*>(p.dZ) + r * p.lddz, c, p.cols, o);
+            for (int i = 0; i < W; ++i) g[i] = value(dy[k], i);
+            activate_each<ACT | GEMM_ACT_GRADIENT, W>(g, [&](int i) { return value(z[k], i); });
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[i] += g[i];   // (outside [first, last) another row's, and unused)
+            if (!p.dZ || r >= hi) continue;
+            bf16* out = static_cast<bf16*>(p.dZ) + r * p.lddz + c0 + rel;
+            if (W == 1) {
+                out[0] = __float2bfloat16_rn(g[0]);
+            } else if (last - first == W) {
+                uint4 u;
+                u.x = bf16x2(g[0], g[1 % W]); u.y = bf16x2(g[2 % W], g[3 % W]);
+                u.z = bf16x2(g[4 % W], g[5 % W]); u.w = bf16x2(g[6 % W], g[7 % W]);
+                *reinterpret_cast<uint4*>(out) = u;
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    if (i >= first && i < last) out[i] = __float2bfloat16_rn(g[i]);
             }
         }
     }
-    if (!p.dbias) return;
+    if (!p.dbias) return;   // (every CTA alike)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) red[group * lanes * 8 + lane * 8 + i] = sum[i];
+    for (int i = 0; i < W; ++i)
+        if (i >= first && i < last) red[group * span + rel + i] = sum[i];
     __syncthreads();
-    float* out = p.parts > 1 ? p.partial + static_cast<int64_t>(blockIdx.y) * p.cols : p.dbias;
-    for (int i = threadIdx.x; i < 8 * lanes; i += kThreads) {
-        float v = red[i];
-        for (int g = 1; g < groups; ++g) v += red[g * lanes * 8 + i];
-        const int64_t col = static_cast<int64_t>(blockIdx.x) * lanes * 8 + i;
-        if (col < p.cols) out[col] = v;
+    if (threadIdx.x < limit) {   // (limit <= span <= kThreads)
+        float v = red[threadIdx.x];
+        for (int g = 1; g < groups; ++g) v += red[g * span + threadIdx.x];
+        red[threadIdx.x] = v;   // (its only reader)
     }
+    float* out = p.parts > cluster ? p.partial + static_cast<int64_t>(blockIdx.y / cluster) * p.cols : p.dbias;
+    join_cluster(red, limit, cluster, [&](int i, float v) { out[c0 + i] = v; });
 }
 
-// Eight elements per thread; the destination's rows are aligned, its pitch a
-// multiple of eight, so that every store is a whole vector (what lies between
-// the columns and the pitch is not used).
-__global__ void __launch_bounds__(256) repitch_kernel(const bf16* src, int64_t ld, bf16* dst, int64_t pitch, int64_t rows,
-                                                      int64_t cols) {
+// Eight elements per thread of one matrix or two; the destinations' rows are
+// aligned, their pitches multiples of eight, so that every store is a whole
+// vector (what lies between the columns and the pitch is not used).
+__global__ void __launch_bounds__(256) repitch_kernel(const Repitch a, const Repitch b) {
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t vecs = pitch / 8, all = rows * vecs, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    const int64_t in_a = a.rows * (a.pitch / 8), all = in_a + b.rows * (b.pitch / 8), step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += step) {
-        const int64_t r = i / vecs, c = (i - r * vecs) * 8;
-        load8<false>(src + r * ld, c, cols).store(dst + r * pitch + c);
+        const Repitch& m = i < in_a ? a : b;
+        const int64_t j = i < in_a ? i : i - in_a, vecs = m.pitch / 8, r = j / vecs, c = (j - r * vecs) * 8;
+        load8<false>(static_cast<const bf16*>(m.src) + r * m.ld, c, m.cols).store(static_cast<bf16*>(m.dst) + r * m.pitch + c);
     }
 }
 
-bool vec_ok(const void* p, int64_t ld) { return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0); }
-bool act_vec(const ActBwd& a) { return vec_ok(a.dY, a.lddy) && vec_ok(a.Z, a.ldz) && vec_ok(a.dZ, a.lddz); }
-
-int act_lanes(const ActBwd& a) {
-    int lanes = 32;
-    if (act_vec(a))
-        while (lanes > 1 && 4 * lanes >= a.cols) lanes /= 2;
-    return lanes;
+// How rows are read, and the threads and columns of a row in a CTA.
+struct Shape {
+    int mode, lanes, span;
+};
+Shape act_shape(const ActBwd& a) {
+    const uintptr_t y = reinterpret_cast<uintptr_t>(a.dY);
+    auto like = [&](const void* p, int64_t ld) {   // dY's rows, modulo sixteen bytes
+        return !p || ((reinterpret_cast<uintptr_t>(p) - y) % 16 == 0 && (ld - a.lddy) % 8 == 0);
+    };
+    Shape s;
+    s.mode = !like(a.Z, a.ldz) || !like(a.dZ, a.lddz) ? kSingles : y % 16 || a.lddy % 8 ? kShifted : kVectors;
+    const int width = s.mode == kSingles ? 1 : 8;
+    auto span = [&](int lanes) { return s.mode == kShifted ? (lanes - 1) * width : lanes * width; };
+    s.lanes = 32;
+    while (s.lanes > 2 && span(s.lanes / 2) >= a.cols) s.lanes /= 2;
+    s.span = span(s.lanes);
+    return s;
 }
 
 }  // namespace
 
-// Row ranges: about eight CTAs per SM over all column blocks, each thread with
-// at least two turns of rows.
+// Row ranges: the CTAs of all column blocks run at once (clusters leave some
+// room), each thread has at least two turns of four rows, and more than one
+// cluster's are whole clusters.
 int act_bwd_parts(const ActBwd& a) {
-    const int lanes = act_lanes(a);
-    const int64_t blocks = (a.cols + 8 * lanes - 1) / (8 * lanes);
-    const int64_t turn = static_cast<int64_t>(kRowsAtOnce) * (kThreads / lanes);
-    int64_t parts = (8 * static_cast<int64_t>(a.num_sms) + blocks - 1) / blocks;
-    const int64_t most = (a.rows + 2 * turn - 1) / (2 * turn);
-    if (parts > most) parts = most;
-    return static_cast<int>(parts < 1 ? 1 : parts);
+    const Shape s = act_shape(a);
+    const int64_t blocks = (a.cols + s.span - 1) / s.span, turn = 4 * (kThreads / s.lanes);
+    const int64_t at_once = std::max<int64_t>(1, static_cast<int64_t>(a.num_sms) * kPerSm * 7 / 8 / blocks);
+    int64_t parts = std::min(at_once, (a.rows + 2 * turn - 1) / (2 * turn));
+    if (parts > kMostClusterCtas) parts = parts / kMostClusterCtas * kMostClusterCtas;
+    return static_cast<int>(parts);
 }
+int act_bwd_clusters(const ActBwd& a) { return a.parts <= kMostClusterCtas ? 1 : a.parts / kMostClusterCtas; }
 
 cudaError_t launch_act_bwd(const ActBwd& a, cudaStream_t stream) {
-    const int lanes = act_lanes(a);
-    const dim3 grid(static_cast<unsigned>((a.cols + 8 * lanes - 1) / (8 * lanes)), static_cast<unsigned>(a.parts));
-    auto go = [&](auto kern) { return launch_chained(kern, grid, kThreads, 0, stream, a, lanes); };
-    const bool vec = act_vec(a);
+    const Shape s = act_shape(a);
+    const int cluster = std::min(a.parts, kMostClusterCtas);
+    const dim3 grid(static_cast<unsigned>((a.cols + s.span - 1) / s.span), static_cast<unsigned>(a.parts));
+    auto launch = [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        const auto kern = s.mode == kVectors ? act_bwd_kernel<ACT, kVectors>
+                          : s.mode == kShifted ? act_bwd_kernel<ACT, kShifted> : act_bwd_kernel<ACT, kSingles>;
+        return launch_clusters(kern, grid, dim3(1, static_cast<unsigned>(cluster), 1), kThreads, 0, stream, a, s.lanes, s.span, cluster);
+    };
     cudaError_t e;
     switch (a.act) {
-        case GEMM_ACT_RELU: e = go(vec ? act_bwd_kernel<GEMM_ACT_RELU, true> : act_bwd_kernel<GEMM_ACT_RELU, false>); break;
-        case GEMM_ACT_GELU: e = go(vec ? act_bwd_kernel<GEMM_ACT_GELU, true> : act_bwd_kernel<GEMM_ACT_GELU, false>); break;
-        case GEMM_ACT_GELU_TANH:
-            e = go(vec ? act_bwd_kernel<GEMM_ACT_GELU_TANH, true> : act_bwd_kernel<GEMM_ACT_GELU_TANH, false>);
-            break;
-        case GEMM_ACT_SILU: e = go(vec ? act_bwd_kernel<GEMM_ACT_SILU, true> : act_bwd_kernel<GEMM_ACT_SILU, false>); break;
-        default: e = go(vec ? act_bwd_kernel<GEMM_ACT_NONE, true> : act_bwd_kernel<GEMM_ACT_NONE, false>); break;
+        case GEMM_ACT_RELU: e = launch(std::integral_constant<int, GEMM_ACT_RELU>{}); break;
+        case GEMM_ACT_GELU: e = launch(std::integral_constant<int, GEMM_ACT_GELU>{}); break;
+        case GEMM_ACT_GELU_TANH: e = launch(std::integral_constant<int, GEMM_ACT_GELU_TANH>{}); break;
+        case GEMM_ACT_SILU: e = launch(std::integral_constant<int, GEMM_ACT_SILU>{}); break;
+        default: e = launch(std::integral_constant<int, GEMM_ACT_NONE>{}); break;
     }
-    if (e == cudaSuccess && a.dbias && a.parts > 1) e = launch_column_sums(a.partial, a.parts, a.cols, a.dbias, stream);
+    const int clusters = act_bwd_clusters(a);
+    if (e == cudaSuccess && a.dbias && clusters > 1) e = launch_column_sums(a.partial, clusters, a.cols, a.dbias, stream);
     return e;
 }
 
-cudaError_t launch_repitch(const void* src, int64_t ld, void* dst, int64_t pitch, int64_t rows, int64_t cols, int num_sms,
-                           cudaStream_t stream) {
-    const int64_t blocks = (rows * (pitch / 8) + 255) / 256, most = 16 * static_cast<int64_t>(num_sms);
-    return launch_chained(repitch_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, stream,
-                          static_cast<const bf16*>(src), ld, static_cast<bf16*>(dst), pitch, rows, cols);
+cudaError_t launch_repitch(const Repitch& a, const Repitch& b, int num_sms, cudaStream_t stream) {
+    const int64_t blocks = (a.rows * (a.pitch / 8) + b.rows * (b.pitch / 8) + 255) / 256, most = 16 * static_cast<int64_t>(num_sms);
+    return launch_chained(repitch_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, 0, stream, a, b);
 }
 
 }  // namespace gemm

@@ -378,6 +378,36 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A float of another CTA of the cluster (behind a barrier).
+__device__ __forceinline__ float load_in_cluster(uint32_t addr_cluster) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr_cluster));
+    return v;
+}
+// Sums over the CTAs of a cluster of n floats that each has in shared memory at
+// `at`, in rank order: put(i, sum) by one thread of one CTA for each i.  The
+// whole cluster.
+constexpr int kMostClusterCtas = 8;
+template <typename F>
+__device__ __forceinline__ void join_cluster(const float* at, int n, int ctas, F put) {
+    if (ctas == 1) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += blockDim.x) put(i, at[i]);
+        return;
+    }
+    const uint32_t base = smem_u32(at);
+    cluster_barrier();
+    for (int i = static_cast<int>(cta_rank_in_cluster()) + ctas * threadIdx.x; i < n; i += ctas * blockDim.x) {
+        float v[kMostClusterCtas], sum = 0.f;   // (asked for together: a remote read takes its time)
+#pragma unroll
+        for (int r = 0; r < kMostClusterCtas; ++r) v[r] = r < ctas ? load_in_cluster(peer_address(base + 4 * i, r)) : 0.f;
+#pragma unroll
+        for (int r = 0; r < kMostClusterCtas; ++r) sum += v[r];
+        put(i, sum);
+    }
+    cluster_barrier();   // the others' shared memory has been read
+}
+
 // Arrives on a barrier of a CTA of the cluster, releasing no memory beyond the
 // CTA: for hand-offs whose data is in TMEM (tcgen05.fence orders it).  A
 // release for the cluster waits for the thread's global accesses.
@@ -427,6 +457,28 @@ __device__ __forceinline__ void alloc_pair(uint32_t dst_smem, uint32_t ncols) {
 }
 __device__ __forceinline__ void free_pair(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// launch_chained with clusters of x * y CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kern)(P...), dim3 grid, dim3 cluster, unsigned threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster.x;
+    attr[0].val.clusterDim.y = cluster.y;
+    attr[0].val.clusterDim.z = cluster.z;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // Host: the kernels' parameters for tiles of bm rows x bn columns of D.

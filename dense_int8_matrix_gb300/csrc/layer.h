@@ -33,10 +33,15 @@ cudaError_t launch_linear_tc2(const LinearLaunch& a, cudaStream_t stream);
 // Tiles of bm (16, 32, 64, 128; GEMM_FORM_TN 64, 128) rows x 128 columns, split_k CTAs each (gemm_linear_skinny.cu).
 cudaError_t launch_linear_skinny(const LinearLaunch& a, cudaStream_t stream);
 
-// Copies a bfloat16 matrix of any address and pitch to rows that are 16-byte
-// aligned (dst, pitch a multiple of 8).
-cudaError_t launch_repitch(const void* src, int64_t ld, void* dst, int64_t pitch, int64_t rows, int64_t cols, int num_sms,
-                           cudaStream_t stream);
+// Copies bfloat16 matrices of any address and pitch to rows that are 16-byte
+// aligned (dst, pitch a multiple of 8); rows == 0: none.
+struct Repitch {
+    const void* src;
+    int64_t ld;
+    void* dst;
+    int64_t pitch, rows, cols;
+};
+cudaError_t launch_repitch(const Repitch& a, const Repitch& b, int num_sms, cudaStream_t stream);
 
 // ---- sums over rows ------------------------------------------------------------
 // out[j] = sum over the parts of partial[part][j], in order (norm.cu).
@@ -47,13 +52,14 @@ struct ActBwd {
     const void *dY, *Z;
     void* dZ;
     float* dbias;     // cols sums, or nullptr
-    float* partial;   // parts x cols sums when parts > 1
+    float* partial;   // clusters x cols sums when there are several clusters
     int64_t rows, cols, lddy, ldz, lddz;
     int act;
     int parts;        // row ranges
     int num_sms;
 };
 int act_bwd_parts(const ActBwd& a);
+int act_bwd_clusters(const ActBwd& a);   // of row ranges, once parts is set
 cudaError_t launch_act_bwd(const ActBwd& a, cudaStream_t stream);
 
 // ---- layer norm (layer_norm.cu, layer_norm_bwd.cu) ------------------------------------------------

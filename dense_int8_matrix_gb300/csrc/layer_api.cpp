@@ -18,22 +18,19 @@ class Scratch {
   public:
     Scratch(cudaMemPool_t pool, cudaStream_t stream) : pool_(pool), stream_(stream) {}
     ~Scratch() {
-        for (void* p : ptr_)
-            if (p) cudaFreeAsync(p, stream_);
+        if (ptr_) cudaFreeAsync(ptr_, stream_);
     }
     Scratch(const Scratch&) = delete;
     Scratch& operator=(const Scratch&) = delete;
-    void* take(int64_t bytes) {   // nullptr if there is none (at most two per call)
-        void* p = nullptr;
-        if (cudaMallocFromPoolAsync(&p, static_cast<size_t>(bytes), pool_, stream_) != cudaSuccess) return nullptr;
-        ptr_[ptr_[0] ? 1 : 0] = p;
-        return p;
+    void* take(int64_t bytes) {   // once per call; nullptr if there is none
+        if (cudaMallocFromPoolAsync(&ptr_, static_cast<size_t>(bytes), pool_, stream_) != cudaSuccess) ptr_ = nullptr;
+        return ptr_;
     }
 
   private:
     cudaMemPool_t pool_;
     cudaStream_t stream_;
-    void* ptr_[2] = {nullptr, nullptr};
+    void* ptr_ = nullptr;
 };
 
 bool act_ok(int32_t act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_SILU; }
@@ -195,23 +192,28 @@ gemm_status gemm_bf16_linear_run(const gemm_plan_linear* plan, const uint16_t* A
     L.pairs = ctx.pairs;
     Scratch scratch(ctx.pool, s);
     const bool sampled = trace_begin_call();
-    auto align = [&](const void** at, int64_t* ld, int64_t rows, int64_t cols) {
-        if (tma_rows(*at, *ld)) return GEMM_OK;
-        const int64_t pitch = (cols + 7) / 8 * 8;
-        void* copy = scratch.take(rows * pitch * 2);
+    Repitch ra{A, lda, nullptr, (cols_a + 7) / 8 * 8, tma_rows(A, lda) ? 0 : rows_a, cols_a};
+    Repitch rb{B, ldb, nullptr, (cols_b + 7) / 8 * 8, tma_rows(B, ldb) ? 0 : rows_b, cols_b};
+    if (ra.rows || rb.rows) {   // one launch, and scratch, for both
+        const int64_t in_a = (ra.rows * ra.pitch * 2 + 255) / 256 * 256;
+        uint8_t* copy = static_cast<uint8_t*>(scratch.take(in_a + rb.rows * rb.pitch * 2));
         if (!copy) return GEMM_ERR_CUDA;
+        ra.dst = copy;
+        rb.dst = copy + in_a;
         void* unit = trace_unit_begin(GEMM_KERNEL_STAGE, s, sampled);
-        const cudaError_t e = launch_repitch(*at, *ld, copy, pitch, rows, cols, ctx.num_sms, s);
+        const cudaError_t e = launch_repitch(ra, rb, ctx.num_sms, s);
         trace_unit_end(unit, s);
         if (e != cudaSuccess) return GEMM_ERR_CUDA;
         trace_launch(GEMM_KERNEL_STAGE);
-        *at = copy;
-        *ld = pitch;
-        return GEMM_OK;
-    };
-    gemm_status r = align(&L.A, &L.lda, rows_a, cols_a);
-    if (r == GEMM_OK) r = align(&L.B, &L.ldb, rows_b, cols_b);
-    if (r != GEMM_OK) return r;
+        if (ra.rows) {
+            L.A = ra.dst;
+            L.lda = ra.pitch;
+        }
+        if (rb.rows) {
+            L.B = rb.dst;
+            L.ldb = rb.pitch;
+        }
+    }
     const int kind = p->path == GEMM_PATH_SKINNY ? GEMM_KERNEL_SKINNY : GEMM_KERNEL_TC;
     void* unit = trace_unit_begin(kind, s, sampled);
     const cudaError_t e = p->path == GEMM_PATH_SKINNY ? launch_linear_skinny(L, s) : launch_linear_tc2(L, s);
@@ -249,9 +251,10 @@ gemm_status gemm_activation_backward(const uint16_t* dY, int64_t lddy, const uin
     a.num_sms = ctx.num_sms;
     a.parts = act_bwd_parts(a);
     Scratch scratch(ctx.pool, s);
-    const bool joined = dbias && a.parts > 1;
+    const int clusters = act_bwd_clusters(a);
+    const bool joined = dbias && clusters > 1;
     if (joined) {
-        a.partial = static_cast<float*>(scratch.take(a.parts * cols * 4));
+        a.partial = static_cast<float*>(scratch.take(clusters * cols * 4));
         if (!a.partial) return GEMM_ERR_CUDA;
     }
     const gemm_status r = staged([&] { return launch_act_bwd(a, s); }, s);

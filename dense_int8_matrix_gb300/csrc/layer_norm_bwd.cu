@@ -527,13 +527,13 @@ __global__ void __launch_bounds__(1024) layer_norm_dx_kernel(const LayerNormBwd 
 constexpr int kColThreads = 256;
 constexpr int kColRows = 4;   // rows in flight per thread
 template <typename T, typename TY, bool VEC>
-__global__ void __launch_bounds__(kColThreads) layer_norm_dw_kernel(const LayerNormBwd p, int lanes) {
+__global__ void __launch_bounds__(kColThreads) layer_norm_dw_kernel(const LayerNormBwd p, int lanes, int cluster) {
     __shared__ float red[2][kColThreads * 8];
     pdl_launch_dependents();
     pdl_wait();
     const int groups = kColThreads / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * lanes + lane) * 8;
-    const int64_t per = (p.rows + p.parts - 1) / p.parts;
+    const int64_t per = (p.rows + gridDim.y - 1) / gridDim.y;
     const int64_t lo = per * blockIdx.y, hi = lo + per < p.rows ? lo + per : p.rows;
     float dw[8], db[8];
 #pragma unroll
@@ -573,15 +573,21 @@ __global__ void __launch_bounds__(kColThreads) layer_norm_dw_kernel(const LayerN
         red[1][(group * lanes + lane) * 8 + i] = db[i];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * lanes; i += kColThreads) {
-        const int which = i / (8 * lanes), j = i % (8 * lanes);
+    const int n = 8 * lanes;   // (at most kColThreads)
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
         float* out = which == 0 ? p.dW : p.dbias;
-        if (!out) continue;
-        float v = red[which][j];
-        for (int g = 1; g < groups; ++g) v += red[which][g * lanes * 8 + j];
-        const int64_t col = static_cast<int64_t>(blockIdx.x) * lanes * 8 + j;
-        if (p.parts > 1) out = p.partial + (static_cast<int64_t>(which) * p.parts + blockIdx.y) * p.d;
-        if (col < p.d) out[col] = v;
+        if (!out) continue;   // (every CTA alike)
+        if (threadIdx.x < n) {
+            float v = red[which][threadIdx.x];
+            for (int g = 1; g < groups; ++g) v += red[which][g * n + threadIdx.x];
+            red[which][threadIdx.x] = v;   // (its only reader)
+        }
+        if (p.parts > 1) out = p.partial + (static_cast<int64_t>(which) * p.parts + blockIdx.y / cluster) * p.d;
+        join_cluster(red[which], n, cluster, [&](int i, float v) {
+            const int64_t col = static_cast<int64_t>(blockIdx.x) * n + i;
+            if (col < p.d) out[col] = v;
+        });
     }
 }
 
@@ -600,7 +606,8 @@ struct Choice {
     Way way;
     int lanes;        // of a row (kByWarps)
     RingShape ring;   // (kByRing, kOdd)
-    int grid;         // CTAs, or row ranges (kTwoPasses)
+    int grid;         // CTAs; row ranges (kTwoPasses)
+    int parts;        // sums to be joined through scratch
 };
 
 // Lanes of a row in the column sums: whole warps unless the row is shorter.
@@ -620,7 +627,7 @@ Choice choose(const LayerNormBwd& a) {
         c.way = kByWarps;
         c.lanes = a.d <= 64 ? 8 : a.d <= 128 ? 16 : 32;
         const int64_t rows = kWarpThreads / c.lanes;
-        c.grid = static_cast<int>(std::min<int64_t>((a.rows + 2 * rows - 1) / (2 * rows), 2 * sms));
+        c.parts = c.grid = static_cast<int>(std::min<int64_t>((a.rows + 2 * rows - 1) / (2 * rows), 2 * sms));
         return c;
     }
     if (a.rows > 2 * sms && a.d <= 8192 && a.d > 16) {
@@ -650,14 +657,17 @@ Choice choose(const LayerNormBwd& a) {
         if (fit) {
             // (the teams' sums take its place: d floats each, fewer bytes than two slots)
             c.way = whole ? kByRing : kOdd;
-            c.grid = r.grid;
+            c.parts = c.grid = r.grid;
             return c;
         }
     }
     c.way = kTwoPasses;
     const int lanes = col_lanes(a.d);
     const int64_t blocks = (a.d + 8 * lanes - 1) / (8 * lanes), turn = static_cast<int64_t>(kColRows) * (kColThreads / lanes);
+    // Up to eight ranges are one cluster and joined in it; of more, the sums go
+    // through scratch.
     c.grid = static_cast<int>(std::max<int64_t>(1, std::min((8 * sms + blocks - 1) / blocks, (a.rows + 2 * turn - 1) / (2 * turn))));
+    c.parts = c.grid <= kMostClusterCtas ? 1 : c.grid;
     return c;
 }
 
@@ -703,7 +713,9 @@ cudaError_t two_passes(const LayerNormBwd& a, const Choice& c, cudaStream_t stre
     if (a.dW || a.dbias) {   // first: dX may be dR, or dY
         const int lanes = col_lanes(a.d);
         const dim3 grid(static_cast<unsigned>((a.d + 8 * lanes - 1) / (8 * lanes)), static_cast<unsigned>(c.grid));
-        const cudaError_t e = launch_chained(layer_norm_dw_kernel<T, TY, VEC>, grid, kColThreads, 0, stream, a, lanes);
+        const int cluster = c.parts == 1 ? c.grid : 1;
+        const cudaError_t e = launch_clusters(layer_norm_dw_kernel<T, TY, VEC>, grid, dim3(1, static_cast<unsigned>(cluster), 1),
+                                              kColThreads, 0, stream, a, lanes, cluster);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
@@ -742,7 +754,7 @@ cudaError_t bwd_type(const LayerNormBwd& a, cudaStream_t stream, int* launches) 
 
 }  // namespace
 
-int layer_norm_bwd_parts(const LayerNormBwd& a) { return choose(a).grid; }
+int layer_norm_bwd_parts(const LayerNormBwd& a) { return choose(a).parts; }
 
 cudaError_t launch_layer_norm_bwd(const LayerNormBwd& a, cudaStream_t stream, int* launches) {
     const bool xb = a.x_type == GEMM_DTYPE_BF16, yb = a.y_type == GEMM_DTYPE_BF16;

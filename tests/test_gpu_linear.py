@@ -238,6 +238,22 @@ def test_activation_backward(act, rows, cols):
             assert torch.equal(out, dZ) and torch.equal(again, db)
 
 
+@pytest.mark.parametrize("places", [((0, 0), (1, 0), (0, 0)), ((3, 1), (3, 1), (0, 0)), ((1, 3), (9, 11), (17, 3)), ((5, 2), (5, 3), (5, 2))])
+@pytest.mark.parametrize("rows,cols", [(1, 3), (9, 5), (333, 1), (70, 249), (2100, 33)])
+def test_activation_backward_of_rows_that_lie_otherwise(rows, cols, places):
+    # pitches and offsets (pad, at) of dY, Z and dZ, alike modulo eight elements or not
+    dy, z = R.normal((rows, cols), 1, 0.1), R.normal((rows, cols), 2, 2.0)
+    want = dy.double() * R.slope("silu", z)
+    size = dy.double().abs() * 2 * ACT_ERR
+    dY, Z = R.padded(dy, *places[0])[0], R.padded(z, *places[1], float("nan"))[0]
+    dZ, buf = R.padded(torch.zeros_like(dy), *places[2], 7.0)
+    db = filled(cols, dtype=torch.float32)
+    B.gemm_activation_backward(dY, Z, R.ACTS["silu"], dZ, db)
+    check(dZ, want, size, torch.bfloat16)
+    assert bool(((db.cpu().double() - want.sum(0)).abs() <= rows * 2.0 ** -24 * want.abs().sum(0) + size.sum(0) + 2.0 ** -100).all())
+    assert bool((R.outside(buf, dZ) == 7.0).all())
+
+
 def test_gradients_against_differences():
     # a layer's forward and backward calls against differences of the 64-bit layer
     m, k, n = 12, 40, 24
