@@ -7,8 +7,8 @@ gathered by expert; two gemm_f8_grouped_run products with ragged rows, with
 gemm_f8_quantize between them.  Backward: the products' input gradients (the
 same grouped product with the transposed weights), the weights' gradients
 (gemm_f8_quantize_cols and the product grouped along K) and
-gemm_norm_backward.  Routing (a matrix product, an argmax and a sort) and the
-activation stay in torch.  `python examples/expert_layer.py` compares the step with
+gemm_norm_backward.  gemm_balance counts the experts' rows; the router's
+product, its argmax, the sort and the activation stay in torch.  `python examples/expert_layer.py` compares the step with
 the same layer in fp32 torch.
 """
 
@@ -79,6 +79,16 @@ def weight_gradient(dy, x, offsets):
     return dw
 
 
+def balance(logits, expert, coef=0.01):
+    """Where the rows of each expert begin once they are sorted by it, and the
+    loss that keeps the experts equally used."""
+    rows, experts = logits.shape
+    counts, offsets, used = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (experts, experts + 1, 1))
+    lse, probs, loss = (torch.empty(n, device="cuda") for n in (rows, experts, 1))
+    B.gemm_balance(logits, expert[:, None].to(torch.int32), coef, counts, offsets, used, lse, probs, loss)
+    return offsets, loss
+
+
 def step(x, r, norm_w, router, w1, w2, d_out):
     """Forward and backward.  x, r, d_out: (rows, d) bfloat16; norm_w: (d,)
     fp32; router: (experts, d); w1: (experts, ff, d), w2: (experts, d, ff)
@@ -92,9 +102,10 @@ def step(x, r, norm_w, router, w1, w2, d_out):
     q, scale = f8_empty(rows, d), torch.empty((d + 127) // 128, rows, device="cuda")
     B.gemm_norm_f8(x, r, norm_w, EPS, h, rstd, q, scale)
 
-    expert = (h.float() @ router.T).argmax(1)
+    logits = h.float() @ router.T
+    expert = logits.argmax(1)
     order = torch.argsort(expert, stable=True)
-    offsets = torch.nn.functional.pad(torch.bincount(expert, minlength=experts).cumsum(0), (1, 0)).to(torch.int32)
+    offsets, _ = balance(logits, expert)
 
     a = f8_empty(rows, d)
     a.view(torch.uint8).copy_(q.view(torch.uint8)[order])
