@@ -179,16 +179,15 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, uint32_t stg
     }
 }
 
-// One or two neighbouring bfloat16 values (two only at even elements); of two
-// columns the second may be past the row.
+// One bfloat16 value, or two at an even element.
 template <int W>
-__device__ __forceinline__ uint32_t load_some(const __nv_bfloat16* p, int64_t cols) {
-    if (W == 2 && cols >= 2) return *reinterpret_cast<const uint32_t*>(p);
+__device__ __forceinline__ uint32_t load_some(const __nv_bfloat16* p) {
+    if constexpr (W == 2) return *reinterpret_cast<const uint32_t*>(p);
     return *reinterpret_cast<const uint16_t*>(p);
 }
 template <int W>
-__device__ __forceinline__ void store_some(__nv_bfloat16* p, int64_t cols, const float* v) {
-    if (W == 2 && cols >= 2)
+__device__ __forceinline__ void store_some(__nv_bfloat16* p, const float* v) {
+    if constexpr (W == 2)
         *reinterpret_cast<uint32_t*>(p) = bf16x2(v[0], v[W - 1]);
     else
         *p = __float2bfloat16_rn(v[0]);
@@ -239,19 +238,21 @@ __device__ __forceinline__ void finish_column(const LinearParams& p, int row0, i
 }
 // The same 32 x 32 block of a ragged edge, or of rows that are not aligned
 // for vectors: a lane takes one column of every row, or (PAIRS, rows at even
-// elements) two columns of every other row, so that every access is contiguous
-// along a row.  What is read is asked for sixteen rows ahead.
+// elements, all columns there) two columns of every other row, so that every
+// access is contiguous along a row.  What is read is asked for eight rows
+// ahead.
 template <bool F32, int ACT, bool PAIRS>
 __device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t stg, int lane, int row0, int row_end, int col0) {
     constexpr bool kReadZ = (ACT & GEMM_ACT_GRADIENT) != 0;
     constexpr int W = PAIRS ? 2 : 1;          // columns of a lane, and rows of an access
-    constexpr int N = 16 / W;                 // accesses in flight
+    constexpr int N = 8 / W;                  // accesses in flight; 16 / W: 5 to 10 % slower (1965 x 3842, 594 x 1153), by the size of the code
+    static_assert(!(F32 && PAIRS), "fp32 columns are single");
     const int c = PAIRS ? (lane & 15) * 2 : lane, r0 = PAIRS ? lane >> 4 : 0;
-    const int col = col0 + c, cols = p.n - col;   // the lane's columns: all W, or the first, or none
-    if (cols <= 0) return;
+    const int col = col0 + c;
+    if (!PAIRS && col >= p.n) return;
     float bias[W];
 #pragma unroll
-    for (int t = 0; t < W; ++t) bias[t] = p.bias && t < cols ? __ldg(p.bias + col + t) : 0.f;
+    for (int t = 0; t < W; ++t) bias[t] = p.bias ? __ldg(p.bias + col + t) : 0.f;
     const int64_t row = row0 + r0;
     const __nv_bfloat16* zp = p.Z + row * p.ldz + col;
     const uint8_t* rp = static_cast<const uint8_t*>(p.R) + (row * p.ldr + col) * (F32 ? 4 : 2);
@@ -260,18 +261,15 @@ __device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t st
 #pragma unroll 1
     for (int j = 0; j < 32 / W; j += N) {
         if (W * j >= rows) break;
-        uint32_t z[N], r[N * (F32 ? W : 1)];
+        uint32_t z[N], r[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const bool in = W * (j + i) < rows;
-            if constexpr (kReadZ) z[i] = in ? load_some<W>(zp + W * (j + i) * p.ldz, cols) : 0u;
-            if constexpr (F32) {
-#pragma unroll
-                for (int t = 0; t < W; ++t)
-                    r[i * W + t] = p.R && in && t < cols ? reinterpret_cast<const uint32_t*>(rp)[W * (j + i) * p.ldr + t] : 0u;
-            } else {
-                r[i] = p.R && in ? load_some<W>(reinterpret_cast<const __nv_bfloat16*>(rp) + W * (j + i) * p.ldr, cols) : 0u;
-            }
+            z[i] = r[i] = 0u;
+            if (kReadZ && in) z[i] = load_some<W>(zp + W * (j + i) * p.ldz);
+            if (p.R && in)
+                r[i] = F32 ? reinterpret_cast<const uint32_t*>(rp)[W * (j + i) * p.ldr]
+                           : load_some<W>(reinterpret_cast<const __nv_bfloat16*>(rp) + W * (j + i) * p.ldr);
         }
         float v[N * W];
 #pragma unroll
@@ -285,26 +283,22 @@ __device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t st
             if (p.Z)
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    if (W * (j + i) < rows) store_some<W>(const_cast<__nv_bfloat16*>(zp) + W * (j + i) * p.ldz, cols, v + i * W);
+                    if (W * (j + i) < rows) store_some<W>(const_cast<__nv_bfloat16*>(zp) + W * (j + i) * p.ldz, v + i * W);
         activate_each<ACT, N * W>(v, [&](int i) {
             return kReadZ ? __uint_as_float(i % W ? z[i / W] & 0xffff0000u : z[i / W] << 16) : 0.f;
         });
+        if (p.R)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (p.R)
+            for (int i = 0; i < N * W; ++i)
+                v[i] += F32 ? __uint_as_float(r[i / W]) : __uint_as_float(i % W ? r[i / W] & 0xffff0000u : r[i / W] << 16);
 #pragma unroll
-                for (int t = 0; t < W; ++t)
-                    v[i * W + t] += F32 ? __uint_as_float(r[F32 ? i * W + t : 0]) : __uint_as_float(t ? r[i] & 0xffff0000u : r[i] << 16);
+        for (int i = 0; i < N; ++i)
             if (W * (j + i) < rows) {
-                if constexpr (F32) {
-#pragma unroll
-                    for (int t = 0; t < W; ++t)
-                        if (t < cols) reinterpret_cast<float*>(dp)[W * (j + i) * p.ldd + t] = v[i * W + t];
-                } else {
-                    store_some<W>(reinterpret_cast<__nv_bfloat16*>(dp) + W * (j + i) * p.ldd, cols, v + i * W);
-                }
+                if constexpr (F32)
+                    reinterpret_cast<float*>(dp)[W * (j + i) * p.ldd] = v[i];
+                else
+                    store_some<W>(reinterpret_cast<__nv_bfloat16*>(dp) + W * (j + i) * p.ldd, v + i * W);
             }
-        }
     }
 }
 // Either of them for the block at (row0, col0); rows at or past row_end are
@@ -317,7 +311,7 @@ __device__ __forceinline__ void finish(const LinearParams& p, uint32_t stg, int 
         else finish_ragged<true, ACT, false>(p, stg, lane, row0, row_end, col0);
     } else {
         if (vec) finish_block<false, ACT>(p, stg, lane, row0, row_end, col0);
-        else if (p.pairs) finish_ragged<false, ACT, true>(p, stg, lane, row0, row_end, col0);
+        else if (p.pairs && col0 + 32 <= p.n) finish_ragged<false, ACT, true>(p, stg, lane, row0, row_end, col0);
         else finish_ragged<false, ACT, false>(p, stg, lane, row0, row_end, col0);
     }
 }
