@@ -486,8 +486,8 @@ cudaError_t fwd_aligned(const LayerNormFwd& a, cudaStream_t stream) {
     if (!whole && many && a.d <= 8192 && a.d > 16) {
         RingShape r;
         r.dense = a.ldx == a.d && (!a.R || a.ldr == a.d) && (!a.H || a.ldh == a.d) && a.ldy == a.d;
-        if (r.dense && a.d <= 512) {   // a warp's rows: about 2 KiB
-            r.per = static_cast<int>(std::max<int64_t>(4, std::min<int64_t>(32, 2048 / (std::max(es, ey) * a.d) / 4 * 4)));
+        if (r.dense && a.d <= 512) {   // a warp's rows
+            r.per = rows_of_a_warp(a.d * std::max(es, ey));
             r.team = 32;
             const int j = static_cast<int>((a.d + 31) / 32);
             r.each = j + j % 2;

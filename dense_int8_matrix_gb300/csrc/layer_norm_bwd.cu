@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(256) layer_norm_join_kernel(const LayerNormBwd
 
 // dx: one CTA per row, the row in registers.
 template <typename T, typename TY, int V, bool VEC>
-__global__ void __launch_bounds__(1024) layer_norm_dx_kernel(const LayerNormBwd p, bool wvec) {
+__global__ void __launch_bounds__(1024, 1) layer_norm_dx_kernel(const LayerNormBwd p, bool wvec) {
     __shared__ float red[2][32];
     pdl_launch_dependents();
     pdl_wait();
@@ -636,8 +636,8 @@ Choice choose(const LayerNormBwd& a) {
         if (whole) {
             r.per = kPair;
             team_of(&r, a.d / 8, {2, 1});
-        } else if (r.dense && a.d <= 512) {   // a warp's rows: about 2 KiB
-            r.per = static_cast<int>(std::max<int64_t>(4, std::min<int64_t>(32, 2048 / (std::max(es, ey) * a.d) / 4 * 4)));
+        } else if (r.dense && a.d <= 512) {   // a warp's rows
+            r.per = rows_of_a_warp(a.d * std::max(es, ey));
             r.team = 32;
             const int j = static_cast<int>((a.d + 31) / 32);
             r.each = j + j % 2;
