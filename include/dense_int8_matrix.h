@@ -523,7 +523,8 @@ GEMM_API gemm_status gemm_bf16_linear_plan_for_sms(int32_t form, int64_t m, int6
  * GEMM_FORM_TN 64 or 128, bn 128) or split_k (1, 2, 4 or 8); sums then join
  * in another order.  One plan always gives the same bits.
  * Errors: GEMM_ERR_INVALID_ARG (null pointer, bad plan, pitch too small or
- * above 2^31, unknown type or activation, residual == D with another pitch),
+ * above 2^31, unknown type or activation, residual == D with another pitch,
+ * an output that is an operand or the other output),
  * GEMM_ERR_MISALIGNED (A, B, D, residual, Z or bias not element aligned),
  * GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
  */
@@ -557,7 +558,7 @@ GEMM_API gemm_status gemm_activation_backward(const uint16_t *dY, int64_t lddy, 
  * (rows floats each, may be NULL) are kept for the backward pass.  Pitches in
  * elements; d <= GEMM_NORM_MAX_D; eps >= 0.  A row that holds an infinity or
  * a NaN gives NaN; so does a constant row with eps = 0.
- * Errors: as gemm_norm_f8.
+ * Errors: as gemm_norm_f8; GEMM_ERR_INVALID_ARG also for Y that is X, R or H.
  */
 GEMM_API gemm_status gemm_layer_norm(const void *X, int64_t ldx, const void *R, int64_t ldr, const float *W,
                                      const float *bias, float eps, int32_t x_type, int32_t y_type, int64_t rows,
@@ -574,7 +575,7 @@ GEMM_API gemm_status gemm_layer_norm(const void *X, int64_t ldx, const void *R, 
  * the gradient of X and of R, and may be dR itself, or dY if the types are
  * the same (with that one's pitch).  dW and dbias may be NULL.  Sums are
  * taken in a fixed order: the same call gives the same bits.
- * Errors: as gemm_norm_f8.
+ * Errors: as gemm_norm_f8; GEMM_ERR_INVALID_ARG also for dX that is H.
  */
 GEMM_API gemm_status gemm_layer_norm_backward(const void *dY, int64_t lddy, const void *H, int64_t ldh, const float *W,
                                               const float *mean, const float *rstd, const void *dR, int64_t lddr,
@@ -612,10 +613,11 @@ GEMM_API gemm_status gemm_balance(const void *X, int64_t ldx, int32_t x_type, in
  * Its gradient: with f_e = counts[e] / sum counts (a constant) and p as above
  *   dX[i][e] = dR[i][e] + dloss * coef * experts / T * p[i][e] * (f_e - sum_j f_j p[i][j])
  * lse (which rows are padding; p is formed anew), counts and used as
- * gemm_balance wrote them; dloss: one float on the device.  dR (x_type, may be NULL: 0) is the gradient that reaches the
- * logits by other ways; dX (x_type) may be dR itself (with its pitch).  Rows
- * that are padding, or whose lse is -infinity, get dR (or 0), whatever their
- * logits are.  Errors: as gemm_balance.
+ * gemm_balance wrote them; dloss: one float on the device.  dR (x_type, may
+ * be NULL: 0) is the gradient that reaches the logits by other ways; dX
+ * (x_type) may be dR itself (with its pitch).  Rows that are padding, or whose
+ * lse is -infinity, get dR (or 0), whatever their logits are.
+ * Errors: as gemm_balance; GEMM_ERR_INVALID_ARG also for dX that is X.
  */
 GEMM_API gemm_status gemm_balance_backward(const void *X, int64_t ldx, int32_t x_type, int64_t rows, int32_t experts,
                                            const float *lse, const int32_t *counts, const int32_t *used, float coef,

@@ -161,6 +161,48 @@ def check_backward(rows, d, tx, ty, pad=0, at=0, seed=0):
 
 
 @pytest.mark.parametrize("tx,ty", TYPES)
+@pytest.mark.parametrize("rows,d,pad,at", [
+    (304, 401, 0, 0), (305, 401, 0, 0), (608, 511, 0, 0), (609, 511, 0, 0), (1216, 511, 0, 0), (1217, 500, 3, 1), (2433, 17, 0, 0),
+    (700, 16, 0, 0), (700, 16, 1, 1), (700, 9, 3, 1), (1000, 33, 15, 1), (613, 4088, 0, 0), (613, 4096, 8, 0), (613, 4104, 0, 0),
+    (613, 4097, 0, 0), (620, 8184, 0, 0), (620, 8191, 0, 0), (620, 8192, 1, 0), (620, 8200, 0, 0), (620, 8193, 0, 0)])
+def test_where_the_kernels_change(rows, d, pad, at, tx, ty):
+    x, r, w, b = inputs(rows, d, rows + d, tx)
+    check_forward(x, r, w, b, EPS, tx, ty, pad, at)
+    check_backward(rows, d, tx, ty, pad, at)
+
+
+@pytest.mark.parametrize("tx,ty", [(BF16, BF16), (F32, BF16)])
+@pytest.mark.parametrize("rows,d", [(3, 40), (700, 40), (700, 136), (700, 1032), (700, 5000), (320, 9000)])
+def test_matrices_that_lie_differently(rows, d, tx, ty):
+    # every matrix with a pitch and an offset of its own: the same values as dense ones
+    x, r, w, b = inputs(rows, d, rows + d, tx)
+    dy, dr = R.normal((rows, d), 1, 0.1, ty), R.normal((rows, d), 2, 0.1, tx)
+    _, mean, _, rstd, _ = R.layer_norm(x, r, w, b, EPS, tx)
+    W, bias, M, S = w.cuda(), b.cuda(), mean.float().cuda(), rstd.float().cuda()
+    mats = lambda *m: [R.padded(t, *m[i % len(m)], 7.0) for i, t in enumerate((x, r, x, dy, dy, dr, x))]  # noqa: E731
+    outs = []
+    for places in (((0, 0),), ((8, 0), (1, 1), (0, 0), (3, 2), (8, 8), (0, 0), (5, 3)), ((0, 0), (0, 0), (8, 0), (0, 1), (0, 0), (0, 1), (0, 0))):
+        (X, _), (Rr, _), (H, hbuf), (Y, ybuf), (dY, _), (dR, _), (dX, xbuf) = mats(*places)
+        dW, dB = torch.full((d,), float("nan"), device="cuda"), torch.full((d,), float("nan"), device="cuda")
+        B.gemm_layer_norm(X, Rr, W, bias, EPS, H, torch.empty_like(M), torch.empty_like(S), Y)
+        B.gemm_layer_norm_backward(dY, H, W, M, S, dR, dX, dW, dB)
+        for buf, view in ((hbuf, H), (ybuf, Y), (xbuf, dX)):
+            assert bool((R.outside(buf, view) == 7.0).all())
+        outs.append((H, Y, dX, dW, dB))
+    for other in outs[1:]:
+        assert torch.equal(other[0], outs[0][0])
+        # Sums may be taken in another order.  y and dx: each side is rounded once (half a step each), and the
+        # sums behind them are off by a few 2^-24 of the row's size.  dw and db: each side by rows 2^-24 of the sum
+        # of the terms' sizes, and |xhat| <= sqrt(d).
+        step = 2 * R.HALF_STEP[tx]
+        for got, want, eps in ((other[1], outs[0][1], 2.0 ** -7), (other[2], outs[0][2], max(step, 2.0 ** -12))):
+            assert bool(((got.double() - want.double()).abs() <= eps * (want.double().abs() + 2.0 ** -10 * want.double().abs().max())).all())
+        size = (rows + 64) * 2.0 ** -23 * dy.double().abs().sum(0).cuda()
+        for got, want, most in ((other[3], outs[0][3], d ** 0.5), (other[4], outs[0][4], 1.0)):
+            assert bool(((got.double() - want.double()).abs() <= most * size).all())
+
+
+@pytest.mark.parametrize("tx,ty", TYPES)
 @pytest.mark.parametrize("rows,d", SHAPES + [(5000, 64), (3000, 300), (200, 4104)])
 def test_backward(rows, d, tx, ty):
     check_backward(rows, d, tx, ty)

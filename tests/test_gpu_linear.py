@@ -239,7 +239,7 @@ def test_activation_backward(act, rows, cols):
 
 
 @pytest.mark.parametrize("places", [((0, 0), (1, 0), (0, 0)), ((3, 1), (3, 1), (0, 0)), ((1, 3), (9, 11), (17, 3)), ((5, 2), (5, 3), (5, 2))])
-@pytest.mark.parametrize("rows,cols", [(1, 3), (9, 5), (333, 1), (70, 249), (2100, 33)])
+@pytest.mark.parametrize("rows,cols", [(1, 3), (9, 5), (333, 1), (70, 249), (2100, 33), (150, 777), (440, 334)])
 def test_activation_backward_of_rows_that_lie_otherwise(rows, cols, places):
     # pitches and offsets (pad, at) of dY, Z and dZ, alike modulo eight elements or not
     dy, z = R.normal((rows, cols), 1, 0.1), R.normal((rows, cols), 2, 2.0)

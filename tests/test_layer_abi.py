@@ -131,6 +131,21 @@ def test_balance_backward_refusals(lib):
         assert run(**bad) == MIS, bad
 
 
+def test_outputs_that_are_operands_are_refused(lib):
+    p = B.gemm_bf16_linear_plan_for_sms(16, 24, 24, 152)
+    A, Bm, Z, R, D = (P * i for i in range(1, 6))
+    for a, b, z, r, d in ((D, Bm, Z, R, D), (A, D, Z, R, D), (A, Bm, D, R, D), (A, Bm, A, R, D), (A, Bm, Bm, R, D), (A, Bm, R, R, D)):
+        assert lib.gemm_bf16_linear_run(ctypes.byref(p), a, 24, b, 24, 0, B.GEMM_ACT_SILU, z, 24, r, 24, B.GEMM_OUT_BF16, d, 24, None) == INV
+    act = B.GEMM_ACT_SILU | B.GEMM_ACT_GRADIENT
+    assert lib.gemm_bf16_linear_run(ctypes.byref(p), A, 24, Bm, 24, 0, act, D, 24, R, 24, B.GEMM_OUT_BF16, D, 24, None) == INV
+    X, R, H, Y, W, dW = (P * i for i in range(1, 7))
+    for y, mean, rstd in ((X, 0, 0), (R, 0, 0), (H, 0, 0), (Y, dW, dW)):
+        assert lib.gemm_layer_norm(X, 24, R, 24, W, 0, 1e-5, 1, 1, 16, 24, H, 24, mean, rstd, y, 24, None) == INV
+    for dx, dw in ((H, dW), (Y, W)):
+        assert lib.gemm_layer_norm_backward(X, 24, H, 24, W, P, P, R, 24, 1, 1, 16, 24, dx, 24, dw, W, None) == INV
+    assert lib.gemm_balance_backward(X, 8, 2, 16, 8, P, P, P, 1.0, P, R, 8, X, 8, None) == INV
+
+
 # ------------------------------------------------------------ the binding --
 
 def linear_plan(form):
