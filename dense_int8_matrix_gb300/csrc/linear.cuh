@@ -179,18 +179,21 @@ __device__ __forceinline__ void finish_block(const LinearParams& p, uint32_t stg
     }
 }
 
+__device__ __forceinline__ void ld_shared_pair(uint32_t at, float& a, float& b) {
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(at) : "memory");
+}
 // One bfloat16 value, or two at an even element.
 template <int W>
-__device__ __forceinline__ uint32_t load_some(const __nv_bfloat16* p) {
+__device__ __forceinline__ uint32_t load_some(const uint8_t* p) {
     if constexpr (W == 2) return *reinterpret_cast<const uint32_t*>(p);
     return *reinterpret_cast<const uint16_t*>(p);
 }
 template <int W>
-__device__ __forceinline__ void store_some(__nv_bfloat16* p, const float* v) {
+__device__ __forceinline__ void store_some(uint8_t* p, const float* v) {
     if constexpr (W == 2)
         *reinterpret_cast<uint32_t*>(p) = bf16x2(v[0], v[W - 1]);
     else
-        *p = __float2bfloat16_rn(v[0]);
+        *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(v[0]);
 }
 
 // Asks the L2 for the rows that the epilogue of rows row0 .. row0 + 31 and
@@ -245,7 +248,7 @@ template <bool F32, int ACT, bool PAIRS>
 __device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t stg, int lane, int row0, int row_end, int col0) {
     constexpr bool kReadZ = (ACT & GEMM_ACT_GRADIENT) != 0;
     constexpr int W = PAIRS ? 2 : 1;          // columns of a lane, and rows of an access
-    constexpr int N = 8 / W;                  // accesses in flight; 16 / W: 5 to 10 % slower (1965 x 3842, 594 x 1153), by the size of the code
+    constexpr int N = 8 / W;                  // accesses in flight; twice as many: 5 to 10 % slower, by the size of the code
     static_assert(!(F32 && PAIRS), "fp32 columns are single");
     const int c = PAIRS ? (lane & 15) * 2 : lane, r0 = PAIRS ? lane >> 4 : 0;
     const int col = col0 + c;
@@ -253,37 +256,46 @@ __device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t st
     float bias[W];
 #pragma unroll
     for (int t = 0; t < W; ++t) bias[t] = p.bias ? __ldg(p.bias + col + t) : 0.f;
+    constexpr int ES = F32 ? 4 : 2;
     const int64_t row = row0 + r0;
-    const __nv_bfloat16* zp = p.Z + row * p.ldz + col;
-    const uint8_t* rp = static_cast<const uint8_t*>(p.R) + (row * p.ldr + col) * (F32 ? 4 : 2);
-    uint8_t* dp = static_cast<uint8_t*>(p.D) + (row * p.ldd + col) * (F32 ? 4 : 2);
+    uint8_t* z_at = reinterpret_cast<uint8_t*>(p.Z) + (row * p.ldz + col) * 2;
+    const uint8_t* r_at = static_cast<const uint8_t*>(p.R) + (row * p.ldr + col) * ES;
+    uint8_t* d_at = static_cast<uint8_t*>(p.D) + (row * p.ldd + col) * ES;
+    const int64_t z_step = 2 * W * p.ldz, r_step = ES * W * p.ldr, d_step = ES * W * p.ldd;
     const int rows = row_end - row0 - r0;
+    // (row r0 + W i of the staging buffer: its 16-byte pieces are XORed with the row modulo 8, of which r0 is the
+    // lowest bit or nothing)
+    static_assert(W * N == 8, "j + i is i modulo 8 / W");
+    uint32_t s_at = stg + r0 * 128;
+    const uint32_t piece = (((c >> 2) ^ r0) << 4) + (c & 3) * 4;
 #pragma unroll 1
-    for (int j = 0; j < 32 / W; j += N) {
-        if (W * j >= rows) break;
+    for (int j = 0; j < 32; j += 8, s_at += 8 * 128) {
+        if (j >= rows) break;
         uint32_t z[N], r[N];
+        if constexpr (kReadZ)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const bool in = W * (j + i) < rows;
-            z[i] = r[i] = 0u;
-            if (kReadZ && in) z[i] = load_some<W>(zp + W * (j + i) * p.ldz);
-            if (p.R && in)
-                r[i] = F32 ? reinterpret_cast<const uint32_t*>(rp)[W * (j + i) * p.ldr]
-                           : load_some<W>(reinterpret_cast<const __nv_bfloat16*>(rp) + W * (j + i) * p.ldr);
-        }
+            for (int i = 0; i < N; ++i, z_at += z_step) z[i] = j + W * i < rows ? load_some<W>(z_at) : 0u;
+        if (p.R)
+#pragma unroll
+            for (int i = 0; i < N; ++i, r_at += r_step)
+                r[i] = j + W * i < rows ? (F32 ? *reinterpret_cast<const uint32_t*>(r_at) : load_some<W>(r_at)) : 0u;
         float v[N * W];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int rr = r0 + W * (j + i);
-            const uint32_t at = stg + rr * 128 + (((c >> 2) ^ (rr & 7)) << 4) + (c & 3) * 4;
+            const uint32_t at = s_at + W * i * 128 + (piece ^ (W * i << 4));
+            if constexpr (W == 2) {
+                ld_shared_pair(at, v[2 * i], v[W * i + W - 1]);
+            } else {
+                v[i] = __uint_as_float(ld_shared_u32(at));
+            }
 #pragma unroll
-            for (int t = 0; t < W; ++t) v[i * W + t] = __uint_as_float(ld_shared_u32(at + 4 * t)) + bias[t];
+            for (int t = 0; t < W; ++t) v[i * W + t] += bias[t];
         }
         if constexpr (!kReadZ)
             if (p.Z)
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (W * (j + i) < rows) store_some<W>(const_cast<__nv_bfloat16*>(zp) + W * (j + i) * p.ldz, v + i * W);
+                for (int i = 0; i < N; ++i, z_at += z_step)
+                    if (j + W * i < rows) store_some<W>(z_at, v + i * W);
         activate_each<ACT, N * W>(v, [&](int i) {
             return kReadZ ? __uint_as_float(i % W ? z[i / W] & 0xffff0000u : z[i / W] << 16) : 0.f;
         });
@@ -292,12 +304,12 @@ __device__ __forceinline__ void finish_ragged(const LinearParams& p, uint32_t st
             for (int i = 0; i < N * W; ++i)
                 v[i] += F32 ? __uint_as_float(r[i / W]) : __uint_as_float(i % W ? r[i / W] & 0xffff0000u : r[i / W] << 16);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (W * (j + i) < rows) {
+        for (int i = 0; i < N; ++i, d_at += d_step)
+            if (j + W * i < rows) {
                 if constexpr (F32)
-                    reinterpret_cast<float*>(dp)[W * (j + i) * p.ldd] = v[i];
+                    *reinterpret_cast<float*>(d_at) = v[i];
                 else
-                    store_some<W>(reinterpret_cast<__nv_bfloat16*>(dp) + W * (j + i) * p.ldd, v + i * W);
+                    store_some<W>(d_at, v + i * W);
             }
     }
 }
