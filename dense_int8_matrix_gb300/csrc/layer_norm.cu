@@ -474,7 +474,10 @@ cudaError_t fwd_aligned(const LayerNormFwd& a, cudaStream_t stream) {
     const int64_t es = sizeof(T), ey = sizeof(TY);
     const bool whole = VEC && a.d % 8 == 0;
     const bool many = a.rows > 4 * sms;
-    if (whole && many && a.d > 768 && a.d <= 8192) {
+    // Short rows: one warp's in the ring (two at a time) once there are many of
+    // bfloat16 (87381 x 384: 50 us, 67 by a warp per row; 2000 x 384 5.4, 5.1); fp32 and
+    // up to 768 elements a warp per row (52428 x 640: 64 us, 73 through the ring).
+    if (whole && many && a.d <= 8192 && (a.d > 768 || (es == 2 && a.d > 128 && a.d <= 512 && a.rows >= 32 * sms))) {
         RingShape r;
         r.per = kPair;
         r.dense = 0;

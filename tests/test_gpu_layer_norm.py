@@ -163,7 +163,8 @@ def check_backward(rows, d, tx, ty, pad=0, at=0, seed=0):
 @pytest.mark.parametrize("tx,ty", TYPES)
 @pytest.mark.parametrize("rows,d,pad,at", [
     (304, 401, 0, 0), (305, 401, 0, 0), (608, 511, 0, 0), (609, 511, 0, 0), (1216, 511, 0, 0), (1217, 500, 3, 1), (2433, 17, 0, 0),
-    (700, 16, 0, 0), (700, 16, 1, 1), (700, 9, 3, 1), (1000, 33, 15, 1), (613, 4088, 0, 0), (613, 4096, 8, 0), (613, 4104, 0, 0),
+    (4863, 192, 0, 0), (4865, 136, 0, 0),
+    (4864, 512, 8, 0), (700, 16, 0, 0), (700, 16, 1, 1), (700, 9, 3, 1), (1000, 33, 15, 1), (613, 4088, 0, 0), (613, 4096, 8, 0), (613, 4104, 0, 0),
     (613, 4097, 0, 0), (620, 8184, 0, 0), (620, 8191, 0, 0), (620, 8192, 1, 0), (620, 8200, 0, 0), (620, 8193, 0, 0)])
 def test_where_the_kernels_change(rows, d, pad, at, tx, ty):
     x, r, w, b = inputs(rows, d, rows + d, tx)
