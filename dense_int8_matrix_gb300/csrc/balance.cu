@@ -36,11 +36,6 @@ constexpr int kExpertsPerThread = GEMM_BALANCE_MAX_EXPERTS / kThreads;
 constexpr int kMaxParts = 256;
 static_assert(kLossThreads >= GEMM_BALANCE_MAX_EXPERTS && kMaxParts <= kLossThreads && kLossThreads == 1024, "a thread per expert and per part");
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));   // (volatile: stays behind the barrier)
-    return v;
-}
 __device__ __forceinline__ int32_t ld_cluster_i32(uint32_t addr) {
     int32_t v;
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -282,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, U == 8 ? 2 : 3) balance_rows_kernel(
         if (cluster == 1) return sums[c];
         float v[kCluster], all = 0.f;
 #pragma unroll
-        for (int r = 0; r < kCluster; ++r) v[r] = ld_cluster_f32(peer_address(sums0 + 4 * c, r));
+        for (int r = 0; r < kCluster; ++r) v[r] = load_in_cluster(peer_address(sums0 + 4 * c, r));
 #pragma unroll
         for (int r = 0; r < kCluster; ++r) all += v[r];
         return all;

@@ -70,9 +70,10 @@ def test_dense_layer_step_against_differences():
         assert abs(along - slope) <= 0.02 * got[name].double().norm().item() * way.norm().item() / got[name].numel() ** 0.5 * 3, name
 
 
-def test_dense_layer_step_captured():
+@pytest.mark.parametrize("rows,d,ff", [(333, 136, 520), (700, 99, 333)])
+def test_dense_layer_step_captured(rows, d, ff):
     import dense_layer
-    first, second = dense_layer.inputs(333, 136, 520, seed=1), dense_layer.inputs(333, 136, 520, seed=2)
+    first, second = dense_layer.inputs(rows, d, ff, seed=1), dense_layer.inputs(rows, d, ff, seed=2)
     want = [dense_layer.step(*a) for a in (first, second)]
     graphs = []
     for _ in range(2):   # two graphs of the same step, replayed on two streams at once
