@@ -4,7 +4,10 @@
 //   loss = coef * E * sum(f * P)
 //   dx = dr + dloss * coef * E / T * p * (f - sum(f * p))
 //
-// Bound by DRAM: the logits are read once by each pass.  L lanes (as many as
+// The logits are read once by each pass.  65536 x 256 fp32: forward 25 us (20 of them
+// the rows, bound by instructions and the latency of a row's sums: 20
+// instructions per logit, as long from the L2 as from DRAM), gradient 32 us, 6.3
+// TB/s, bound by DRAM.  L lanes (as many as
 // have sixteen columns each, 32 at most) hold a row, so that a warp takes 32 / L
 // rows at once, whatever the number of experts, and a lane has the same columns
 // of every row: its sums of p stay with it.  (Four columns per lane leave the
