@@ -205,8 +205,8 @@ __device__ __forceinline__ void start_ring(ChunkRing& ring, const LayerNormFwd& 
 
 // Longer aligned rows, many of them: two rows per team from its ring, V vectors
 // of eight values per thread and row.  Bound by DRAM (8192 x 8192 bfloat16 89 us, 6.0
-// TB/s; 32768 x 1024 46 us, 5.8), with the issue slots half used; one row at a time
-// leaves the latency of its two sums open (118 us).
+// TB/s; 32768 x 1024 46 us, 5.8), with the issue slots half used (118 us by a CTA
+// per row, whose two sums nothing hides).
 constexpr int kPair = 2;
 template <typename T, typename TY, int V>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_ring_kernel(const LayerNormFwd p, const RingShape shape, bool wvec, bool bvec) {

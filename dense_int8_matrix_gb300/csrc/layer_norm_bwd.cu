@@ -192,7 +192,7 @@ __device__ __forceinline__ void start_ring(ChunkRing& ring, const LayerNormBwd& 
 // Longer aligned rows: two rows per team from its ring, V vectors of eight
 // values per thread and row, whose w, dw and db stay in registers.  Bound by a
 // row's two sums as much as by DRAM: 4096 x 8192 bfloat16 55 us, 4.8 TB/s (50 without
-// dw and db; 91 one row at a time), 16384 x 2048 fp32 79 us, 6.0 TB/s.
+// dw and db; 91 with one row in a CTA), 16384 x 2048 fp32 79 us, 6.0 TB/s.
 constexpr int kPair = 2;
 template <typename T, typename TY, int V>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_bwd_ring_kernel(const LayerNormBwd p, const RingShape shape, bool wvec) {
@@ -451,23 +451,23 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_bwd_odd_kernel(con
     }
 }
 
-// dW and dbias from the CTAs' sums, both in one launch: a CTA takes eight columns
-// (a sector of 32 bytes of each partial); its 32 groups of eight lanes take every
-// 32nd partial, four loads at a time, and are joined in a fixed order.  Latency:
-// about 4 us of a call.
+// dW and dbias from the CTAs' sums, both in one launch: a CTA takes sixteen
+// columns; its 16 groups of sixteen lanes take every 16th partial, ten loads at a
+// time, and are joined in a fixed order.  Latency: about 4 us of a call (4096 x 8192
+// 56.2 us with sixteen columns, 58.7 with eight, 57.2 with 32).
 __global__ void __launch_bounds__(256) layer_norm_join_kernel(const LayerNormBwd p, int from) {
-    constexpr int kLoads = 4, kGroups = 32;
-    __shared__ float red[8][8];
+    constexpr int kCols = 16, kLoads = 10, kGroups = 256 / kCols;
+    __shared__ float red[8][kCols];
     pdl_launch_dependents();
     pdl_wait();
     const int which = from + static_cast<int>(blockIdx.y);
     const float* partial = p.partial + static_cast<int64_t>(which) * p.parts * p.d;
     float* out = which == 0 ? p.dW : p.dbias;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 8 + (lane & 7);
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kCols + lane % kCols;
     float s = 0.f;
     if (c < p.d) {
-        for (int i = warp * 4 + (lane >> 3); i < p.parts; i += kLoads * kGroups) {
+        for (int i = static_cast<int>(threadIdx.x) / kCols; i < p.parts; i += kLoads * kGroups) {
             float v[kLoads];
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
@@ -476,11 +476,11 @@ __global__ void __launch_bounds__(256) layer_norm_join_kernel(const LayerNormBwd
             for (int j = 0; j < kLoads; ++j) s += v[j];
         }
     }
-    s += __shfl_xor_sync(0xffffffffu, s, 8);
-    s += __shfl_xor_sync(0xffffffffu, s, 16);
-    if (lane < 8) red[warp][lane] = s;
+#pragma unroll
+    for (int o = kCols; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane < kCols) red[warp][lane] = s;
     __syncthreads();
-    if (threadIdx.x < 8 && c < p.d) {
+    if (threadIdx.x < kCols && c < p.d) {
         s = red[0][lane];
 #pragma unroll
         for (int i = 1; i < 8; ++i) s += red[i][lane];
@@ -754,7 +754,7 @@ cudaError_t bwd_type(const LayerNormBwd& a, cudaStream_t stream, int* launches) 
     if (e != cudaSuccess) return e;
     ++*launches;
     if (a.parts == 1 || !(a.dW || a.dbias)) return cudaSuccess;
-    const dim3 grid(static_cast<unsigned>((a.d + 7) / 8), a.dW && a.dbias ? 2 : 1);
+    const dim3 grid(static_cast<unsigned>((a.d + 15) / 16), a.dW && a.dbias ? 2 : 1);
     e = launch_chained(layer_norm_join_kernel, grid, 256, 0, stream, a, a.dW ? 0 : 1);
     if (e == cudaSuccess) ++*launches;
     return e;
