@@ -191,7 +191,7 @@ __device__ __forceinline__ void start_ring(ChunkRing& ring, const LayerNormBwd& 
 
 // Longer aligned rows: two rows per team from its ring, V vectors of eight
 // values per thread and row, whose w, dw and db stay in registers.  Bound by a
-// row's two sums as much as by DRAM: 4096 x 8192 bfloat16 55 us, 4.8 TB/s (50 without
+// row's two sums as much as by DRAM: 4096 x 8192 bfloat16 54 us, 5.0 TB/s (50 without
 // dw and db; 91 with one row in a CTA), 16384 x 2048 fp32 79 us, 6.0 TB/s.
 constexpr int kPair = 2;
 template <typename T, typename TY, int V>
