@@ -4,7 +4,8 @@
 //
 // Bound by DRAM.  The variance is taken of h - mean, not of h^2: the row is in
 // registers, so the second pass costs no memory traffic, and a mean far from
-// zero cancels nothing.  Rows come through a ring of bulk copies where there are
+// zero cancels nothing.  That pass also gives the mean's own rounding error
+// (settle).  Rows come through a ring of bulk copies where there are
 // many and they are longer, or not aligned; short aligned rows take a warp, or part
 // of one, each; few rows a CTA each.
 #include <algorithm>
@@ -26,6 +27,15 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     return warp_sum((threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f);
+}
+__device__ __forceinline__ float2 cta_sum(float2 v, float2* red) {
+    v = make_float2(warp_sum(v.x), warp_sum(v.y));
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : make_float2(0.f, 0.f);
+    return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -52,17 +62,34 @@ __device__ __forceinline__ float sum8(const Vec8<T>& x) {
     for (int i = 0; i < 8; ++i) s += a[i];
     return s;
 }
-// Sum of (h - mean)^2 over the eight values that lie in the row.
+// Sums of h - mean and of its square over the eight values that lie in the row.
 template <typename T>
-__device__ __forceinline__ float squares8(const Vec8<T>& x, float mean, int64_t c, int64_t d) {
-    float a[8], s = 0.f;
+__device__ __forceinline__ float2 residuals8(const Vec8<T>& x, float mean, int64_t c, int64_t d) {
+    float a[8];
+    float2 s = make_float2(0.f, 0.f);
     x.get(a);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float e = c + i < d ? a[i] - mean : 0.f;
-        s += e * e;
+        s.x += e;
+        s.y += e * e;
     }
     return s;
+}
+// A row's rstd from the sums of e = h - mean and of e^2, and its mean without the
+// rounding error of the sum that it came from: that error is the mean of e.
+//   mean' = mean + off,  sum (h - mean')^2 = sum e^2 - 2 off sum e + d off^2,
+// less d rest^2 for what the rounding of mean' leaves.  In a constant row every e
+// is k units in the last place, k <= 22 (as many roundings lead to the mean, each
+// of half a unit at most), and k^2 d < 2^24: both sums are exact, mean' is the
+// value itself, and y = bias whatever the value, d and the kernel are.  (The
+// rounded mean alone: a row of 1000 with d = 776 gave 0.019 W.)
+__device__ __forceinline__ void settle(float sum, float squares, float d, float inv_d, float eps, float& mean, float& rstd) {
+    const float all = __fmul_rn(sum, inv_d), to = mean + all, off = to - mean, rest = all - off;
+    float q = fmaf(off, fmaf(d, off, -2.f * sum), squares);
+    q = fmaf(-d * rest, rest, q);
+    mean = to;
+    rstd = 1.f / sqrtf((q < 0.f ? 0.f : q * inv_d) + eps);   // (NaN stays)
 }
 template <typename T, typename TY>
 __device__ __forceinline__ Vec8<TY> normed(const Vec8<T>& x, float mean, float rstd, const float (&w)[8], const float (&b)[8]) {
@@ -83,13 +110,14 @@ __device__ __forceinline__ void load_wb(const LayerNormFwd& p, int64_t c, bool w
 
 // One CTA per row, or (WARP) a warp per row: V vectors of eight values per
 // thread, vector v of thread t at column 8 * (v * threads + t).  Bound by latency
-// (1 x 8192 3.2 us); with long rows one CTA's loads wait for its two sums: 2048 x
-// 16384 bfloat16 76 us, 3.5 TB/s.  A warp per row: 43690 x 768 55 us, 4.9 TB/s
+// (1 x 8192 3.4 us); with long rows one CTA's loads wait for its sums: 2048 x
+// 16384 bfloat16 77 us, 3.5 TB/s.  A warp per row: 43690 x 768 54 us, 5.0 TB/s
 // (fp32 70 us, 6.7 TB/s).
 constexpr int kWarpThreads = 256;
 template <typename T, typename TY, int V, bool VEC, bool WARP>
 __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) layer_norm_fwd_kernel(const LayerNormFwd p, bool wvec, bool bvec) {
-    __shared__ float red[2][32];
+    __shared__ float red[32];
+    __shared__ float2 red2[32];
     pdl_launch_dependents();
     pdl_wait();
     const int t = WARP ? threadIdx.x & 31 : threadIdx.x, nt = WARP ? 32 : blockDim.x;
@@ -108,12 +136,17 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) layer_norm_fwd_ker
         if (p.H) store8<VEC>(static_cast<T*>(p.H) + row * p.ldh, column(v), p.d, h[v]);
         sum += sum8(h[v]);   // (columns past the row are zero)
     }
-    const float mean = (WARP ? warp_sum(sum) : cta_sum(sum, red[0])) / static_cast<float>(p.d);
-    float ss = 0.f;
+    const float d = static_cast<float>(p.d), inv_d = 1.f / d;
+    float mean = __fmul_rn(WARP ? warp_sum(sum) : cta_sum(sum, red), inv_d), rstd;   // (rounded: settle counts on it)
+    float2 e = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int v = 0; v < V; ++v) ss += squares8(h[v], mean, column(v), p.d);
-    ss = WARP ? warp_sum(ss) : cta_sum(ss, red[1]);
-    const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
+    for (int v = 0; v < V; ++v) {
+        const float2 s = residuals8(h[v], mean, column(v), p.d);
+        e.x += s.x;
+        e.y += s.y;
+    }
+    e = WARP ? make_float2(warp_sum(e.x), warp_sum(e.y)) : cta_sum(e, red2);
+    settle(e.x, e.y, d, inv_d, p.eps, mean, rstd);
     if (t == 0) {
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
@@ -128,7 +161,7 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) layer_norm_fwd_ker
 
 // Short aligned rows: L lanes hold a row (eight values each), 32 / L rows per
 // warp, w and b in registers, and the next rows on their way while these are
-// worked on.  Bound by DRAM: 524288 x 64 and 262144 x 128 bfloat16 52 us, 5.2 TB/s.
+// worked on.  Bound by DRAM: 524288 x 64 and 262144 x 128 bfloat16 47 us, 5.7 TB/s.
 template <typename T, typename TY, int L>
 __global__ void __launch_bounds__(kWarpThreads) layer_norm_fwd_warp_kernel(const LayerNormFwd p, bool wvec, bool bvec) {
     constexpr int kRows = 32 / L, V = 1;
@@ -140,7 +173,7 @@ __global__ void __launch_bounds__(kWarpThreads) layer_norm_fwd_warp_kernel(const
     float w[V][8], b[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) load_wb(p, column(v), wvec, bvec, w[v], b[v]);
-    const float inv_d = 1.f / static_cast<float>(p.d);
+    const float d = static_cast<float>(p.d), inv_d = 1.f / d;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kWarpThreads / 32) * kRows;
     int64_t first = (static_cast<int64_t>(blockIdx.x) * (kWarpThreads / 32) + (threadIdx.x >> 5)) * kRows;
     Vec8<T> x[V], r[V];
@@ -168,11 +201,15 @@ __global__ void __launch_bounds__(kWarpThreads) layer_norm_fwd_warp_kernel(const
             sum += sum8(h[v]);
         }
         fetch(row + step);
-        const float mean = lanes_sum<L>(sum) * inv_d;
-        float ss = 0.f;
+        float mean = __fmul_rn(lanes_sum<L>(sum), inv_d), rstd;
+        float2 e = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) ss += squares8(h[v], mean, column(v), p.d);
-        const float rstd = 1.f / sqrtf(lanes_sum<L>(ss) * inv_d + p.eps);
+        for (int v = 0; v < V; ++v) {
+            const float2 s = residuals8(h[v], mean, column(v), p.d);
+            e.x += s.x;
+            e.y += s.y;
+        }
+        settle(lanes_sum<L>(e.x), lanes_sum<L>(e.y), d, inv_d, p.eps, mean, rstd);
         if (!mine) continue;
         if (l == 0) {
             if (p.mean) p.mean[row] = mean;
@@ -204,14 +241,15 @@ __device__ __forceinline__ void start_ring(ChunkRing& ring, const LayerNormFwd& 
 }
 
 // Longer aligned rows, many of them: two rows per team from its ring, V vectors
-// of eight values per thread and row.  Bound by DRAM (8192 x 8192 bfloat16 89 us, 6.0
-// TB/s; 32768 x 1024 46 us, 5.8), with the issue slots half used (118 us by a CTA
+// of eight values per thread and row.  Bound by DRAM (8192 x 8192 bfloat16 85 us, 6.3
+// TB/s; 32768 x 1024 47 us, 5.7), with the issue slots half used (118 us by a CTA
 // per row, whose two sums nothing hides).
 constexpr int kPair = 2;
 template <typename T, typename TY, int V>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_ring_kernel(const LayerNormFwd p, const RingShape shape, bool wvec, bool bvec) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 red[2][kRingThreads / 32];
+    __shared__ float2 red[kRingThreads / 32];
+    __shared__ float4 red4[kRingThreads / 32];
     __shared__ __align__(8) uint64_t bars[kRingThreads / 32][ChunkRing::kSlots];
     __shared__ uint32_t abort_flag;
     const int d = static_cast<int>(p.d), lane = threadIdx.x & 31;
@@ -238,17 +276,26 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_ring_kernel(co
             b[v].p[i] = pair_of(__float_as_uint(g[2 * i]), __float_as_uint(g[2 * i + 1]));
         }
     }
-    // the sums of both rows over the team
-    auto sums = [&](uint64_t x, uint64_t y, float2* at) {
+    // sums of both rows over the team
+    auto sums = [&](uint64_t x, uint64_t y) {
         float2 v = make_float2(warp_sum(sum_of(x)), warp_sum(sum_of(y)));
         if (team.warps == 1) {
             __syncwarp();
             return v;
         }
-        if (lane == 0) at[threadIdx.x >> 5] = v;
+        if (lane == 0) red[threadIdx.x >> 5] = v;
         team.sync();
-        v = lane < team.warps ? at[team.id * team.warps + lane] : make_float2(0.f, 0.f);
+        v = lane < team.warps ? red[team.id * team.warps + lane] : make_float2(0.f, 0.f);
         return make_float2(warp_sum(v.x), warp_sum(v.y));
+    };
+    auto sums4 = [&](const uint64_t (&x)[kPair], const uint64_t (&y)[kPair]) {
+        auto warps = [](const float4& v) { return make_float4(warp_sum(v.x), warp_sum(v.y), warp_sum(v.z), warp_sum(v.w)); };
+        float4 v = warps(make_float4(sum_of(x[0]), sum_of(y[0]), sum_of(x[1]), sum_of(y[1])));
+        if (team.warps == 1) return v;
+        if (lane == 0) red4[threadIdx.x >> 5] = v;
+        team.sync();
+        v = lane < team.warps ? red4[team.id * team.warps + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        return warps(v);
     };
     const float inv_d = 1.f / static_cast<float>(d);
     int s = 0;
@@ -282,9 +329,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_ring_kernel(co
                 for (int i = 0; i < 4; ++i) part[r] = add2(part[r], x.p[i]);
             }
         }
-        const float2 total = sums(part[0], part[1], red[0]);
+        const float2 total = sums(part[0], part[1]);
         if (team.thread == 0) ring.fill(c + shape.slots * ring.by, s);   // the whole team has read the slot
-        const float mean[kPair] = {total.x * inv_d, total.y * inv_d};
+        float mean[kPair] = {__fmul_rn(total.x, inv_d), __fmul_rn(total.y, inv_d)}, rstd[kPair];
+        uint64_t square[kPair] = {0, 0};
         part[0] = part[1] = 0;
 #pragma unroll
         for (int r = 0; r < kPair; ++r) {
@@ -297,12 +345,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_ring_kernel(co
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint64_t e = add2(x.p[i], minus);
-                    part[r] = fma2(e, e, part[r]);
+                    part[r] = add2(part[r], e);
+                    square[r] = fma2(e, e, square[r]);
                 }
             }
         }
-        const float2 ss = sums(part[0], part[1], red[1]);
-        const float rstd[kPair] = {1.f / sqrtf(ss.x * inv_d + p.eps), 1.f / sqrtf(ss.y * inv_d + p.eps)};
+        const float4 e = sums4(part, square);
+        settle(e.x, e.y, static_cast<float>(d), inv_d, p.eps, mean[0], rstd[0]);
+        settle(e.z, e.w, static_cast<float>(d), inv_d, p.eps, mean[1], rstd[1]);
 #pragma unroll
         for (int r = 0; r < kPair; ++r) {
             if (r >= n) break;
@@ -332,13 +382,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_ring_kernel(co
 // between each value is taken by itself, neighbouring lanes neighbouring values,
 // J values per thread and row.  Dense short rows: a warp per team, which takes
 // several rows at a time.  Bound by the instructions that each value takes and
-// the rows' sums: 33520 x 1001 bfloat16 90 us, 3.0 TB/s, 4096 x 8191 87 us (137 by a CTA
-// per row), 516222 x 65 193 us, 1.4 TB/s; 20919 x 401 fp32 31 us, 4.3 TB/s.
+// the rows' sums: 33520 x 1001 bfloat16 94 us, 2.9 TB/s, 4096 x 8191 90 us (137 by a CTA
+// per row), 516222 x 65 204 us, 1.3 TB/s; 20919 x 401 fp32 32 us, 4.2 TB/s.  (Of that the
+// mean's correction is 1 to 6 %.)
 template <typename T, typename TY, int J>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_odd_kernel(const LayerNormFwd p, const RingShape shape) {
     extern __shared__ __align__(16) uint8_t smem[];
     constexpr int kRows = rows_together(J);
-    __shared__ float red[2][kRingThreads / 32 * kRows];
+    __shared__ float red[kRingThreads / 32 * kRows], red2[2 * (kRingThreads / 32 * kRows)];
     __shared__ __align__(8) uint64_t bars[kRingThreads / 32][ChunkRing::kSlots];
     __shared__ uint32_t abort_flag;
     const int d = static_cast<int>(p.d), lane = threadIdx.x & 31;
@@ -385,7 +436,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_odd_kernel(con
         };
         for (int r0 = 0; r0 < n; r0 += kRows) {
             uint64_t a[kRows][P];
-            float mean[kRows], rstd[kRows];
+            float mean[kRows], rstd[kRows], e2[2 * kRows];
 #pragma unroll
             for (int q = 0; q < kRows; ++q) {
                 mean[q] = 0.f;
@@ -404,36 +455,39 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_odd_kernel(con
                 }
                 mean[q] = sum_of(sum2);
             }
-            team.sum(mean, red[0]);
+            team.sum(mean, red);
 #pragma unroll
             for (int q = 0; q < kRows; ++q) {
-                rstd[q] = 0.f;
+                e2[2 * q] = e2[2 * q + 1] = 0.f;
                 if (r0 + q >= n) continue;
-                mean[q] *= inv_d;
+                mean[q] = __fmul_rn(mean[q], inv_d);
                 const uint64_t minus = both(-mean[q]);
-                uint64_t ss2 = 0;
+                uint64_t sum2 = 0, ss2 = 0;
 #pragma unroll
                 for (int i = 0; i < P; ++i) {
                     // (a value past the row stays zero)
                     a[q][i] = add2(a[q][i], pair_of(in(2 * i) ? static_cast<uint32_t>(minus) : 0u, in(2 * i + 1) ? static_cast<uint32_t>(minus) : 0u));
+                    sum2 = add2(sum2, a[q][i]);
                     ss2 = fma2(a[q][i], a[q][i], ss2);
                 }
-                rstd[q] = sum_of(ss2);
+                e2[2 * q] = sum_of(sum2);
+                e2[2 * q + 1] = sum_of(ss2);
             }
-            team.sum(rstd, red[1]);
+            team.sum(e2, red2);
 #pragma unroll
             for (int q = 0; q < kRows; ++q) {
                 if (r0 + q >= n) continue;
-                rstd[q] = 1.f / sqrtf(rstd[q] * inv_d + p.eps);
+                const float before = mean[q];
+                settle(e2[2 * q], e2[2 * q + 1], static_cast<float>(d), inv_d, p.eps, mean[q], rstd[q]);
                 if (first == 0) {
                     if (p.mean) p.mean[row0 + r0 + q] = mean[q];
                     if (p.rstd) p.rstd[row0 + r0 + q] = rstd[q];
                 }
                 TY* y = reinterpret_cast<TY*>(y_at(r0 + q)) + first;
-                const uint64_t scale = both(rstd[q]);
+                const uint64_t scale = both(rstd[q]), minus = both(before - mean[q]);
 #pragma unroll
                 for (int i = 0; i < P; ++i)
-                    put_pair(fma2(mul2(a[q][i], scale), w[i], b[i]), y + 2 * i * stride, stride, in(2 * i), in(2 * i + 1));
+                    put_pair(fma2(mul2(add2(a[q][i], minus), scale), w[i], b[i]), y + 2 * i * stride, stride, in(2 * i), in(2 * i + 1));
             }
         }
         // What was staged leaves; the buffer before it has been read by then.
@@ -482,7 +536,7 @@ cudaError_t fwd_aligned(const LayerNormFwd& a, cudaStream_t stream) {
     const bool whole = VEC && a.d % 8 == 0;
     const bool many = a.rows > 4 * sms;
     // Short rows: one warp's in the ring (two at a time) once there are many of
-    // bfloat16 (87381 x 384: 50 us, 67 by a warp per row; 2000 x 384 5.4, 5.1); fp32 and
+    // bfloat16 (87381 x 384: 51 us, 67 by a warp per row; 2000 x 384 5.4, 5.1); fp32 and
     // up to 768 elements a warp per row (52428 x 640: 64 us, 73 through the ring).
     if (whole && many && a.d <= 8192 && (a.d > 768 || (es == 2 && a.d > 128 && a.d <= 512 && a.rows >= 32 * sms))) {
         RingShape r;

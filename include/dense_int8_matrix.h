@@ -556,8 +556,10 @@ GEMM_API gemm_status gemm_activation_backward(const uint16_t *dY, int64_t lddy, 
  * W: d floats; bias: d floats or NULL.  H (x_type; may be NULL if R is NULL)
  * gets h and may be X or R itself (with that one's pitch).  mean and rstd
  * (rows floats each, may be NULL) are kept for the backward pass.  Pitches in
- * elements; d <= GEMM_NORM_MAX_D; eps >= 0.  A row that holds an infinity or
- * a NaN gives NaN; so does a constant row with eps = 0.
+ * elements; d <= GEMM_NORM_MAX_D; eps >= 0.  The mean is corrected by the mean
+ * of h - mean, so that its error goes by the row's spread, not by its size, and
+ * a constant row gives Y = bias exactly (NaN with eps = 0; magnitudes to 1e22).
+ * A row that holds an infinity or a NaN gives NaN.
  * Errors: as gemm_norm_f8; GEMM_ERR_INVALID_ARG also for Y that is X, R or H.
  */
 GEMM_API gemm_status gemm_layer_norm(const void *X, int64_t ldx, const void *R, int64_t ldr, const float *W,
