@@ -3,6 +3,7 @@
 
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <initializer_list>
 
 #include "context.h"
 
@@ -17,6 +18,18 @@ inline bool pitch_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= (int
 inline int elem_bytes(int type) { return type == GEMM_DTYPE_BF16 ? 2 : 4; }
 inline bool real_type(int type) { return type == GEMM_DTYPE_BF16 || type == GEMM_DTYPE_F32; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// No output (nullptr: none) is one of the operands, or another output.
+inline bool apart(std::initializer_list<const void*> outputs, std::initializer_list<const void*> operands) {
+    for (const void* const* o = outputs.begin(); o != outputs.end(); ++o) {
+        if (!*o) continue;
+        for (const void* p : operands)
+            if (*o == p) return false;
+        for (const void* const* other = outputs.begin(); other != o; ++other)
+            if (*o == *other) return false;
+    }
+    return true;
+}
 
 // One timed unit of kind GEMM_KERNEL_STAGE.
 template <typename Launch>

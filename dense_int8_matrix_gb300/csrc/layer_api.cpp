@@ -161,7 +161,8 @@ gemm_status gemm_bf16_linear_run(const gemm_plan_linear* plan, const uint16_t* A
     if (residual == D && ldr != ldd) return GEMM_ERR_INVALID_ARG;
     const uintptr_t es = out_type == GEMM_OUT_F32 ? 4 : 2;
     if (!al(A, 2) || !al(B, 2) || !al(Z, 2) || !al(D, es) || !al(residual, es) || !al(bias, 4)) return GEMM_ERR_MISALIGNED;
-    if (D == A || D == B || D == Z || (Z && !grad && (Z == A || Z == B || Z == residual))) return GEMM_ERR_INVALID_ARG;
+    const void* const z_out = grad ? nullptr : Z;
+    if (!apart({D, z_out}, {A, B, bias}) || D == Z || (z_out && z_out == residual)) return GEMM_ERR_INVALID_ARG;
     DeviceContext ctx;
     const gemm_status st = device_context(&ctx);
     if (st != GEMM_OK) return st;
@@ -233,6 +234,7 @@ gemm_status gemm_activation_backward(const uint16_t* dY, int64_t lddy, const uin
     if (!pitch_ok(lddy, cols) || (Z && !pitch_ok(ldz, cols)) || (dZ && !pitch_ok(lddz, cols))) return GEMM_ERR_INVALID_ARG;
     if ((dZ == dY && lddz != lddy) || (dZ && dZ == Z && lddz != ldz)) return GEMM_ERR_INVALID_ARG;
     if (!al(dY, 2) || !al(Z, 2) || !al(dZ, 2) || !al(dbias, 4)) return GEMM_ERR_MISALIGNED;
+    if (!apart({dbias}, {dY, Z, dZ})) return GEMM_ERR_INVALID_ARG;
     DeviceContext ctx;
     const gemm_status st = device_context(&ctx);
     if (st != GEMM_OK) return st;
@@ -277,7 +279,7 @@ gemm_status gemm_layer_norm(const void* X, int64_t ldx, const void* R, int64_t l
     if (!al(X, es) || !al(R, es) || !al(H, es) || !al(Y, elem_bytes(y_type)) || !al(W, 4) || !al(bias, 4) || !al(mean, 4) ||
         !al(rstd, 4))
         return GEMM_ERR_MISALIGNED;
-    if (Y == X || Y == R || Y == H || (mean && mean == rstd)) return GEMM_ERR_INVALID_ARG;
+    if (!apart({H, mean, rstd, Y}, {W, bias}) || !apart({mean, rstd, Y}, {X, R})) return GEMM_ERR_INVALID_ARG;
     DeviceContext ctx;
     const gemm_status st = device_context(&ctx);
     if (st != GEMM_OK) return st;
@@ -319,7 +321,7 @@ gemm_status gemm_layer_norm_backward(const void* dY, int64_t lddy, const void* H
     if (!al(dY, elem_bytes(y_type)) || !al(H, es) || !al(dR, es) || !al(dX, es) || !al(W, 4) || !al(mean, 4) ||
         !al(rstd, 4) || !al(dW, 4) || !al(dbias, 4))
         return GEMM_ERR_MISALIGNED;
-    if (dX == H || (dW && dW == dbias)) return GEMM_ERR_INVALID_ARG;
+    if (!apart({dX, dW, dbias}, {H, W, mean, rstd}) || !apart({dW, dbias}, {dY, dR})) return GEMM_ERR_INVALID_ARG;
     DeviceContext ctx;
     const gemm_status st = device_context(&ctx);
     if (st != GEMM_OK) return st;
@@ -369,6 +371,7 @@ gemm_status gemm_balance(const void* X, int64_t ldx, int32_t x_type, int64_t row
                           static_cast<const void*>(loss)})
         if (!al(p, 4)) return GEMM_ERR_MISALIGNED;
     if (!al(X, elem_bytes(x_type))) return GEMM_ERR_MISALIGNED;
+    if (!apart({counts, offsets, used, lse, probs, loss}, {X, index})) return GEMM_ERR_INVALID_ARG;
     DeviceContext ctx;
     const gemm_status st = device_context(&ctx);
     if (st != GEMM_OK) return st;
@@ -416,7 +419,7 @@ gemm_status gemm_balance_backward(const void* X, int64_t ldx, int32_t x_type, in
     const int es = elem_bytes(x_type);
     if (!al(X, es) || !al(dR, es) || !al(dX, es) || !al(lse, 4) || !al(counts, 4) || !al(used, 4) || !al(dloss, 4))
         return GEMM_ERR_MISALIGNED;
-    if (dX == X) return GEMM_ERR_INVALID_ARG;
+    if (!apart({dX}, {X, lse, counts, used, dloss})) return GEMM_ERR_INVALID_ARG;
     DeviceContext ctx;
     const gemm_status st = device_context(&ctx);
     if (st != GEMM_OK) return st;

@@ -540,8 +540,8 @@ GEMM_API gemm_status gemm_bf16_linear_run(const gemm_plan_linear *plan, const ui
  * GEMM_ACT_NONE.  dZ or dbias may be NULL, not both; dZ may be dY or Z itself
  * (with its pitch).  Sums are taken in a fixed order.
  * Errors: GEMM_ERR_INVALID_ARG (null pointer, size outside [1, 2^30], pitch,
- * unknown activation, dZ in place with another pitch), GEMM_ERR_MISALIGNED
- * (not element aligned), GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
+ * unknown activation, dZ in place with another pitch, dbias that is dY, Z or
+ * dZ), GEMM_ERR_MISALIGNED (not element aligned), GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
  */
 GEMM_API gemm_status gemm_activation_backward(const uint16_t *dY, int64_t lddy, const uint16_t *Z, int64_t ldz,
                                               int32_t activation, int64_t rows, int64_t cols, uint16_t *dZ,
@@ -560,7 +560,8 @@ GEMM_API gemm_status gemm_activation_backward(const uint16_t *dY, int64_t lddy, 
  * of h - mean, so that its error goes by the row's spread, not by its size, and
  * a constant row gives Y = bias exactly (NaN with eps = 0; magnitudes to 1e22).
  * A row that holds an infinity or a NaN gives NaN.
- * Errors: as gemm_norm_f8; GEMM_ERR_INVALID_ARG also for Y that is X, R or H.
+ * Errors: as gemm_norm_f8; GEMM_ERR_INVALID_ARG also for any other output that
+ * is an operand or another output.
  */
 GEMM_API gemm_status gemm_layer_norm(const void *X, int64_t ldx, const void *R, int64_t ldr, const float *W,
                                      const float *bias, float eps, int32_t x_type, int32_t y_type, int64_t rows,
@@ -577,7 +578,8 @@ GEMM_API gemm_status gemm_layer_norm(const void *X, int64_t ldx, const void *R, 
  * the gradient of X and of R, and may be dR itself, or dY if the types are
  * the same (with that one's pitch).  dW and dbias may be NULL.  Sums are
  * taken in a fixed order: the same call gives the same bits.
- * Errors: as gemm_norm_f8; GEMM_ERR_INVALID_ARG also for dX that is H.
+ * Errors: as gemm_norm_f8; GEMM_ERR_INVALID_ARG also for any other output that
+ * is an operand or another output.
  */
 GEMM_API gemm_status gemm_layer_norm_backward(const void *dY, int64_t lddy, const void *H, int64_t ldh, const float *W,
                                               const float *mean, const float *rstd, const void *dR, int64_t lddr,
@@ -604,8 +606,8 @@ GEMM_API gemm_status gemm_layer_norm_backward(const void *dY, int64_t lddy, cons
  * Sums are taken in a fixed order.
  * Errors: GEMM_ERR_INVALID_ARG (null pointer; rows outside [1, 2^30];
  * experts outside [1, GEMM_BALANCE_MAX_EXPERTS]; top_k below 1; rows * top_k
- * above 2^31 - 1; pitch; unknown type), GEMM_ERR_MISALIGNED (not element
- * aligned), GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
+ * above 2^31 - 1; pitch; unknown type; an output that is an operand or another
+ * output), GEMM_ERR_MISALIGNED (not element aligned), GEMM_ERR_UNSUPPORTED_DEVICE, GEMM_ERR_CUDA.
  */
 GEMM_API gemm_status gemm_balance(const void *X, int64_t ldx, int32_t x_type, int64_t rows, int32_t experts,
                                   const int32_t *index, int32_t top_k, float coef, int32_t *counts, int32_t *offsets,
@@ -619,7 +621,7 @@ GEMM_API gemm_status gemm_balance(const void *X, int64_t ldx, int32_t x_type, in
  * be NULL: 0) is the gradient that reaches the logits by other ways; dX
  * (x_type) may be dR itself (with its pitch).  Rows that are padding, or whose
  * lse is -infinity, get dR (or 0), whatever their logits are.
- * Errors: as gemm_balance; GEMM_ERR_INVALID_ARG also for dX that is X.
+ * Errors: as gemm_balance; dR is the only operand that dX may be.
  */
 GEMM_API gemm_status gemm_balance_backward(const void *X, int64_t ldx, int32_t x_type, int64_t rows, int32_t experts,
                                            const float *lse, const int32_t *counts, const int32_t *used, float coef,
