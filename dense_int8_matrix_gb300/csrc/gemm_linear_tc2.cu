@@ -341,9 +341,13 @@ bool encode_operand(CUtensorMap* map, const LinearLaunch& a, bool is_b, int box_
 // K steps that are added up in TMEM.  Relative error of sums of products of normal
 // values, fp32 output, against 64 bits: 4096 products in one chunk 4.4e-6 (a
 // plain fp32 matrix product 6e-7), 131072 1.5e-4, and 8e-4 if all are positive;
-// chunks of 512 keep it near 6e-7.  bfloat16 outputs are rounded to 2e-3, so
-// theirs need only stay short of that.
-int chunk_of(const LinearLaunch& a) { return (a.out_f32 ? 512 : 2048) / kLinBK; }
+// chunks of 512 keep it near 6e-7.  Small tiles take chunks of 512 whatever the
+// output (at most 2 % longer).  The two-SM tiles take 2048 for bfloat16 outputs, whose
+// rounding is 2e-3: reading an accumulator costs the MMAs a quarter of a
+// microsecond (8192^3 571 us with 2048, 575 with 1024, 612 with 512; 4096^3 with GELU and
+// residual 90, 100, 110), and what it saves, 5e-6 of a sum of positive products
+// against 1e-6, changes one in a thousand of the outputs by their last bit.
+int chunk_of(const LinearLaunch& a) { return (a.out_f32 || a.bm < 256 ? 512 : 2048) / kLinBK; }
 
 LinearParams linear_params(const LinearLaunch& a, int bm, int bn) {
     LinearParams p;
