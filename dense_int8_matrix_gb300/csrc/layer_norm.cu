@@ -244,7 +244,6 @@ __device__ __forceinline__ void start_ring(ChunkRing& ring, const LayerNormFwd& 
 // of eight values per thread and row.  Bound by DRAM (8192 x 8192 bfloat16 85 us, 6.3
 // TB/s; 32768 x 1024 47 us, 5.7), with the issue slots half used (118 us by a CTA
 // per row, whose two sums nothing hides).
-constexpr int kPair = 2;
 template <typename T, typename TY, int V>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_fwd_ring_kernel(const LayerNormFwd p, const RingShape shape, bool wvec, bool bvec) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -521,8 +520,17 @@ bool al16(const void* p, int64_t pitch_bytes) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && pitch_bytes % 16 == 0;
 }
 
+// Bytes of a slot and of a team's staging buffers (unaligned rows: two of them).
+template <typename T>
+int64_t slot_bytes(const LayerNormFwd& a, int per, bool dense) { return (a.R ? 2 : 1) * ChunkRing::place(a.d * sizeof(T), per, dense); }
+template <typename T, typename TY>
+int64_t out_bytes(const LayerNormFwd& a, int per, bool dense) {
+    return 2 * (ChunkRing::place(a.d * sizeof(TY), per, dense) + (a.H ? ChunkRing::place(a.d * sizeof(T), per, dense) : 0));
+}
+
 template <typename K, typename... A>
-cudaError_t ring_launch(K kern, const LayerNormFwd& a, const RingShape& r, cudaStream_t stream, A... more) {
+cudaError_t ring_launch(K kern, const LayerNormFwd& a, const RingShape& r, bool holds, cudaStream_t stream, A... more) {
+    if (!holds) return cudaErrorInvalidValue;
     const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), static_cast<int>(kRingSmem), true);
     if (e != cudaSuccess) return e;
     return launch_chained(kern, dim3(static_cast<unsigned>(r.grid)), r.team * r.teams, static_cast<size_t>(r.smem), stream, a, r, more...);
@@ -543,9 +551,11 @@ cudaError_t fwd_aligned(const LayerNormFwd& a, cudaStream_t stream) {
         r.per = kPair;
         r.dense = 0;
         team_of(&r, nv, {2, 1});
-        if (fit_ring(&r, a.rows, (a.R ? 2 : 1) * ChunkRing::place(a.d * es, kPair, false), 0, a.num_sms))
-            return r.each == 2 ? ring_launch(layer_norm_fwd_ring_kernel<T, TY, 2>, a, r, stream, wvec, bvec)
-                               : ring_launch(layer_norm_fwd_ring_kernel<T, TY, 1>, a, r, stream, wvec, bvec);
+        if (fit_ring(&r, a.rows, slot_bytes<T>(a, r.per, false), 0, a.num_sms)) {
+            const bool holds = !r.dense && ring_holds(r, kPair, nv, slot_bytes<T>(a, kPair, false), 0, 0);
+            return r.each == 2 ? ring_launch(layer_norm_fwd_ring_kernel<T, TY, 2>, a, r, holds, stream, wvec, bvec)
+                               : ring_launch(layer_norm_fwd_ring_kernel<T, TY, 1>, a, r, holds, stream, wvec, bvec);
+        }
     }
     if (!whole && many && a.d <= 8192 && a.d > 16) {
         RingShape r;
@@ -559,25 +569,23 @@ cudaError_t fwd_aligned(const LayerNormFwd& a, cudaStream_t stream) {
             r.per = 2;
             team_of(&r, a.d, {16, 14, 12, 10, 8});
         }
-        auto fits = [&] {
-            const int64_t out = ChunkRing::place(a.d * ey, r.per, r.dense) + (a.H ? ChunkRing::place(a.d * es, r.per, r.dense) : 0);
-            return fit_ring(&r, a.rows, (a.R ? 2 : 1) * ChunkRing::place(a.d * es, r.per, r.dense), 2 * out, a.num_sms);
-        };
+        auto fits = [&] { return fit_ring(&r, a.rows, slot_bytes<T>(a, r.per, r.dense), out_bytes<T, TY>(a, r.per, r.dense), a.num_sms); };
         bool fit = fits();
         if (!fit && r.per == 2) {   // longer rows one by one
             r.per = 1;
             fit = fits();
         }
+        const bool holds = fit && ring_holds(r, r.per, a.d, slot_bytes<T>(a, r.per, r.dense), out_bytes<T, TY>(a, r.per, r.dense), 0);
         if (fit)
             switch (r.each) {
-                case 2: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 2>, a, r, stream);
-                case 4: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 4>, a, r, stream);
-                case 6: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 6>, a, r, stream);
-                case 8: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 8>, a, r, stream);
-                case 10: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 10>, a, r, stream);
-                case 14: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 14>, a, r, stream);
-                case 12: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 12>, a, r, stream);
-                default: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 16>, a, r, stream);
+                case 2: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 2>, a, r, holds, stream);
+                case 4: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 4>, a, r, holds, stream);
+                case 6: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 6>, a, r, holds, stream);
+                case 8: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 8>, a, r, holds, stream);
+                case 10: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 10>, a, r, holds, stream);
+                case 14: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 14>, a, r, holds, stream);
+                case 12: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 12>, a, r, holds, stream);
+                default: return ring_launch(layer_norm_fwd_odd_kernel<T, TY, 16>, a, r, holds, stream);
             }
     }
     if (a.d <= 768 && a.rows >= 8 * sms) {   // a warp per row, once there are eight for every SM

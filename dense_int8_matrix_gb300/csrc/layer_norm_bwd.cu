@@ -193,7 +193,6 @@ __device__ __forceinline__ void start_ring(ChunkRing& ring, const LayerNormBwd& 
 // values per thread and row, whose w, dw and db stay in registers.  Bound by a
 // row's two sums as much as by DRAM: 4096 x 8192 bfloat16 54 us, 5.0 TB/s (50 without
 // dw and db; 91 with one row in a CTA), 16384 x 2048 fp32 79 us, 6.0 TB/s.
-constexpr int kPair = 2;
 template <typename T, typename TY, int V>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_bwd_ring_kernel(const LayerNormBwd p, const RingShape shape, bool wvec) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -624,6 +623,15 @@ int col_lanes(int64_t d) {
     return lanes;
 }
 
+// Bytes of a slot and of a team's staging buffers (unaligned rows: two of them).
+int64_t slot_bytes(const LayerNormBwd& a, int per, bool dense) {
+    const int64_t es = a.x_type == GEMM_DTYPE_BF16 ? 2 : 4, ey = a.y_type == GEMM_DTYPE_BF16 ? 2 : 4;
+    return ChunkRing::place(a.d * ey, per, dense) + (a.dR ? 2 : 1) * ChunkRing::place(a.d * es, per, dense);
+}
+int64_t out_bytes(const LayerNormBwd& a, int per, bool dense) {
+    return 2 * ChunkRing::place(a.d * (a.x_type == GEMM_DTYPE_BF16 ? 2 : 4), per, dense);
+}
+
 Choice choose(const LayerNormBwd& a) {
     Choice c{};
     const bool vec = bwd_vec(a), whole = vec && a.d % 8 == 0;
@@ -653,17 +661,13 @@ Choice choose(const LayerNormBwd& a) {
             r.per = 2;
             team_of(&r, a.d, {16, 14, 12, 10, 8});
         }
-        auto fits = [&] {
-            const int64_t slot = ChunkRing::place(a.d * ey, r.per, r.dense) + (a.dR ? 2 : 1) * ChunkRing::place(a.d * es, r.per, r.dense);
-            return fit_ring(&r, a.rows, slot, whole ? 0 : 2 * ChunkRing::place(a.d * es, r.per, r.dense), a.num_sms);
-        };
+        auto fits = [&] { return fit_ring(&r, a.rows, slot_bytes(a, r.per, r.dense), whole ? 0 : out_bytes(a, r.per, r.dense), a.num_sms); };
         bool fit = fits();
         if (!fit && !whole && r.per == 2) {   // longer unaligned rows one by one (the aligned kernel takes kPair)
             r.per = 1;
             fit = fits();
         }
         if (fit) {
-            // (the teams' sums take its place: d floats each, fewer bytes than two slots)
             c.way = whole ? kByRing : kOdd;
             c.parts = c.grid = r.grid;
             return c;
@@ -690,8 +694,10 @@ cudaError_t by_warps(const LayerNormBwd& a, const Choice& c, cudaStream_t stream
            : a.d <= 256 ? go(layer_norm_bwd_warp_kernel<T, TY, 32, 1>) : go(layer_norm_bwd_warp_kernel<T, TY, 32, 2>);
 }
 
+// (the teams' sums, d floats each, take the slots' place)
 template <typename K, typename... A>
-cudaError_t ring_launch(K kern, const LayerNormBwd& a, const RingShape& r, cudaStream_t stream, A... more) {
+cudaError_t ring_launch(K kern, const LayerNormBwd& a, const RingShape& r, bool holds, cudaStream_t stream, A... more) {
+    if (!holds) return cudaErrorInvalidValue;
     const cudaError_t e = kernel_attrs_once(reinterpret_cast<const void*>(kern), static_cast<int>(kRingSmem), true);
     if (e != cudaSuccess) return e;
     return launch_chained(kern, dim3(static_cast<unsigned>(r.grid)), r.team * r.teams, static_cast<size_t>(r.smem), stream, a, r, more...);
@@ -699,20 +705,22 @@ cudaError_t ring_launch(K kern, const LayerNormBwd& a, const RingShape& r, cudaS
 template <typename T, typename TY>
 cudaError_t by_ring(const LayerNormBwd& a, const RingShape& r, cudaStream_t stream) {
     const bool wvec = reinterpret_cast<uintptr_t>(a.W) % 16 == 0;
-    return r.each == 1 ? ring_launch(layer_norm_bwd_ring_kernel<T, TY, 1>, a, r, stream, wvec)
-                       : ring_launch(layer_norm_bwd_ring_kernel<T, TY, 2>, a, r, stream, wvec);
+    const bool holds = !r.dense && ring_holds(r, kPair, a.d / 8, slot_bytes(a, kPair, false), 0, 4 * a.d);
+    return r.each == 1 ? ring_launch(layer_norm_bwd_ring_kernel<T, TY, 1>, a, r, holds, stream, wvec)
+                       : ring_launch(layer_norm_bwd_ring_kernel<T, TY, 2>, a, r, holds, stream, wvec);
 }
 template <typename T, typename TY>
 cudaError_t by_odd(const LayerNormBwd& a, const RingShape& r, cudaStream_t stream) {
+    const bool holds = ring_holds(r, r.per, a.d, slot_bytes(a, r.per, r.dense), out_bytes(a, r.per, r.dense), 4 * a.d);
     switch (r.each) {
-        case 2: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 2>, a, r, stream);
-        case 4: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 4>, a, r, stream);
-        case 6: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 6>, a, r, stream);
-        case 8: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 8>, a, r, stream);
-        case 10: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 10>, a, r, stream);
-        case 14: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 14>, a, r, stream);
-        case 12: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 12>, a, r, stream);
-        default: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 16>, a, r, stream);
+        case 2: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 2>, a, r, holds, stream);
+        case 4: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 4>, a, r, holds, stream);
+        case 6: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 6>, a, r, holds, stream);
+        case 8: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 8>, a, r, holds, stream);
+        case 10: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 10>, a, r, holds, stream);
+        case 14: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 14>, a, r, holds, stream);
+        case 12: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 12>, a, r, holds, stream);
+        default: return ring_launch(layer_norm_bwd_odd_kernel<T, TY, 16>, a, r, holds, stream);
     }
 }
 

@@ -250,6 +250,7 @@ struct RingShape {
     int grid;
 };
 constexpr int kRingThreads = 512;   // of 128 registers
+constexpr int kPair = 2;            // rows of a chunk of the kernels of aligned rows
 // Rows that an unaligned kernel of J values per thread works on together
 // (measured, 159783 x 105 bfloat16 forward: 71 us with two, 85 with four, 109
 // with eight).
@@ -296,6 +297,16 @@ inline bool fit_ring(RingShape* r, int64_t rows, int64_t slot, int64_t out, int 
     const int64_t grid = (chunks + teams - 1) / teams;
     r->grid = static_cast<int>(grid < num_sms ? grid : num_sms);
     return true;
+}
+// What a kernel counts on, asked before every launch: chunks of `per` rows, a
+// thread for each of a row's `units`, and room for its slots (of `slot` bytes as the
+// kernel lays them out), its staging buffers (`out`) and, at the end, a team's `sums`.
+// (A ring sized for chunks of one row, under a kernel that takes two, overruns
+// shared memory.)
+inline bool ring_holds(const RingShape& r, int per, int64_t units, int64_t slot, int64_t out, int64_t sums) {
+    return r.per == per && r.team % 32 == 0 && static_cast<int64_t>(r.each) * r.team >= units && r.teams >= 1 &&
+           r.team * r.teams <= kRingThreads && (r.team == 32 || r.teams <= kMostTeams) && r.slots >= 2 && r.slots <= ChunkRing::kSlots &&
+           r.teams * (r.slots * slot + out) <= r.smem && r.teams * sums <= r.smem && r.smem <= kRingSmem && r.grid >= 1;
 }
 
 }  // namespace gemm
