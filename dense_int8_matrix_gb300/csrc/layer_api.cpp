@@ -45,12 +45,12 @@ gemm_status check_linear_shape(int32_t form, int64_t m, int64_t k, int64_t n) {
 // 128 columns, `steps` K steps of 64, `split` CTAs to a tile; on the two-SM tiles
 // in the function below.  The constants were fitted to the times of every
 // configuration on 220 drawn products of all forms on GB300 (152 SMs): a step, what a round of
-// CTAs costs besides, the epilogue (twice as long for rows of D that are no whole
-// vectors: `odd`), and the join of a split.  Two CTAs share an SM below 64 rows and
+// CTAs costs besides, the epilogue (on small tiles 1.3 times as long for rows of D
+// that are no whole vectors: `odd`; the two-SM tiles' takes no longer), and the join of a split.  Two CTAs share an SM below 64 rows and
 // then take 2.5 times as long; clusters of four and eight cannot use every SM.
 double small_time(double tiles, int64_t steps, int bm, int split, bool odd, int num_sms) {
     const double step = bm == 16 ? 0.24 : bm == 32 ? 0.26 : bm == 64 ? 0.25 : 0.36;
-    const double epilogue = bm == 16 ? 0.13 : bm == 32 ? 0.47 : (bm == 64 ? 1.0 : 1.5) * (odd ? 2 : 1);
+    const double epilogue = bm == 16 ? 0.13 : bm == 32 ? 0.47 : (bm == 64 ? 1.0 : 1.5) * (odd ? 1.3 : 1.0);
     const double part = bm < 64 ? (split == 8 ? 1.68 : split == 4 ? 1.86 : 2.0) : split == 8 ? 0.79 : split == 4 ? 0.84 : 1.0;
     const double ctas = tiles * split, room = std::max(1.0, std::floor(part * num_sms));
     const double share = bm < 64 && ctas > num_sms ? 2.5 : 1.0;
@@ -59,8 +59,8 @@ double small_time(double tiles, int64_t steps, int bm, int split, bool odd, int 
 }
 // A tile's epilogue runs beside the next tile's products; a last round that
 // fills at most half of the pairs runs as halves.
-double pair_time(double tiles, int64_t steps, bool odd, int num_sms) {
-    const double pairs = std::max(1, num_sms / 2), epilogue = 4.3 * (odd ? 2 : 1), k = static_cast<double>(steps);
+double pair_time(double tiles, int64_t steps, int num_sms) {
+    const double pairs = std::max(1, num_sms / 2), epilogue = 4.3, k = static_cast<double>(steps);
     const double whole = 0.6 + 0.46 * k, half = 0.56 + 0.38 * k;
     const double rounds = std::floor(tiles / pairs), left = tiles - rounds * pairs;
     double t = 2.9 + (rounds > 0 ? whole + (rounds - 1) * std::max(whole, epilogue) : 0.0);
@@ -70,16 +70,17 @@ double pair_time(double tiles, int64_t steps, bool odd, int num_sms) {
     return t + (2 * left > pairs ? epilogue : epilogue / 2);
 }
 
-// The tile and split of a product: the least estimate.  On those products the
-// choice took 0.7 % longer than the best configuration of each, the two-SM tile
-// for all of them 66 %.
+// The tile and split of a product: the least estimate.  On 870 other products, with
+// the kernels as they are, the choice takes 1.4 % longer than the best
+// configuration of each (the worst by 33 %).  It sees the form and the sizes, not
+// the activation.
 void choose_linear(gemm_plan_linear* p) {
     const int64_t steps = ceil_div(p->k, 64);
     const bool odd = p->n % 8 != 0;
     p->path = GEMM_PATH_TENSOR;
     p->bm = p->bn = 256;
     p->split_k = 1;
-    double best = pair_time(static_cast<double>(ceil_div(p->m, 256)) * static_cast<double>(ceil_div(p->n, 256)), steps, odd, p->num_sms);
+    double best = pair_time(static_cast<double>(ceil_div(p->m, 256)) * static_cast<double>(ceil_div(p->n, 256)), steps, p->num_sms);
     for (int bm = p->form == GEMM_FORM_TN ? 64 : 16; bm <= 128; bm *= 2) {
         if ((bm < 128 && p->m > 8 * bm) || (bm > 16 && bm >= 4 * p->m)) continue;
         const double tiles = static_cast<double>(ceil_div(p->m, bm)) * static_cast<double>(ceil_div(p->n, 128));
