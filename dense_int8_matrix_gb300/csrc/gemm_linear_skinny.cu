@@ -5,7 +5,7 @@
 // the weights) by NT rows (its N side, from A; NT in {16, 32, 64, 128}).  Per K
 // step of 64 a 16 KiB box of B and NT * 128 bytes of A go through a
 // shared-memory ring, and four MMAs (K = 16) add them up in TMEM; chunks of K
-// join fp32 sums in registers (see chunk_of in gemm_linear_tc2.cu).
+// join fp32 sums in registers (see set_chunks in gemm_linear_tc2.cu).
 //
 // With few tiles a cluster of split_k CTAs shares a tile along K.  Each sends
 // its sums to the CTAs that finish them (one share of the rows each) through

@@ -8,7 +8,7 @@
 // TMA, and tcgen05.mma (M = 256, N = 256, K = 16, four per step) adds them up in
 // TMEM, in 32 bits.  The MMA truncates what it adds to an accumulator, an error
 // that grows with K and always points to zero, so that a chunk of K at a time
-// is added up there and the chunks in registers, rounded to nearest (chunk_of).  The two
+// is added up there and the chunks in registers, rounded to nearest (set_chunks).  The two
 // accumulators of 256 columns alternate: one is read while the next chunk, or
 // the next tile, is multiplied.
 //
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kb = 0; kb < steps; ++kb) {
                     const bool fresh = left == 0;
                     if (fresh) {
-                        left = min(p.chunk, steps - kb);
+                        left = min(kb == 0 ? p.first : p.chunk, steps - kb);
                         ok = wait_warp(acce0 + 8u * buf.i, buf.ph ^ 1u, abort_flag, p.err, kDevErrTimeoutMma);
                     }
                     ok = ok && wait_warp(full0 + 8u * st.i, st.ph, abort_flag, p.err, kDevErrTimeoutMma);
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t acc[kTileN / 4];   // pairs of columns; the first half of them for a half
 #pragma unroll
             for (int j = 0; j < kTileN / 4; ++j) acc[j] = 0;
-            for (int kb = 0; kb < steps; kb += p.chunk) {
+            for (int kb = 0; kb < steps; kb += kb == 0 ? p.first : p.chunk) {
                 ok = wait_warp(accf0 + 8u * buf.i, buf.ph, abort_flag, p.err, kDevErrTimeoutEpilogue);
                 if (!ok) break;
                 tc_fence_after();
@@ -341,13 +341,18 @@ bool encode_operand(CUtensorMap* map, const LinearLaunch& a, bool is_b, int box_
 // K steps that are added up in TMEM.  Relative error of sums of products of normal
 // values, fp32 output, against 64 bits: 4096 products in one chunk 4.4e-6 (a
 // plain fp32 matrix product 6e-7), 131072 1.5e-4, and 8e-4 if all are positive;
-// chunks of 512 keep it near 6e-7.  Small tiles take chunks of 512 whatever the
-// output (at most 2 % longer).  The two-SM tiles take 2048 for bfloat16 outputs, whose
-// rounding is 2e-3: reading an accumulator costs the MMAs a quarter of a
-// microsecond (8192^3 571 us with 2048, 575 with 1024, 612 with 512; 4096^3 with GELU and
-// residual 90, 100, 110), and what it saves, 5e-6 of a sum of positive products
-// against 1e-6, changes one in a thousand of the outputs by their last bit.
-int chunk_of(const LinearLaunch& a) { return (a.out_f32 || a.bm < 256 ? 512 : 2048) / kLinBK; }
+// chunks of 512 keep it near 6e-7, and small tiles take them whatever the output
+// (at most 2 % longer).  The two-SM tiles take 1024 for bfloat16 outputs, whose
+// rounding is 2e-3: 8192^3 601 us with Z and GELU_TANH as with 2048, 639 with 512, as
+// reading an accumulator holds the MMAs up.  A tile's first chunk is 1536: the
+// one before it is finished in the time of its first two (4096^3 with GELU and
+// residual 91 us, 95 with 1024).  Positive sums are short by 3e-6 at most, one
+// output in 1300 differs from the rounded exact sum (chunks of 2048: 5.7e-6, one in 800).
+void set_chunks(const LinearLaunch& a, LinearParams* p) {
+    const bool fine = a.out_f32 || a.bm < 256;
+    p->chunk = (fine ? 512 : 1024) / kLinBK;
+    p->first = (fine ? 512 : 1536) / kLinBK;
+}
 
 LinearParams linear_params(const LinearLaunch& a, int bm, int bn) {
     LinearParams p;
@@ -373,7 +378,7 @@ LinearParams linear_params(const LinearLaunch& a, int bm, int bn) {
     p.pairs = aligned_to(a.D, 4) && a.ldd % 2 == 0 && (!a.R || (aligned_to(a.R, 4) && a.ldr % 2 == 0)) &&
               (!a.Z || (aligned_to(a.Z, 4) && a.ldz % 2 == 0));
     p.halves = false;
-    p.chunk = chunk_of(a);
+    set_chunks(a, &p);
     return p;
 }
 

@@ -23,6 +23,7 @@ struct LinearParams {
     int m, n;
     int num_kb;                // K steps
     int chunk;                 // K steps added up in TMEM, before they join sums in registers
+    int first;                 // the same of a two-SM tile's first chunk
     int tiles_m, tiles_n;
     bool out_f32;
     bool mn_a, mn_b;           // A, B stored with their rows (columns of D) contiguous instead of K
