@@ -4,7 +4,7 @@
 //   dz = dy * act'(z),  dbias[j] = sum_i dy[i][j] * act'(z[i][j])
 //
 // Bound by DRAM: every element is read and written once (4096 x 16384, GELU_TANH:
-// 81 us, 5.0 TB/s; RELU 72 us, 5.6 TB/s; more rows in flight per thread spill or
+// 81 us, 4.9 TB/s; RELU 73 us, 5.5 TB/s; more rows in flight per thread spill or
 // cost CTAs).  A thread takes eight columns of a range of rows and keeps their
 // sums; the sums of a CTA are joined in shared memory, those of the row ranges
 // of a cluster through distributed shared memory, and those of clusters by
@@ -37,7 +37,8 @@ constexpr int kPerSm = 4;        // CTAs (of 64 registers per thread)
 // (measured, 55369 x 453, GELU_TANH: 45 us shifted, 128 as singles).
 enum { kVectors, kShifted, kSingles };
 
-// Rows in flight per thread: as many as the registers of kPerSm CTAs hold.
+// Rows in flight per thread: about as many as the registers of kPerSm CTAs hold
+// (four rows of RELU spill 32 to 100 bytes; the others do not).
 template <int ACT, int MODE>
 constexpr int kRows = MODE == kSingles ? 8 : ACT <= GEMM_ACT_RELU ? 4 : 2;
 
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) act_bwd_kernel(const ActBwd 
 // of the matrix and of a row they are read one by one.  What lies between the
 // columns and the pitch is not used.  A warp takes kCopies * 32 vectors of a
 // row, or of neighbouring ones where rows are short.  Measured, 224 x 6401 and
-// 1692 x 6401: the product takes 8 us longer than on aligned rows (14 with
+// 1692 x 6401 (26 us): the product takes 8 us longer than on aligned rows (14 with
 // elements read one by one).
 constexpr int kCopies = 2;
 // Eight elements from `past` (0 .. 7) on of two aligned vectors.

@@ -12,7 +12,8 @@
 // rows at once, whatever the number of experts, and a lane has the same columns
 // of every row: its sums of p stay with it.  (Four columns per lane leave the
 // same work per row to be done for fewer rows at once.)  The next row is on its
-// way while one is worked on.  Sums are joined in a fixed order: rows of a lane, row
+// way while one is worked on (with nine to sixteen experts, a row to a lane, 216 to 316
+// bytes of its registers spill; otherwise eight at most).  Sums are joined in a fixed order: rows of a lane, row
 // groups of a warp, warps of a CTA, the eight CTAs of a cluster (through
 // distributed shared memory), and clusters by a second kernel.  Batches that
 // one cluster (or one CTA) takes in a few turns need no second kernel.

@@ -13,12 +13,12 @@
 // no second launch, and the same bits every time.  Then bias, activation and
 // residual are applied once, to the joined sums.
 //
-// Bound by DRAM for few rows: 1 x 8192 x 8192 25.3 us, 5.3 TB/s, 64 rows 27.2; without
+// Bound by DRAM for few rows: 1 x 8192 x 8192 25.4 us, 5.3 TB/s, 64 rows 28; without
 // the split 223 us.  Otherwise by a fixed part of 4 to 8 us around few K steps
 // (1024^3 8.6 us).
 //
 // Operands that lie across K (GEMM_FORM_NN, GEMM_FORM_TN) are multiplied
-// MN-major, as in gemm_linear_tc2.cu.
+// MN-major, as in gemm_linear_tc2.cu.  (Tiles of 32 rows spill 56 bytes, of 128 rows 8.)
 #include <cuda_runtime.h>
 
 #include <cstring>

@@ -17,10 +17,11 @@
 // other dimension: their boxes are 64 rows by 64 K elements, and the MMA takes
 // them MN-major, so that nothing is ever transposed in memory.
 //
-// Bound by the tensor cores where K is long: 4096^3 79 us (1.73 PFLOP/s; 256 tiles on
-// 76 pairs are 3.5 rounds), 8192^3 579 us (1.90 PFLOP/s, power limited), fp32 output
-// of 4096^3 88 us.  By the epilogue where K is short: about 4.3 us for a tile beside
-// the next one's products, 9 with GELU (8192 x 1024 x 8192 81 us, 122 with GELU).
+// Bound by the tensor cores where K is long: 4096^3 81 us (1.70 PFLOP/s; 256 tiles on
+// 76 pairs are 3.5 rounds), 8192^3 563 to 575 us (1.93 PFLOP/s, power limited), fp32
+// output of 4096^3 87 us.  By the epilogue where K is short: about 4.3 us for a tile
+// beside the next one's products, 9 with GELU (8192 x 1024 x 8192 80 us, 114 with GELU).
+// GELU and its gradient spill 16 and 28 bytes.
 //
 // Roles: warp 0 loads operands, warp 1 of the even CTA issues the MMAs, warps 4
 // to 11 take the sums through shared memory (so that rows leave in contiguous
@@ -346,7 +347,7 @@ bool encode_operand(CUtensorMap* map, const LinearLaunch& a, bool is_b, int box_
 // rounding is 2e-3: 8192^3 601 us with Z and GELU_TANH as with 2048, 639 with 512, as
 // reading an accumulator holds the MMAs up.  A tile's first chunk is 1536: the
 // one before it is finished in the time of its first two (4096^3 with GELU and
-// residual 91 us, 95 with 1024).  Positive sums are short by 3e-6 at most, one
+// residual 91 us, 95 with 1024).  Positive sums are short by 2.4e-6, one
 // output in 1300 differs from the rounded exact sum (chunks of 2048: 5.7e-6, one in 800).
 void set_chunks(const LinearLaunch& a, LinearParams* p) {
     const bool fine = a.out_f32 || a.bm < 256;

@@ -72,7 +72,8 @@ __device__ __forceinline__ Vec8<T> row_dx(const Vec8<TY>& dy, const Vec8<T>& h, 
 
 // Short aligned rows: L lanes hold a row (V vectors of eight values each), 32 / L
 // rows per warp; the next rows are on their way while these are worked on.
-// 524288 x 64 and 262144 x 128 bfloat16 59 us, 4.5 TB/s.
+// 524288 x 64 and 262144 x 128 bfloat16 58 us, 4.6 TB/s.  (L = 32, V = 2, rows of 257 to
+// 512 elements that are too few for the ring: 128 to 532 bytes spill.)
 constexpr int kWarpThreads = 256;
 template <typename T, typename TY, int L, int V>
 __global__ void __launch_bounds__(kWarpThreads, 2) layer_norm_bwd_warp_kernel(const LayerNormBwd p, bool wvec) {
@@ -192,7 +193,7 @@ __device__ __forceinline__ void start_ring(ChunkRing& ring, const LayerNormBwd& 
 // Longer aligned rows: two rows per team from its ring, V vectors of eight
 // values per thread and row, whose w, dw and db stay in registers.  Bound by a
 // row's two sums as much as by DRAM: 4096 x 8192 bfloat16 54 us, 5.0 TB/s (50 without
-// dw and db; 91 with one row in a CTA), 16384 x 2048 fp32 79 us, 6.0 TB/s.
+// dw and db; 91 with one row in a CTA), 16384 x 2048 fp32 78 us, 6.0 TB/s.
 template <typename T, typename TY, int V>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_bwd_ring_kernel(const LayerNormBwd p, const RingShape shape, bool wvec) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -331,7 +332,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_bwd_ring_kernel(co
 // between each value is taken by itself, neighbouring lanes neighbouring values,
 // J values per thread and row.  Dense short rows: a warp per team, which takes
 // several rows at a time.  Bound by the instructions that each value takes: 33520 x
-// 1001 bfloat16 93 us, 2.9 TB/s, 4096 x 8191 93 us, 516222 x 65 143 us, 1.9 TB/s.
+// 1001 bfloat16 91 us, 2.9 TB/s, 4096 x 8191 91 us, 516222 x 65 143 us, 1.9 TB/s.  (J = 12 and
+// 16 spill 12 to 16 bytes.)
 template <typename T, typename TY, int J>
 __global__ void __launch_bounds__(kRingThreads, 1) layer_norm_bwd_odd_kernel(const LayerNormBwd p, const RingShape shape) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -488,8 +490,10 @@ __global__ void __launch_bounds__(256) layer_norm_join_kernel(const LayerNormBwd
 }
 
 // dx: one CTA per row, the row in registers.  With the pass below: 300 x 4096
-// bfloat16 11 us (latency), 2048 x 16384 106 us and 4096 x 8192 fp32 127 us, 2.5 and
-// 3.7 TB/s of what one pass would move.
+// bfloat16 11 us (latency), 2048 x 16384 103 us and 4096 x 8192 fp32 126 us, 2.6 and
+// 3.7 TB/s of what one pass would move.  (V = 4, rows beyond 16384 elements: a CTA's 1024
+// threads have 64 registers each, and 136 to 544 bytes spill; V = 2 of unaligned
+// fp32 rows 12 to 16.)
 template <typename T, typename TY, int V, bool VEC>
 __global__ void __launch_bounds__(1024, 1) layer_norm_dx_kernel(const LayerNormBwd p, bool wvec) {
     __shared__ float red[2][32];

@@ -559,7 +559,8 @@ GEMM_API gemm_status gemm_activation_backward(const uint16_t *dY, int64_t lddy, 
  * elements; d <= GEMM_NORM_MAX_D; eps >= 0.  The mean is corrected by the mean
  * of h - mean, so that its error goes by the row's spread, not by its size, and
  * a constant row gives Y = bias exactly (NaN with eps = 0; magnitudes to 1e22).
- * A row that holds an infinity or a NaN gives NaN.
+ * A row that holds an infinity or a NaN gives NaN, and so does one whose sum
+ * leaves fp32's range; one whose squares do has rstd = 0.
  * Errors: as gemm_norm_f8; GEMM_ERR_INVALID_ARG also for any other output that
  * is an operand or another output.
  */
@@ -591,7 +592,11 @@ GEMM_API gemm_status gemm_layer_norm_backward(const void *dY, int64_t lddy, cons
  * experts (GEMM_DTYPE_BF16 or GEMM_DTYPE_F32, pitch ldx); index: the experts
  * chosen for each row, rows x top_k int32 without gaps.  An index outside
  * [0, experts) is a slot that is not taken (a token that a full expert has
- * turned away); a row without a taken slot is padding and takes no part.
+ * turned away); a row without a taken slot is padding and takes no part.  So a
+ * token that every expert it chose has turned away leaves the loss and the
+ * gradient: where such tokens are to count, pass the router's choices as they
+ * were before any was turned away, and take the offsets of the rows that stay
+ * from a call with those that remain.
  *   counts[e]  = number of slots with index e
  *   offsets[e] = counts[0] + .. + counts[e-1], experts + 1 values: the row
  *                offsets that gemm_f8_grouped_run takes (may be NULL)
